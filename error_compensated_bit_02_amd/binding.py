@@ -18,6 +18,9 @@ LIB_PATH = os.path.join(_PKG, "libob.so")
 
 OB_OK, OB_ERR_INVALID, OB_ERR_ALIGN, OB_ERR_NOMEM, OB_ERR_DEVICE, OB_ERR_SCRATCH = 0, 1, 2, 3, 4, 5
 OB_GRAD_F32, OB_GRAD_BF16 = 0, 1
+OB_ID_I32, OB_ID_I64 = 0, 1
+ACT_FORMATS = {"e4m3": 0, "int8": 1}
+ACT_FNS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
 
 _c_void_p = ctypes.c_void_p
 _i32, _i64, _f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_double
@@ -44,6 +47,20 @@ SIGNATURES = {
     "ob_cltk_configure": (ctypes.c_int, [_c_void_p, _f64, ctypes.POINTER(_i64)]),
     "ob_cltk_layout": (ctypes.c_int, [_c_void_p, ctypes.POINTER(_i64)]),
     "ob_cltk_step": (ctypes.c_int, [_c_void_p, _i64] + [_c_void_p] * 5 + [_c_void_p]),
+    "ob_act_layout": (ctypes.c_int, [_i64, _i64] + [ctypes.POINTER(_i64)] * 3),
+    "ob_act_save": (ctypes.c_int, [_i32, _i32, _i64, _i64, _i32, _c_void_p, _i64, _c_void_p, _i64]
+                    + [_c_void_p] * 3),
+    "ob_act_load": (ctypes.c_int, [_i32, _i64, _i64, _c_void_p, _c_void_p, _i32, _c_void_p, _i64, _c_void_p]),
+    "ob_act_backward": (ctypes.c_int, [_i32, _i32, _i64, _i64, _c_void_p, _c_void_p, _i32, _c_void_p, _i64,
+                                       _c_void_p, _i64, _c_void_p]),
+    "ob_linear_grad_work": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_i64)]),
+    "ob_linear_grad": (ctypes.c_int, [_c_void_p, _i32, _i32, _i32, _i64, _i64, _i64, _i32, _c_void_p, _c_void_p,
+                                      _i32, _c_void_p, _i64, _i32, _c_void_p, _c_void_p, _i64, _c_void_p]),
+    "ob_embedding_lookup": (ctypes.c_int, [_c_void_p, _i32, _i64, _i64, _c_void_p, _i32, _c_void_p, _f64, _i32,
+                                           _c_void_p, _i64, _c_void_p]),
+    "ob_embedding_grad_work": (ctypes.c_int, [_i64, _i64, ctypes.POINTER(_i64)]),
+    "ob_embedding_grad": (ctypes.c_int, [_c_void_p, _i32, _i32, _i64, _i64, _c_void_p, _i32, _f64, _i32, _c_void_p,
+                                         _i64, _i32, _c_void_p, _c_void_p, _i64, _c_void_p]),
     "ob_profile_enable": (ctypes.c_int, [_c_void_p, _i32]),
     "ob_profile_kinds": (_i32, []),
     "ob_profile_kind_name": (ctypes.c_char_p, [_i32]),
@@ -110,6 +127,149 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+_DTYPES = {torch.float32: OB_GRAD_F32, torch.bfloat16: OB_GRAD_BF16}
+
+
+def _device(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise OneBitError(f"{name} must be a device tensor")
+    return t.device
+
+
+def _matrix(t: torch.Tensor, rows: int, cols: int, device, name: str):
+    """(pointer, dtype code, row stride) of a [rows][cols] matrix with adjacent columns."""
+    if _device(t, name) != device:
+        raise OneBitError(f"{name} is on {t.device}, expected {device}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise OneBitError(f"{name} has dtype {t.dtype}, expected one of {tuple(_DTYPES)}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise OneBitError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    if cols > 1 and t.stride(1) != 1:
+        raise OneBitError(f"{name}'s columns must be adjacent (stride {t.stride(1)})")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise OneBitError(f"{name}'s rows overlap (row stride {ld}, {cols} columns)")
+    return t.data_ptr(), code, ld
+
+
+def _stream_on(stream, device: torch.device) -> int:
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if s.device != device:
+        raise OneBitError(f"the stream is on {s.device}, the tensors on {device}")
+    return s.cuda_stream
+
+
+class _on:
+    """Makes `device` current for one call (a launch goes to the current device)."""
+
+    def __init__(self, device: torch.device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _work(work, need: int, stream, device: torch.device):
+    """The caller's scratch, or `need` bytes of torch's, taken on the call's stream."""
+    if work is not None:
+        if _device(work, "work") != device:
+            raise OneBitError(f"work is on {work.device}, expected {device}")
+        if not work.is_contiguous():
+            raise OneBitError("work must be contiguous")
+        have = work.numel() * work.element_size()
+        if have < need:
+            raise OneBitError(f"work has {have} bytes, {need} are needed", OB_ERR_INVALID)
+        return work, have
+    if need == 0:
+        return None, 0
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+
+
+def act_layout(rows: int, cols: int):
+    """(pitch, bytes of codes, bytes of scales) of a rows x cols checkpoint (host only)."""
+    out = [_i64() for _ in range(3)]
+    _check(load_library().ob_act_layout(int(rows), int(cols), *(ctypes.byref(o) for o in out)), "ob_act_layout")
+    return tuple(o.value for o in out)
+
+
+class ActCheckpoint:
+    """An 8-bit checkpoint of an activation [rows][cols] (format in include/ob.h):
+    codes uint8 [rows][pitch] and scales uint8 [ceil(rows/32)][pitch], allocated
+    here on `device` or the caller's own contiguous tensors.
+    """
+
+    def __init__(self, rows: int, cols: int, fmt: str = "e4m3", device=None, codes=None, scales=None):
+        if fmt not in ACT_FORMATS:
+            raise OneBitError(f"unknown format {fmt!r}, expected one of {tuple(ACT_FORMATS)}")
+        self.lib = load_library()
+        self.rows, self.cols, self.fmt = int(rows), int(cols), fmt
+        self.pitch, code_bytes, scale_bytes = act_layout(self.rows, self.cols)
+        if (codes is None) != (scales is None):
+            raise OneBitError("codes and scales are given together or not at all")
+        if codes is None:
+            device = torch.device("cuda" if device is None else device)
+            codes = torch.empty(self.rows, self.pitch, dtype=torch.uint8, device=device)
+            scales = torch.empty(scale_bytes // self.pitch, self.pitch, dtype=torch.uint8, device=device)
+        u8 = (torch.uint8,)
+        self._codes, self._scales = _ptr(codes, u8, code_bytes, "codes"), _ptr(scales, u8, scale_bytes, "scales")
+        if codes.device != scales.device:
+            raise OneBitError(f"codes are on {codes.device}, scales on {scales.device}")
+        self.codes, self.scales, self.device = codes, scales, codes.device
+        self._format = ACT_FORMATS[fmt]
+
+    @staticmethod
+    def _fn(act: str) -> int:
+        if act not in ACT_FNS:
+            raise OneBitError(f"unknown activation {act!r}, expected one of {tuple(ACT_FNS)}")
+        return ACT_FNS[act]
+
+    def save(self, x, act: str = "none", y=None, stream=None) -> None:
+        """Keep x; with an activation also y = act(x) in the same pass (y may be x)."""
+        fn = self._fn(act)
+        xp, dtype, ldx = _matrix(x, self.rows, self.cols, self.device, "x")
+        yp, ldy = None, self.cols
+        if (y is None) != (fn == 0):
+            raise OneBitError("y is given with an activation, and only then")
+        if y is not None:
+            yp, ydtype, ldy = _matrix(y, self.rows, self.cols, self.device, "y")
+            if ydtype != dtype:
+                raise OneBitError(f"y has dtype {y.dtype}, x {x.dtype}")
+        with _on(self.device):
+            st = self.lib.ob_act_save(self._format, fn, self.rows, self.cols, dtype, xp, ldx, yp, ldy,
+                                      self._codes, self._scales, _stream_on(stream, self.device))
+        _check(st, "ob_act_save")
+
+    def load(self, out, stream=None) -> None:
+        """Write the kept values (exact in float32 and in bfloat16)."""
+        op, dtype, ldo = _matrix(out, self.rows, self.cols, self.device, "out")
+        with _on(self.device):
+            st = self.lib.ob_act_load(self._format, self.rows, self.cols, self._codes, self._scales, dtype, op, ldo,
+                                      _stream_on(stream, self.device))
+        _check(st, "ob_act_load")
+
+    def act_backward(self, act: str, dy, dx, stream=None) -> None:
+        """dx = dy * act'(kept values); dx may be dy."""
+        fn = self._fn(act)
+        gp, dtype, lddy = _matrix(dy, self.rows, self.cols, self.device, "dy")
+        xp, xdtype, lddx = _matrix(dx, self.rows, self.cols, self.device, "dx")
+        if xdtype != dtype:
+            raise OneBitError(f"dx has dtype {dx.dtype}, dy {dy.dtype}")
+        with _on(self.device):
+            st = self.lib.ob_act_backward(self._format, fn, self.rows, self.cols, self._codes, self._scales, dtype,
+                                          gp, lddy, xp, lddx, _stream_on(stream, self.device))
+        _check(st, "ob_act_backward")
+
+
 class OneBitAdam:
     """Context for one tensor list: owns an ob_ctx (device scratch) and checks
     buffer shapes before calling into the library.
@@ -140,6 +300,7 @@ class OneBitAdam:
         _check(self.lib.ob_init(ctypes.byref(ctx), self.T, arr, self.W, code, self.beta1, self.eps),
                "ob_init")
         self._ctx = ctx
+        self.device = torch.device("cuda", torch.cuda.current_device())   # where the context's tables live
         self.S = self.lib.ob_server_scale_count(self._ctx)
 
     def set_trust_ratio(self, enable: bool, weight_decay: float = 0.0) -> None:
@@ -281,6 +442,83 @@ class OneBitAdam:
             self._ctx, _ptr(err_w, f32, self.W * self.N, "err_w"), _ptr(err_s, f32, self.N, "err_s"),
             _stream(stream))
         _check(st, "ob_begin_compression")
+
+    # -- what fills a gradient row -------------------------------------------
+    def _on_device(self, t: torch.Tensor, name: str) -> None:
+        if _device(t, name) != self.device:
+            raise OneBitError(f"{name} is on {t.device}, the context on {self.device}")
+
+    def _ids(self, ids: torch.Tensor):
+        self._on_device(ids, "ids")
+        if ids.dtype not in (torch.int32, torch.int64):
+            raise OneBitError(f"ids has dtype {ids.dtype}, expected int32 or int64")
+        if ids.dim() != 1 or not ids.is_contiguous():
+            raise OneBitError("ids must be contiguous and have one dimension")
+        return ids.data_ptr(), OB_ID_I64 if ids.dtype == torch.int64 else OB_ID_I32, ids.numel()
+
+    def _tensor(self, t, name: str) -> int:
+        if not 0 <= int(t) < self.T:
+            raise OneBitError(f"{name} {t} is not one of the list's {self.T} tensors", OB_ERR_INVALID)
+        return int(t)
+
+    def embedding_lookup(self, tensor, dim, ids, params, out, scale=1.0, stream=None) -> None:
+        """out[t] = scale * E[ids[t]], E = tensor `tensor` of params as [numel/dim][dim]."""
+        ip, idt, n = self._ids(ids)
+        self._on_device(params, "params")
+        op, odt, ldo = _matrix(out, n, int(dim), self.device, "out")
+        with _on(self.device):
+            st = self.lib.ob_embedding_lookup(
+                self._ctx, self._tensor(tensor, "tensor"), int(dim), n, ip, idt,
+                _ptr(params, (torch.float32,), self.N, "params"), float(scale), odt, op, ldo,
+                _stream_on(stream, self.device))
+        _check(st, "ob_embedding_lookup")
+
+    def embedding_grad(self, worker, tensor, dim, ids, dy, grads, scale=1.0, accumulate=False, work=None,
+                       stream=None) -> None:
+        """The lookup's gradient into row `worker` of grads.  work: scratch of
+        embedding_grad_work bytes; taken from torch when not given."""
+        ip, idt, n = self._ids(ids)
+        gp, gdt, lddy = _matrix(dy, n, int(dim), self.device, "dy")
+        self._on_device(grads, "grads")
+        work, have = _work(work, self.embedding_grad_work(n, dim), stream, self.device)
+        with _on(self.device):
+            st = self.lib.ob_embedding_grad(
+                self._ctx, int(worker), self._tensor(tensor, "tensor"), int(dim), n, ip, idt, float(scale), gdt, gp,
+                lddy, 1 if accumulate else 0, self._grad_ptr(grads), None if work is None else work.data_ptr(), have,
+                _stream_on(stream, self.device))
+        _check(st, "ob_embedding_grad")
+
+    def embedding_grad_work(self, tokens, dim) -> int:
+        """Bytes of scratch that embedding_grad needs."""
+        need = _i64()
+        _check(self.lib.ob_embedding_grad_work(int(tokens), int(dim), ctypes.byref(need)), "ob_embedding_grad_work")
+        return need.value
+
+    def linear_grad(self, worker, weight, bias, checkpoint, dy, grads, accumulate=False, work=None,
+                    stream=None) -> None:
+        """Weight (tensor `weight`) and bias (tensor `bias`, or None) gradient of a
+        linear layer from its input's checkpoint, into row `worker` of grads."""
+        rows, cols = checkpoint.rows, checkpoint.cols
+        weight = self._tensor(weight, "weight")
+        bias = -1 if bias is None else self._tensor(bias, "bias")
+        out = self.numel[weight] // cols
+        self._on_device(checkpoint.codes, "checkpoint")
+        gp, gdt, lddy = _matrix(dy, rows, out, self.device, "dy")
+        self._on_device(grads, "grads")
+        work, have = _work(work, self.linear_grad_work(rows, out, cols, dy.dtype, bias >= 0), stream, self.device)
+        with _on(self.device):
+            st = self.lib.ob_linear_grad(
+                self._ctx, int(worker), weight, bias, rows, out, cols, checkpoint._format, checkpoint._codes,
+                checkpoint._scales, gdt, gp, lddy, 1 if accumulate else 0, self._grad_ptr(grads),
+                None if work is None else work.data_ptr(), have, _stream_on(stream, self.device))
+        _check(st, "ob_linear_grad")
+
+    def linear_grad_work(self, rows, out_features, in_features, dy_dtype=torch.bfloat16, bias=True) -> int:
+        """Bytes of scratch that linear_grad needs."""
+        need = _i64()
+        _check(self.lib.ob_linear_grad_work(int(rows), int(out_features), int(in_features), _DTYPES[dy_dtype],
+                                            1 if bias else 0, ctypes.byref(need)), "ob_linear_grad_work")
+        return need.value
 
     # -- kernel timing -------------------------------------------------------
     def profile(self, enable: bool) -> None:

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libob.so")
 SOURCES = [os.path.join(CSRC, "kernels.hip"), os.path.join(CSRC, "topk.hip"),
-           os.path.join(CSRC, "api.cpp")]
+           os.path.join(CSRC, "activation.hip"), os.path.join(CSRC, "linear_grad.hip"),
+           os.path.join(CSRC, "embedding.hip"), os.path.join(CSRC, "api.cpp")]
 
 FLAGS = [
     "--offload-arch=gfx950",

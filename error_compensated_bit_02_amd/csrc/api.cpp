@@ -10,6 +10,7 @@
 #include <utility>
 #include <vector>
 
+#include "activation.h"
 #include "internal.h"
 
 namespace {
@@ -66,7 +67,8 @@ const char *const kKindNames[] = {
     "worker_pass1", "scale_finalize", "worker_pass2", "server_pass1",
     "server_pass2", "server_pass2_update", "apply_update", "worker_residual",
     "server_residual", "update_residual", "materialize", "warmup", "zero_errors",
-    "trust_norms", "trust_ratio", "cltk_select", "cltk_gather", "cltk_average"};
+    "trust_norms", "trust_ratio", "cltk_select", "cltk_gather", "cltk_average",
+    "embedding_lookup", "embedding_order", "embedding_sum", "linear_grad", "linear_join"};
 static_assert(sizeof(kKindNames) / sizeof(kKindNames[0]) == ob::K_NUM_KINDS,
               "one name per kernel kind");
 
@@ -94,9 +96,10 @@ int check_ptrs(const P *...ps) {
 }
 
 // Brackets one launch with events when profiling is on.  On a failure the
-// event pair goes back to the pool.
+// event pair goes back to the pool.  own_tables: the launch reads the
+// context's tables or scratch, so rewriting them has to wait for it.
 template <typename F>
-int timed(ob_ctx *c, ob::Kind kind, hipStream_t s, F &&launch, bool events = true) {
+int timed(ob_ctx *c, ob::Kind kind, hipStream_t s, F &&launch, bool events = true, bool own_tables = true) {
   EventPair ev;
   const bool profiling = events && c->profiling;
   if (profiling) {
@@ -116,8 +119,10 @@ int timed(ob_ctx *c, ob::Kind kind, hipStream_t s, F &&launch, bool events = tru
     }
   }
   launch();
-  c->launched = true;
-  c->last_stream = s;
+  if (own_tables) {
+    c->launched = true;
+    c->last_stream = s;
+  }
   const bool launched = hipGetLastError() == hipSuccess;
   if (profiling) {
     if (!launched || hipEventRecord(ev.stop, s) != hipSuccess) {
@@ -127,6 +132,47 @@ int timed(ob_ctx *c, ob::Kind kind, hipStream_t s, F &&launch, bool events = tru
     c->pending[kind].push_back(ev);
   }
   return launched ? OB_OK : OB_ERR_DEVICE;
+}
+
+// Launches of the gradient-making operators: they use the caller's buffers
+// only.
+template <typename F>
+int timed_free(ob_ctx *c, ob::Kind kind, hipStream_t s, F &&launch) {
+  return timed(c, kind, s, launch, true, false);
+}
+
+bool dtype_ok(int32_t d) { return d == OB_GRAD_F32 || d == OB_GRAD_BF16; }
+int64_t dtype_size(int32_t d) { return d == OB_GRAD_BF16 ? 2 : 4; }
+
+// A device pointer that needs only its element's alignment.
+int check_elements(const void *p, int64_t size) {
+  if (p == nullptr) return OB_ERR_INVALID;
+  return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(size) == 0 ? OB_OK : OB_ERR_ALIGN;
+}
+
+// A [rows][cols] matrix with row stride ld: extents that 64-bit byte offsets hold.
+bool matrix_ok(int64_t rows, int64_t cols, int64_t ld) {
+  return ld >= cols && (rows <= 1 || ld <= (int64_t{1} << 60) / rows);
+}
+
+bool act_shape_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 1 && cols <= (int64_t{1} << 30) && rows <= (int64_t{1} << 31) &&
+         ob::act_tiles(rows, cols) <= ob::kMaxGrid * ob::kWaves;
+}
+
+bool act_format_ok(int32_t f) { return f == OB_ACT_E4M3 || f == OB_ACT_INT8; }
+bool act_fn_ok(int32_t f) { return f >= OB_FN_NONE && f <= OB_FN_SILU; }
+
+// Where worker w's gradient of tensor t starts in grads.
+void *grad_at(const ob_ctx *c, void *grads, int32_t w, int32_t t) {
+  const int64_t at = static_cast<int64_t>(w) * c->N + c->off[t];
+  return static_cast<char *>(grads) + at * (c->bf16 ? 2 : 4);
+}
+
+int check_work(int64_t need, const void *work, int64_t work_bytes) {
+  if (need == 0) return OB_OK;
+  if (work_bytes < need) return OB_ERR_INVALID;
+  return check_ptr(work);
 }
 
 // Per-step scratch of one call: the context's own, or the static buffer of
@@ -739,6 +785,200 @@ int ob_cltk_step(ob_ctx *c, int64_t step, const void *grads, float *memory, int3
     st2 = timed(c, ob::K_TOPK_AVERAGE, s,
                 [&] { ob::launch_topk(ob::TopkStage::kAverage, c->geo, c->bf16, a, s); });
   return st2;
+}
+
+int ob_act_layout(int64_t rows, int64_t cols, int64_t *pitch, int64_t *code_bytes, int64_t *scale_bytes) {
+  if (pitch == nullptr || code_bytes == nullptr || scale_bytes == nullptr) return OB_ERR_INVALID;
+  if (!act_shape_ok(rows, cols)) return OB_ERR_INVALID;
+  *pitch = ob::act_pitch(cols);
+  *code_bytes = rows * *pitch;
+  *scale_bytes = ob::act_blocks(rows) * *pitch;
+  return OB_OK;
+}
+
+int ob_act_save(int32_t format, int32_t fn, int64_t rows, int64_t cols, int32_t dtype, const void *x, int64_t ldx,
+                void *y, int64_t ldy, uint8_t *codes, uint8_t *scales, void *stream) {
+  if (!act_format_ok(format) || !act_fn_ok(fn) || !dtype_ok(dtype) || !act_shape_ok(rows, cols)) return OB_ERR_INVALID;
+  if (!matrix_ok(rows, cols, ldx) || (fn != OB_FN_NONE && !matrix_ok(rows, cols, ldy))) return OB_ERR_INVALID;
+  if (rows == 0) return OB_OK;
+  if (fn == OB_FN_NONE && y != nullptr) return OB_ERR_INVALID;
+  int st = check_elements(x, dtype_size(dtype));
+  if (st == OB_OK && fn != OB_FN_NONE) st = check_elements(y, dtype_size(dtype));
+  if (st == OB_OK) st = check_ptrs(codes, scales);
+  if (st) return st;
+  ob::ActArgs a{};
+  a.rows = rows;
+  a.cols = cols;
+  a.x = x;
+  a.ldx = ldx;
+  a.y = y;
+  a.ldy = fn == OB_FN_NONE ? 0 : ldy;
+  a.codes = codes;
+  a.scales = scales;
+  ob::launch_act(true, format, fn, dtype == OB_GRAD_BF16, a, static_cast<hipStream_t>(stream));
+  return hipGetLastError() == hipSuccess ? OB_OK : OB_ERR_DEVICE;
+}
+
+int ob_act_load(int32_t format, int64_t rows, int64_t cols, const uint8_t *codes, const uint8_t *scales, int32_t dtype,
+                void *out, int64_t ldo, void *stream) {
+  if (!act_format_ok(format) || !dtype_ok(dtype) || !act_shape_ok(rows, cols) || !matrix_ok(rows, cols, ldo))
+    return OB_ERR_INVALID;
+  if (rows == 0) return OB_OK;
+  int st = check_elements(out, dtype_size(dtype));
+  if (st == OB_OK) st = check_ptrs(codes, scales);
+  if (st) return st;
+  ob::ActArgs a{};
+  a.rows = rows;
+  a.cols = cols;
+  a.y = out;
+  a.ldy = ldo;
+  a.codes_in = codes;
+  a.scales_in = scales;
+  ob::launch_act(false, format, OB_FN_NONE, dtype == OB_GRAD_BF16, a, static_cast<hipStream_t>(stream));
+  return hipGetLastError() == hipSuccess ? OB_OK : OB_ERR_DEVICE;
+}
+
+int ob_act_backward(int32_t format, int32_t fn, int64_t rows, int64_t cols, const uint8_t *codes, const uint8_t *scales,
+                    int32_t dtype, const void *dy, int64_t lddy, void *dx, int64_t lddx, void *stream) {
+  if (!act_format_ok(format) || !act_fn_ok(fn) || fn == OB_FN_NONE || !dtype_ok(dtype) || !act_shape_ok(rows, cols))
+    return OB_ERR_INVALID;
+  if (!matrix_ok(rows, cols, lddy) || !matrix_ok(rows, cols, lddx)) return OB_ERR_INVALID;
+  if (rows == 0) return OB_OK;
+  int st = check_elements(dy, dtype_size(dtype));
+  if (st == OB_OK) st = check_elements(dx, dtype_size(dtype));
+  if (st == OB_OK) st = check_ptrs(codes, scales);
+  if (st) return st;
+  ob::ActArgs a{};
+  a.rows = rows;
+  a.cols = cols;
+  a.x = dy;
+  a.ldx = lddy;
+  a.y = dx;
+  a.ldy = lddx;
+  a.codes_in = codes;
+  a.scales_in = scales;
+  ob::launch_act(false, format, fn, dtype == OB_GRAD_BF16, a, static_cast<hipStream_t>(stream));
+  return hipGetLastError() == hipSuccess ? OB_OK : OB_ERR_DEVICE;
+}
+
+int ob_linear_grad_work(int64_t rows, int64_t out_features, int64_t in_features, int32_t dy_dtype, int32_t bias,
+                        int64_t *work_bytes) {
+  if (work_bytes == nullptr || !dtype_ok(dy_dtype) || out_features < 1 || !act_shape_ok(rows, in_features) ||
+      !ob::linear_fits(rows, out_features, in_features))
+    return OB_ERR_INVALID;
+  *work_bytes = static_cast<int64_t>(
+      ob::linear_work_bytes(rows, out_features, in_features, dy_dtype == OB_GRAD_BF16, bias != 0));
+  return OB_OK;
+}
+
+int ob_linear_grad(ob_ctx *c, int32_t worker, int32_t weight, int32_t bias, int64_t rows, int64_t out_features,
+                   int64_t in_features, int32_t format, const uint8_t *codes, const uint8_t *scales, int32_t dy_dtype,
+                   const void *dy, int64_t lddy, int32_t accumulate, void *grads, void *work, int64_t work_bytes,
+                   void *stream) {
+  if (c == nullptr || worker < 0 || worker >= c->W || weight < 0 || weight >= c->T || bias < -1 || bias >= c->T ||
+      bias == weight)
+    return OB_ERR_INVALID;
+  int64_t need = 0;
+  if (!act_format_ok(format) ||
+      ob_linear_grad_work(rows, out_features, in_features, dy_dtype, bias >= 0, &need) != OB_OK)
+    return OB_ERR_INVALID;
+  if (c->numel[weight] / in_features != out_features || c->numel[weight] % in_features != 0) return OB_ERR_INVALID;
+  if (bias >= 0 && c->numel[bias] != out_features) return OB_ERR_INVALID;
+  if (!matrix_ok(rows, out_features, lddy)) return OB_ERR_INVALID;
+  int st = check_ptr(grads);
+  if (st == OB_OK && rows > 0) st = check_elements(dy, dtype_size(dy_dtype));
+  if (st == OB_OK && rows > 0) st = check_ptrs(codes, scales);
+  if (st == OB_OK) st = check_work(need, work, work_bytes);
+  if (st) return st;
+  ob::LinearArgs a{};
+  a.rows = rows;
+  a.out = out_features;
+  a.in = in_features;
+  a.codes = codes;
+  a.scales = scales;
+  a.pitch = ob::act_pitch(in_features);
+  a.fmt = format;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.dy_bf16 = dy_dtype == OB_GRAD_BF16;
+  a.dw = grad_at(c, grads, worker, weight);
+  a.db = bias >= 0 ? grad_at(c, grads, worker, bias) : nullptr;
+  a.grad_bf16 = c->bf16;
+  a.accumulate = accumulate != 0;
+  a.work = work;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = timed_free(c, ob::K_LINEAR_GRAD, s, [&] { ob::launch_linear_grad(a, s); });
+  if (st == OB_OK && ob::linear_needs_join(a))
+    st = timed_free(c, ob::K_LINEAR_JOIN, s, [&] { ob::launch_linear_join(a, s); });
+  return st;
+}
+
+int ob_embedding_lookup(ob_ctx *c, int32_t tensor, int64_t dim, int64_t tokens, const void *ids, int32_t id_dtype,
+                        const float *params, double scale, int32_t out_dtype, void *out, int64_t ldo, void *stream) {
+  if (c == nullptr || tensor < 0 || tensor >= c->T || dim < 1 || tokens < 0 || !dtype_ok(out_dtype) ||
+      (id_dtype != OB_ID_I32 && id_dtype != OB_ID_I64) || !std::isfinite(scale))
+    return OB_ERR_INVALID;
+  if (c->numel[tensor] % dim != 0 || !ob::embed_fits(tokens, c->numel[tensor] / dim, dim) ||
+      !matrix_ok(tokens, dim, ldo))
+    return OB_ERR_INVALID;
+  if (tokens == 0) return OB_OK;
+  int st = check_ptr(params);
+  if (st == OB_OK) st = check_elements(ids, id_dtype == OB_ID_I64 ? 8 : 4);
+  if (st == OB_OK) st = check_elements(out, dtype_size(out_dtype));
+  if (st) return st;
+  ob::EmbedArgs a{};
+  a.ids = ids;
+  a.ids64 = id_dtype == OB_ID_I64;
+  a.tokens = tokens;
+  a.vocab = c->numel[tensor] / dim;
+  a.dim = dim;
+  a.scale = static_cast<float>(scale);
+  a.table = params + c->off[tensor];
+  a.out = out;
+  a.ldo = ldo;
+  a.value_bf16 = out_dtype == OB_GRAD_BF16;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed_free(c, ob::K_EMBED_LOOKUP, s, [&] { ob::launch_embed_lookup(a, s); });
+}
+
+int ob_embedding_grad_work(int64_t tokens, int64_t dim, int64_t *work_bytes) {
+  if (work_bytes == nullptr || tokens < 0 || dim < 1 || !ob::embed_fits(tokens, 1, dim)) return OB_ERR_INVALID;
+  *work_bytes = static_cast<int64_t>(ob::embed_work_bytes(tokens, dim));
+  return OB_OK;
+}
+
+int ob_embedding_grad(ob_ctx *c, int32_t worker, int32_t tensor, int64_t dim, int64_t tokens, const void *ids,
+                      int32_t id_dtype, double scale, int32_t dy_dtype, const void *dy, int64_t lddy,
+                      int32_t accumulate, void *grads, void *work, int64_t work_bytes, void *stream) {
+  if (c == nullptr || worker < 0 || worker >= c->W || tensor < 0 || tensor >= c->T || dim < 1 || tokens < 0 ||
+      !dtype_ok(dy_dtype) || (id_dtype != OB_ID_I32 && id_dtype != OB_ID_I64) || !std::isfinite(scale))
+    return OB_ERR_INVALID;
+  if (c->numel[tensor] % dim != 0 || !ob::embed_fits(tokens, c->numel[tensor] / dim, dim) ||
+      !matrix_ok(tokens, dim, lddy))
+    return OB_ERR_INVALID;
+  int st = check_ptr(grads);
+  if (st == OB_OK && tokens > 0) st = check_elements(ids, id_dtype == OB_ID_I64 ? 8 : 4);
+  if (st == OB_OK && tokens > 0) st = check_elements(dy, dtype_size(dy_dtype));
+  if (st == OB_OK) st = check_work(static_cast<int64_t>(ob::embed_work_bytes(tokens, dim)), work, work_bytes);
+  if (st) return st;
+  ob::EmbedArgs a{};
+  a.ids = ids;
+  a.ids64 = id_dtype == OB_ID_I64;
+  a.tokens = tokens;
+  a.vocab = c->numel[tensor] / dim;
+  a.dim = dim;
+  a.scale = static_cast<float>(scale);
+  a.dy = dy;
+  a.lddy = lddy;
+  a.value_bf16 = dy_dtype == OB_GRAD_BF16;
+  a.grad = grad_at(c, grads, worker, tensor);
+  a.grad_bf16 = c->bf16;
+  a.accumulate = accumulate != 0;
+  a.work = work;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (tokens > 0 || !a.accumulate) st = timed_free(c, ob::K_EMBED_ORDER, s, [&] { ob::launch_embed_order(a, s); });
+  if (st == OB_OK && tokens > 0) st = timed_free(c, ob::K_EMBED_SUM, s, [&] { ob::launch_embed_sum(a, s); });
+  return st;
 }
 
 int ob_profile_enable(ob_ctx *c, int32_t enable) {

@@ -100,6 +100,11 @@ enum Kind {
   K_TOPK_SELECT,
   K_TOPK_GATHER,
   K_TOPK_AVERAGE,
+  K_EMBED_LOOKUP,
+  K_EMBED_ORDER,
+  K_EMBED_SUM,
+  K_LINEAR_GRAD,
+  K_LINEAR_JOIN,
   K_NUM_KINDS
 };
 
@@ -237,6 +242,70 @@ void launch_trust_ratio(const Geometry &g, const double2 *partials, float *ratio
 void launch_materialize(const Geometry &g, const MaterializeArgs &a, hipStream_t s);
 void launch_warmup(const Geometry &g, bool bf16, const WarmupArgs &a, hipStream_t s);
 void launch_zero_errors(const Geometry &g, float *err_w, float *err_s, hipStream_t s);
+
+// 8-bit activation checkpoints (activation.hip; the format is in activation.h).
+constexpr int kActNone = 0, kActGelu = 1, kActGeluTanh = 2, kActSilu = 3;   // ob_act_fn
+struct ActArgs {
+  int64_t rows, cols;
+  const void *x;             // save: the activation's input; backward: dy; load: null
+  int64_t ldx;               // its row stride in elements
+  void *y;                   // save: the activation's output or null; backward: dx; load: the values
+  int64_t ldy;
+  uint8_t *codes;            // [rows][pitch] written by save
+  uint8_t *scales;           // [ceil(rows/32)][pitch]
+  const uint8_t *codes_in;   // read by load and backward
+  const uint8_t *scales_in;
+  int64_t pitch;             // the rest is filled in by launch_act
+  uint32_t col_tiles, tiles;
+};
+int64_t act_tiles(int64_t rows, int64_t cols);   // wavefronts of one launch
+void launch_act(bool save, int fmt, int act, bool bf16, ActArgs a, hipStream_t s);
+
+// Embedding lookup and gradient (embedding.hip).
+struct EmbedArgs {
+  const void *ids;           // [tokens] int32 or int64
+  bool ids64;
+  int64_t tokens, vocab, dim;
+  float scale;
+  const float *table;        // lookup: [vocab][dim]
+  void *out;                 // lookup: [tokens][ldo]
+  int64_t ldo;
+  const void *dy;            // gradient: [tokens][lddy]
+  int64_t lddy;
+  bool value_bf16;           // element type of out, of dy
+  void *grad;                // gradient: [vocab][dim], the list's gradient type
+  bool grad_bf16;
+  bool accumulate;
+  void *work;
+};
+// Whether launch sizes and 32-bit positions hold these counts.
+bool embed_fits(int64_t tokens, int64_t vocab, int64_t dim);
+size_t embed_work_bytes(int64_t tokens, int64_t dim);
+void launch_embed_lookup(const EmbedArgs &a, hipStream_t s);
+void launch_embed_order(const EmbedArgs &a, hipStream_t s);   // sorted positions; zeroes the gradient
+void launch_embed_sum(const EmbedArgs &a, hipStream_t s);     // one sum per row present
+
+// Weight and bias gradient from a checkpoint (linear_grad.hip).
+struct LinearArgs {
+  int64_t rows, out, in;     // tokens, rows of the weight, columns of the weight
+  const uint8_t *codes;      // [rows][pitch]
+  const uint8_t *scales;     // [ceil(rows/32)][pitch]
+  int64_t pitch;
+  int fmt;
+  const void *dy;            // [rows][lddy]
+  int64_t lddy;
+  bool dy_bf16;
+  void *dw;                  // [out][in], the list's gradient type
+  void *db;                  // [out] or null
+  bool grad_bf16;
+  bool accumulate;
+  void *work;
+};
+bool linear_fits(int64_t rows, int64_t out, int64_t in);
+size_t linear_work_bytes(int64_t rows, int64_t out, int64_t in, bool dy_bf16, bool bias);
+void launch_linear_grad(const LinearArgs &a, hipStream_t s);
+bool linear_needs_join(const LinearArgs &a);
+void launch_linear_join(const LinearArgs &a, hipStream_t s);
 
 // The no-allocation step's scratch: one static device array of this many
 // bytes per GPU (kernels.hip), which holds the step's partial sums and trust

@@ -88,6 +88,24 @@ typedef enum {
   OB_GRAD_BF16 = 1      /* gradients are bfloat16 (widened exactly to fp32) */
 } ob_grad_dtype;
 
+/* Element types of activations and their gradients are ob_grad_dtype codes. */
+typedef enum {
+  OB_ID_I32 = 0,        /* token ids are int32 */
+  OB_ID_I64 = 1         /* token ids are int64 */
+} ob_id_dtype;
+
+typedef enum {
+  OB_ACT_E4M3 = 0,      /* 8-bit floats: 4 exponent and 3 mantissa bits, no infinities (OCP) */
+  OB_ACT_INT8 = 1       /* two's complement integers -127..127 */
+} ob_act_format;
+
+typedef enum {
+  OB_FN_NONE = 0,
+  OB_FN_GELU = 1,       /* x * Phi(x), Phi the normal distribution function */
+  OB_FN_GELU_TANH = 2,  /* x * (1 + tanh(sqrt(2/pi) * (x + 0.044715 x^3))) / 2 */
+  OB_FN_SILU = 3        /* x / (1 + exp(-x)) */
+} ob_act_fn;
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char *ob_status_string(int status);
 
@@ -330,6 +348,91 @@ int ob_cltk_configure(ob_ctx *ctx, double density, int64_t *k_total);
 int ob_cltk_layout(const ob_ctx *ctx, int64_t *k_off);
 int ob_cltk_step(ob_ctx *ctx, int64_t step, const void *grads, float *memory, int32_t *index,
                  float *values, float *average, void *stream);
+
+/* ------------------------------------------------------------------------
+ * What fills a worker's gradient row: embedding lookup and gradient, 8-bit
+ * activation checkpoints, and the linear layer's gradient from one.
+ *
+ * Matrices are [rows][cols] with a row stride of ld >= cols elements; their
+ * pointers need the alignment of their element only (rows that all start on
+ * 16 bytes are read and written faster).  params, grads, codes, scales and
+ * work are aligned to 16 bytes as everywhere.  The *_grad calls write one
+ * tensor's gradient into row `worker` of grads [W][N] (the context's gradient
+ * type); padding and all other tensors and rows stay untouched.  With
+ * accumulate != 0 they add to what the tensor's gradient holds (in fp32,
+ * rounded once), otherwise they overwrite it.  Sums over tokens are fp32, in
+ * an order that depends on the sizes alone: the same call gives the same
+ * bits.  A call with no rows (tokens) reads nothing: its matrices and
+ * checkpoint may be NULL, and a gradient is written as 0 or left as it was.
+ *
+ * `work` is the caller's scratch of at least the bytes that the matching
+ * *_work call gives (host only; NULL when that is 0): each call writes what it
+ * reads there, so it needs no clearing and may be reused by the next call on
+ * the stream.  These calls use no scratch of the context: calls on different
+ * streams may overlap as long as their buffers and work do not.  They allocate
+ * nothing and may be captured into a HIP graph.
+ * ------------------------------------------------------------------------ */
+
+/* Source: the jarxiv page on "Activations and Gradients Compression for
+ * Model-Parallel Training", Abstract (activations kept or sent in compressed
+ * form).  The page gives no format; this one is the library's.
+ *
+ * 8-bit activation checkpoint of x [rows][cols]: codes [rows][pitch] bytes and
+ * scales [ceil(rows/32)][pitch] bytes, pitch = 64*ceil(cols/64).  Element
+ * (r, c) stands for code(r, c) * 2^(scales(r/32, c) - 127): 32 consecutive
+ * rows of a column share a power-of-two scale, the smallest (and at least
+ * 2^-111) for which the block's largest |x| fits the format (448 for e4m3, 127
+ * for int8); magnitudes past 1.875 * 2^127 count as that; codes are rounded to
+ * nearest even.  A block with a NaN or an
+ * infinity has scale byte 255 and stands for NaN throughout.  Every value is
+ * exact in bf16.  Bytes cols..pitch-1 of a row are never written and their
+ * content never reaches a result.
+ *
+ * ob_act_layout (host only): the pitch and the two sizes; rows up to 2^31,
+ * cols up to 2^30. */
+int ob_act_layout(int64_t rows, int64_t cols, int64_t *pitch, int64_t *code_bytes, int64_t *scale_bytes);
+
+/* Writes x's checkpoint and, with fn != OB_FN_NONE, y = fn(x) in the same
+ * pass.  x and y have type dtype; y may be x itself (same ld), and is NULL
+ * with OB_FN_NONE. */
+int ob_act_save(int32_t format, int32_t fn, int64_t rows, int64_t cols, int32_t dtype, const void *x, int64_t ldx,
+                void *y, int64_t ldy, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* The checkpoint's values; with dtype bf16 or fp32 alike they are exact. */
+int ob_act_load(int32_t format, int64_t rows, int64_t cols, const uint8_t *codes, const uint8_t *scales, int32_t dtype,
+                void *out, int64_t ldo, void *stream);
+
+/* dx = dy * fn'(checkpoint's values); dx may be dy itself (same ld).  fn is
+ * not OB_FN_NONE. */
+int ob_act_backward(int32_t format, int32_t fn, int64_t rows, int64_t cols, const uint8_t *codes, const uint8_t *scales,
+                    int32_t dtype, const void *dy, int64_t lddy, void *dx, int64_t lddx, void *stream);
+
+/* Gradient of a linear layer y = x W^T + b whose input x [rows][in_features]
+ * was kept as a checkpoint:
+ *   dW[o][i] = sum over r of dy[r][o] * xhat[r][i],  db[o] = sum over r of dy[r][o]
+ * tensor `weight` of the list is W [out_features][in_features], tensor `bias`
+ * is b [out_features] (-1: none).  dy is [rows][out_features], fp32 or bf16;
+ * products are exact and summed in fp32.  rows and in_features at most 2^24. */
+int ob_linear_grad_work(int64_t rows, int64_t out_features, int64_t in_features, int32_t dy_dtype, int32_t bias,
+                        int64_t *work_bytes);
+int ob_linear_grad(ob_ctx *ctx, int32_t worker, int32_t weight, int32_t bias, int64_t rows, int64_t out_features,
+                   int64_t in_features, int32_t format, const uint8_t *codes, const uint8_t *scales, int32_t dy_dtype,
+                   const void *dy, int64_t lddy, int32_t accumulate, void *grads, void *work, int64_t work_bytes,
+                   void *stream);
+
+/* Embedding lookup: out[t] = fp32(scale) * E[ids[t]], with tensor `tensor` of
+ * params [N] as the table E [numel/dim][dim] (at most 2^31 - 1 rows; at most
+ * 16,777,215 tokens).  A negative id is padding and gives a row of zeros; an id
+ * past the table gives a row of NaN.  out is [tokens][dim] of out_dtype. */
+int ob_embedding_lookup(ob_ctx *ctx, int32_t tensor, int64_t dim, int64_t tokens, const void *ids, int32_t id_dtype,
+                        const float *params, double scale, int32_t out_dtype, void *out, int64_t ldo, void *stream);
+
+/* Its gradient: dE[v] = fp32(scale) * (sum over t with ids[t] = v of dy[t]);
+ * ids outside the table contribute nothing.  dy is [tokens][dim] of dy_dtype. */
+int ob_embedding_grad_work(int64_t tokens, int64_t dim, int64_t *work_bytes);
+int ob_embedding_grad(ob_ctx *ctx, int32_t worker, int32_t tensor, int64_t dim, int64_t tokens, const void *ids,
+                      int32_t id_dtype, double scale, int32_t dy_dtype, const void *dy, int64_t lddy,
+                      int32_t accumulate, void *grads, void *work, int64_t work_bytes, void *stream);
 
 /* Kernel timing for measurement.  With profiling on, every kernel the context
  * launches is bracketed by HIP events on its stream.  ob_profile_read waits for

@@ -1,0 +1,702 @@
+"""The gradient-making operators on the GPU against plain 64-bit definitions
+(tests/grad_ops.py).  What has one right answer (codes, scales, decoded values,
+lookups, and sums of small integers, which fp32 holds exactly) must match bit
+for bit; the rest is held to bounds counted from the roundings made."""
+import numpy as np
+import pytest
+import torch
+
+import grad_ops as ref
+from error_compensated_bit_02_amd import ActCheckpoint, OneBitAdam, OneBitError
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+FNS = ["gelu", "gelu_tanh", "silu"]
+TYPES = [torch.float32, torch.bfloat16]
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+
+
+def _gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _put(t, dtype, extra=0, offset=0):
+    """t on the GPU as a view with row stride cols + extra, starting `offset` elements into its buffer."""
+    rows, cols = t.shape
+    flat = torch.full((offset + max(rows, 1) * (cols + extra),), 7.0, dtype=dtype, device=DEV)
+    view = flat[offset:].view(max(rows, 1), cols + extra)[:rows, :cols]
+    view.copy_(t.to(dtype))
+    return view, flat
+
+
+def _activations(rows, cols, seed):
+    x = torch.randn(rows, cols, generator=_gen(seed))
+    if cols > 2:
+        x[:, cols // 2] *= 50.0        # an outlier column
+        x[:, 1] = 0.0                  # an empty one
+    return x
+
+
+def _checkpoint(x, fmt):
+    ck = ActCheckpoint(x.shape[0], x.shape[1], fmt, device=DEV)
+    ck.codes.fill_(0x55)
+    ck.scales.fill_(0x55)
+    ck.save(x)
+    return ck
+
+
+# ---------------------------------------------------------------------------
+# the checkpoint
+# ---------------------------------------------------------------------------
+def _check_checkpoint(x, fmt):
+    """Scales, values and untouched padding of the checkpoint of x (a device matrix)."""
+    rows, cols = x.shape
+    ck = _checkpoint(x, fmt)
+    x64 = _f64(x)
+    want = ref.quantised(x64, fmt)
+    scales, codes = ck.scales.cpu().numpy(), ck.codes.cpu().numpy()
+    assert np.array_equal(scales[:, :cols], ref.scale_bytes(x64, fmt))
+    assert np.array_equal(ref.decoded(codes, scales, cols, fmt), want, equal_nan=True)
+    assert (scales[:, cols:] == 0x55).all() and (codes[:, cols:] == 0x55).all()
+    for dtype in TYPES:
+        out, flat = _put(torch.zeros(rows, cols), dtype, extra=3)
+        ck.load(out)
+        assert np.array_equal(_f64(out), want, equal_nan=True)
+        assert (flat.view(rows, cols + 3)[:, cols:] == 7.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,extra,offset", [
+    (1, 1, 0, 0), (1, 129, 0, 0), (31, 65, 0, 0), (32, 128, 0, 0), (33, 63, 1, 1), (64, 136, 8, 0), (97, 200, 0, 4),
+    (5, 1000, 24, 8)])
+def test_checkpoint(fmt, dtype, rows, cols, extra, offset):
+    x, _ = _put(_activations(rows, cols, 1), dtype, extra, offset)
+    _check_checkpoint(x, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_checkpoint_borders(fmt):
+    """Largest codes and the values just past them, ties, subnormals, zeros of
+    both signs, the largest and smallest floats; one column each."""
+    up = lambda v: float(np.nextafter(np.float32(v), np.float32(np.inf)))   # noqa: E731
+    lead = [448.0, up(448.0), 464.0, 127.0, up(127.0), 127.5, 1.0, up(1.75), 1.75, 1.984375, up(1.984375), 0.0, -0.0,
+            3.4028234663852886e38, 2.0 ** 126, 1.1754943508222875e-38, 1e-45, 2.0 ** -104, 2.0 ** -111, 2.0 ** -113]
+    x = torch.zeros(40, len(lead))
+    for c, v in enumerate(lead):
+        x[0, c] = v
+        x[1:32, c] = v * torch.linspace(-1.0, 1.0, 31)
+        x[3:9, c] = v * torch.tensor([17 / 32, 19 / 32, 33 / 64, 2.0 ** -9, 2.0 ** -16, 1.5 * 2.0 ** -16])
+        x[33, c] = -v
+    _check_checkpoint(x.to(DEV), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_checkpoint_of_a_non_finite_element(fmt, bad):
+    """Its block reads as NaN, the other blocks do not change."""
+    x = _activations(70, 100, 2)
+    x[40, 7] = bad
+    x[69, 99] = bad
+    xg = x.to(DEV)
+    _check_checkpoint(xg, fmt)
+    ck = _checkpoint(xg, fmt)
+    dy = torch.ones(70, 100, device=DEV)
+    dx = torch.empty_like(dy)
+    for fn in FNS:
+        ck.act_backward(fn, dy, dx)
+        nan = torch.isnan(dx).cpu()
+        assert nan[32:64, 7].all() and nan[64:, 99].all() and int(nan.sum()) == 32 + 6
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_every_code(fmt):
+    """All 256 codes at the smallest, a middle and the largest scale, in both
+    types.  At the largest some codes (which save never writes there) stand for
+    values past the range of floats: infinities once in a float."""
+    codes = torch.arange(256, dtype=torch.uint8).repeat(3, 1).repeat_interleave(32, dim=0)
+    scales = torch.tensor([16, 127, 247 if fmt == "e4m3" else 249], dtype=torch.uint8).unsqueeze(1).repeat(1, 256)
+    with np.errstate(over="ignore"):
+        want = ref.decoded(codes.numpy(), scales.numpy(), 256, fmt).astype(np.float32).astype(np.float64)
+    if fmt == "int8":
+        codes[:, 128] = 0      # -128 is not a code
+        want[:, 128] = 0.0
+    ck = ActCheckpoint(96, 256, fmt, codes=codes.to(DEV), scales=scales.to(DEV))
+    for dtype in TYPES:
+        out = torch.empty(96, 256, dtype=dtype, device=DEV)
+        ck.load(out)
+        assert np.array_equal(_f64(out), want, equal_nan=True)
+
+
+# ---------------------------------------------------------------------------
+# activations
+# ---------------------------------------------------------------------------
+def _near(got, want, bound, dtype):
+    """|got - want| within `bound` plus the store's half step (and 2^-126, what a flushed tiny number loses)."""
+    got = _f64(got)
+    lim = bound + (np.abs(want) + bound) * ref.HALF[dtype] + 2.0 ** -126
+    bad = ~(np.abs(got - want) <= lim)
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], want[bad][:4], lim[bad][:4])
+
+
+def _spread(rows, cols, seed):
+    """Values over the whole working range of the activations."""
+    x = torch.randn(rows, cols, generator=_gen(seed))
+    x[:, ::3] *= 4.0
+    x[0, :] = torch.linspace(-12.0, 12.0, cols)
+    return x
+
+
+@pytest.mark.parametrize("fn", FNS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,extra,offset", [(1, 1, 0, 0), (1, 512, 0, 0), (33, 97, 0, 0), (64, 256, 8, 8), (45, 130, 5, 1)])
+def test_save_with_activation(fn, dtype, rows, cols, extra, offset):
+    x, _ = _put(_spread(rows, cols, 3), dtype, extra, offset)
+    y, flat = _put(torch.zeros(rows, cols), dtype, extra, offset)
+    ck = ActCheckpoint(rows, cols, "e4m3", device=DEV)
+    ck.save(x, act=fn, y=y)
+    x64 = _f64(x)
+    want = ref.act(x64, fn)
+    # Phi or sigma below 2^-126 may flush to 0 before it is multiplied by x: |x| * 2^-126 more
+    _near(y, want, np.abs(want) * ref.act_error(x64, fn) + np.abs(x64) * 2.0 ** -126, dtype)
+    if extra:
+        assert (flat[offset:].view(rows, cols + extra)[:, cols:] == 7.0).all()
+    plain = ActCheckpoint(rows, cols, "e4m3", device=DEV)
+    plain.save(x)
+    assert torch.equal(plain.codes[:, :cols], ck.codes[:, :cols]) and torch.equal(plain.scales[:, :cols], ck.scales[:, :cols])
+    z = x.clone() if extra == 0 else x
+    ck.save(z, act=fn, y=z)            # in place
+    assert torch.equal(z, y)
+    assert torch.equal(plain.codes[:, :cols], ck.codes[:, :cols])
+
+
+def _slope_bound(x, fn):
+    """Error of act'(x): its two terms carry act_error each, and lose what a
+    factor flushed below 2^-126 is multiplied by, at most 2|x|(1 + 3*0.044715 x^2)."""
+    a = np.abs(ref.act_slope(x, fn))
+    second = np.abs(ref.act_slope(x, fn) - (ref._phi(x) if fn == "gelu" else
+                                            ref._sigmoid(ref.C * (x + ref.K * x ** 3) if fn == "gelu_tanh" else x)))
+    return (a + 2 * second) * ref.act_error(x, fn) + 2.0 ** -126 * (1 + 2 * np.abs(x) * (1 + 3 * ref.K * x * x))
+
+
+@pytest.mark.parametrize("fn", FNS)
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,extra,offset", [(1, 1, 0, 0), (3, 700, 0, 0), (64, 128, 0, 0), (77, 131, 9, 3)])
+def test_act_backward(fn, fmt, dtype, rows, cols, extra, offset):
+    ck = _checkpoint(_spread(rows, cols, 4).to(DEV), fmt)
+    dy, _ = _put(torch.randn(rows, cols, generator=_gen(5)), dtype, extra, offset)
+    dx, flat = _put(torch.zeros(rows, cols), dtype, extra, offset)
+    ck.act_backward(fn, dy, dx)
+    xhat = ref.decoded(ck.codes.cpu().numpy(), ck.scales.cpu().numpy(), cols, fmt)
+    dy64 = _f64(dy)
+    _near(dx, dy64 * ref.act_slope(xhat, fn), np.abs(dy64) * (_slope_bound(xhat, fn) + 2 * ref.U32 * np.abs(ref.act_slope(xhat, fn))),
+          dtype)
+    if extra:
+        assert (flat[offset:].view(rows, cols + extra)[:, cols:] == 7.0).all()
+    ck.act_backward(fn, dy, dy)        # in place
+    assert torch.equal(dy, dx)
+
+
+@pytest.mark.parametrize("fn", FNS)
+def test_act_backward_of_huge_values(fn):
+    """Slopes far out are 0 and 1, not the NaN of 0 times an overflow."""
+    x = torch.tensor([[-1e30, -1e12, -300.0, -60.0, 60.0, 300.0, 1e12, 1e30]]).repeat(2, 1)
+    ck = _checkpoint(x.to(DEV), "int8")
+    dy = torch.ones(2, 8, device=DEV)
+    ck.act_backward(fn, dy, dy)
+    want = torch.tensor([0.0, 0.0, 0.0, 0.0, 1.0, 1.0, 1.0, 1.0])
+    assert torch.allclose(dy[0].cpu(), want, rtol=0, atol=1e-20)
+
+
+@pytest.mark.parametrize("fn", FNS)
+def test_act_backward_against_differences(fn):
+    """d/dx of the saved activation: central differences with h = 2^-6 of fp32
+    values of size up to 5 are off by 5 * 2^-23 / h = 4e-5 from rounding and
+    h^2/6 times a third derivative below 2 = 1e-4 from curvature."""
+    ck = _checkpoint(torch.linspace(-4.0, 4.0, 512).view(4, 128).to(DEV), "int8")
+    x = torch.empty(4, 128, device=DEV)
+    ck.load(x)
+    h = 2.0 ** -6
+    scratch = ActCheckpoint(4, 128, device=DEV)
+    lo, hi = torch.empty_like(x), torch.empty_like(x)
+    scratch.save(x - h, act=fn, y=lo)
+    scratch.save(x + h, act=fn, y=hi)
+    dx = torch.empty_like(x)
+    ck.act_backward(fn, torch.ones_like(x), dx)
+    assert float(((hi.double() - lo.double()) / (2 * h) - dx.double()).abs().max()) < 1.5e-4
+
+
+# ---------------------------------------------------------------------------
+# linear gradient
+# ---------------------------------------------------------------------------
+def _linear_case(rows, out, inp, dy_dtype, grad, fmt, bias, extra=0, offset=0, whole=False, seed=6, workers=2):
+    """A list [other, weight, bias, other] and the buffers of one call."""
+    opt = OneBitAdam([5, out * inp, out, 9], workers, "bf16" if grad == torch.bfloat16 else "f32")
+    if whole:      # small whole numbers: every product and sum is exact in fp32
+        x = torch.randint(-8, 9, (rows, inp), generator=_gen(seed)).float()
+        dy = torch.randint(-4, 5, (rows, out), generator=_gen(seed + 1)).float()
+    else:
+        x = _activations(rows, inp, seed)
+        dy = torch.randn(rows, out, generator=_gen(seed + 1))
+    ck = _checkpoint(x.to(DEV), fmt) if rows else ActCheckpoint(0, inp, fmt, device=DEV)
+    dyg, _ = _put(dy, dy_dtype, extra, offset)
+    grads = torch.full((workers, opt.N), 3.0, dtype=grad, device=DEV)
+    return opt, ck, dyg, grads
+
+
+def _others_untouched(opt, grads, worker, tensors, keep=3.0):
+    g = grads.clone()
+    for t in tensors:
+        g[worker, opt.offsets[t]: opt.offsets[t] + opt.numel[t]] = keep
+    assert (g == keep).all()
+
+
+LINEAR_SHAPES = [(1, 1, 1), (1, 64, 64), (3, 17, 33), (32, 128, 128), (33, 129, 127), (64, 100, 257), (700, 130, 70),
+                 (513, 260, 390), (2500, 64, 40)]
+
+
+@pytest.mark.parametrize("rows,out,inp", LINEAR_SHAPES)
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dy_dtype", TYPES)
+def test_linear_grad_of_whole_numbers(rows, out, inp, fmt, dy_dtype):
+    """Sums of at most 2500 * 8 * 4 = 80000: exact in fp32, so bit for bit."""
+    opt, ck, dy, grads = _linear_case(rows, out, inp, dy_dtype, torch.float32, fmt, True, whole=True)
+    opt.linear_grad(1, 1, 2, ck, dy, grads)
+    xhat = ref.decoded(ck.codes.cpu().numpy(), ck.scales.cpu().numpy(), inp, fmt)
+    dw, db, _, _ = ref.linear(_f64(dy), xhat)
+    a, b = opt.offsets[1], opt.offsets[2]
+    assert np.array_equal(_f64(grads[1, a: a + out * inp]).reshape(out, inp), dw)
+    assert np.array_equal(_f64(grads[1, b: b + out]), db)
+    _others_untouched(opt, grads, 1, [1, 2])
+    opt.linear_grad(1, 1, 2, ck, dy, grads, accumulate=True)
+    assert np.array_equal(_f64(grads[1, a: a + out * inp]).reshape(out, inp), 2 * dw)
+    assert np.array_equal(_f64(grads[1, b: b + out]), 2 * db)
+
+
+@pytest.mark.parametrize("rows,out,inp,extra,offset", [
+    (1, 5, 7, 0, 0), (40, 65, 130, 0, 0), (300, 128, 256, 128, 0), (1000, 72, 96, 8, 8), (257, 33, 65, 7, 1), (96, 41, 48, 7, 0)])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dy_dtype,grad", [(torch.float32, torch.float32), (torch.bfloat16, torch.float32),
+                                           (torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16)])
+@pytest.mark.parametrize("bias", [True, False])
+def test_linear_grad(rows, out, inp, extra, offset, fmt, dy_dtype, grad, bias):
+    """n additions in any order are off by n * 2^-24 of the sum of magnitudes;
+    twice that for the matrix unit, whose inner sums may truncate."""
+    opt, ck, dy, grads = _linear_case(rows, out, inp, dy_dtype, grad, fmt, bias, extra, offset)
+    opt.linear_grad(0, 1, 2 if bias else None, ck, dy, grads)
+    xhat = ref.decoded(ck.codes.cpu().numpy(), ck.scales.cpu().numpy(), inp, fmt)
+    dw, db, mw, mb = ref.linear(_f64(dy), xhat)
+    a, b = opt.offsets[1], opt.offsets[2]
+    n = 2 * (rows + 8) * ref.U32
+    _near(grads[0, a: a + out * inp].view(out, inp), dw, n * mw, grad)
+    if bias:
+        _near(grads[0, b: b + out], db, n * mb, grad)
+    _others_untouched(opt, grads, 0, [1, 2] if bias else [1])
+    again = torch.full_like(grads, 3.0)
+    opt.linear_grad(0, 1, 2 if bias else None, ck, dy, again)
+    assert torch.equal(again, grads)
+    # one rounding more where it adds to what is there
+    before = grads.clone()
+    opt.linear_grad(0, 1, 2 if bias else None, ck, dy, grads, accumulate=True)
+    old = _f64(before[0, a: a + out * inp].view(out, inp))
+    _near(grads[0, a: a + out * inp].view(out, inp), old + dw, n * mw + ref.U32 * (np.abs(old) + np.abs(dw)), grad)
+
+
+def test_linear_grad_fp32_keeps_small_parts():
+    """An fp32 dY whose low bits carry the answer: 1 + 2^-20 against -1, and
+    values near both ends of the range."""
+    rows, out, inp = 64, 3, 2
+    dy = torch.zeros(rows, out)
+    dy[0, 0], dy[1, 0] = 1.0 + 2.0 ** -20, -1.0
+    dy[0, 1] = 1.2345678e38
+    dy[0, 2] = 2.3456789e-30
+    x = torch.ones(rows, inp)
+    opt = OneBitAdam([out * inp], 1)
+    ck = _checkpoint(x.to(DEV), "e4m3")
+    grads = torch.zeros(1, opt.N, device=DEV)
+    opt.linear_grad(0, 0, None, ck, dy.to(DEV), grads)
+    got = grads[0, : out * inp].view(out, inp).cpu()
+    assert torch.equal(got, torch.tensor([[2.0 ** -20] * 2, [float(dy[0, 1])] * 2, [float(dy[0, 2])] * 2]))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dy_dtype", TYPES)
+def test_linear_grad_of_non_finite_values(fmt, dy_dtype):
+    """A NaN block reaches its column of the weight only, an infinite dY its row."""
+    rows, out, inp = 100, 20, 30
+    x = torch.randint(1, 5, (rows, inp), generator=_gen(8)).float()
+    x[50, 4] = float("nan")
+    dy = torch.ones(rows, out)
+    dy[3, 6] = float("inf")
+    opt = OneBitAdam([out * inp, out], 1)
+    ck = _checkpoint(x.to(DEV), fmt)
+    grads = torch.zeros(1, opt.N, device=DEV)
+    opt.linear_grad(0, 0, 1, ck, dy.to(dy_dtype).to(DEV), grads)
+    w = grads[0, : out * inp].view(out, inp).cpu()
+    assert torch.isnan(w[:, 4]).all()
+    rest = torch.cat([w[:, :4], w[:, 5:]], dim=1)
+    assert torch.isinf(rest[6]).all() and torch.isfinite(torch.cat([rest[:6], rest[7:]])).all()
+    b = grads[0, opt.offsets[1]: opt.offsets[1] + out].cpu()
+    assert torch.isinf(b[6]) and torch.isfinite(torch.cat([b[:6], b[7:]])).all()
+
+
+def test_linear_grad_of_no_rows():
+    opt, ck, dy, grads = _linear_case(0, 6, 10, torch.bfloat16, torch.float32, "e4m3", True)
+    opt.linear_grad(0, 1, 2, ck, dy, grads, accumulate=True)
+    assert (grads == 3.0).all()
+    opt.linear_grad(0, 1, 2, ck, dy, grads)
+    a, b = opt.offsets[1], opt.offsets[2]
+    assert (grads[0, a: a + 60] == 0).all() and (grads[0, b: b + 6] == 0).all()
+    _others_untouched(opt, grads, 0, [1, 2])
+
+
+def test_linear_grad_against_differences():
+    """The layer is linear in W: with whole numbers, the change of sum(dy * (x W^T))
+    along a direction equals the gradient along it exactly."""
+    rows, out, inp = 90, 40, 50
+    opt, ck, dy, grads = _linear_case(rows, out, inp, torch.bfloat16, torch.float32, "int8", False, whole=True)
+    x = torch.empty(rows, inp, device=DEV)
+    ck.load(x)
+    opt.linear_grad(0, 1, None, ck, dy, grads)
+    dw = grads[0, opt.offsets[1]: opt.offsets[1] + out * inp].view(out, inp).double()
+    w = torch.randint(-3, 4, (out, inp), generator=_gen(9)).double().to(DEV)
+    d = torch.randint(-3, 4, (out, inp), generator=_gen(10)).double().to(DEV)
+    loss = lambda m: float((dy.double() * (x.double() @ m.t().contiguous())).sum())   # noqa: E731
+    assert loss(w + d) - loss(w) == float((dw * d).sum())
+
+
+# ---------------------------------------------------------------------------
+# embedding
+# ---------------------------------------------------------------------------
+def _ids(tokens, vocab, seed, pad=0.1, hot=0.3, dtype=torch.int64):
+    g = _gen(seed)
+    ids = torch.randint(0, vocab, (tokens,), generator=g)
+    ids[torch.rand(tokens, generator=g) < hot] = vocab // 2        # one frequent token
+    u = torch.rand(tokens, generator=g)
+    ids[u < pad] = -1
+    ids[(u >= pad) & (u < pad * 1.2)] = vocab                      # past the table
+    return ids.to(dtype)
+
+
+@pytest.mark.parametrize("tokens,vocab,dim,extra,offset", [
+    (1, 1, 1, 0, 0), (1, 50, 1024, 0, 0), (7, 30, 96, 0, 0), (1000, 77, 2056, 8, 8), (65, 100, 33, 2, 1), (300, 9, 5, 0, 0)])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("idt", [torch.int32, torch.int64])
+def test_embedding_lookup(tokens, vocab, dim, extra, offset, dtype, idt):
+    opt = OneBitAdam([3, vocab * dim, 4], 1)
+    params = torch.randn(opt.N, generator=_gen(11)).to(DEV)
+    ids = _ids(tokens, vocab, 12, dtype=idt)
+    out, flat = _put(torch.zeros(tokens, dim), dtype, extra, offset)
+    opt.embedding_lookup(1, dim, ids.to(DEV), params, out, scale=1.7)
+    table = params[opt.offsets[1]: opt.offsets[1] + vocab * dim].view(vocab, dim).cpu()
+    rows = table[ids.long().clamp(0, vocab - 1)] * torch.tensor(1.7, dtype=torch.float32)
+    rows[ids < 0] = 0.0
+    rows[ids >= vocab] = float("nan")
+    assert np.array_equal(_f64(out), _f64(rows.to(dtype)), equal_nan=True)
+    if extra:
+        assert (flat[offset:].view(tokens, dim + extra)[:, dim:] == 7.0).all()
+
+
+EMBED_SHAPES = [(1, 1, 1), (1, 50, 24), (31, 7, 8), (32, 7, 8), (33, 7, 8), (64, 3, 40), (257, 40, 520), (1000, 999, 33),
+                (4096, 50, 16), (4097, 50, 16), (9001, 20, 8), (70001, 300, 8), (5000, 1 << 20, 1), (3000, 2, 1032)]
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", EMBED_SHAPES)
+@pytest.mark.parametrize("dy_dtype,idt", [(torch.float32, torch.int64), (torch.bfloat16, torch.int32)])
+def test_embedding_grad_of_whole_numbers(tokens, vocab, dim, dy_dtype, idt):
+    """Sums of at most 70001 * 4: exact in fp32, so bit for bit."""
+    opt = OneBitAdam([70, vocab * dim, 4], 2)
+    ids = _ids(tokens, vocab, 13, dtype=idt)
+    dy = torch.randint(-4, 5, (tokens, dim), generator=_gen(14)).to(dy_dtype).to(DEV)
+    grads = torch.full((2, opt.N), 3.0, device=DEV)
+    opt.embedding_grad(1, 1, dim, ids.to(DEV), dy, grads, scale=0.5)
+    want, _, _ = ref.embedding_grad(ids.long().numpy(), _f64(dy), vocab)
+    a = opt.offsets[1]
+    got = grads[1, a: a + vocab * dim].view(vocab, dim)
+    assert np.array_equal(_f64(got), 0.5 * want)
+    _others_untouched(opt, grads, 1, [1])
+    opt.embedding_grad(1, 1, dim, ids.to(DEV), dy, grads, scale=1.0, accumulate=True)
+    assert np.array_equal(_f64(got), 1.5 * want)
+    _others_untouched(opt, grads, 1, [1])
+
+
+@pytest.mark.parametrize("tokens,vocab,dim,extra,offset", [(500, 30, 64, 0, 0), (2000, 5, 100, 8, 0), (700, 200, 129, 1, 1), (6000, 60, 72, 24, 8)])
+@pytest.mark.parametrize("dy_dtype,grad", [(torch.float32, torch.float32), (torch.bfloat16, torch.float32),
+                                           (torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16)])
+def test_embedding_grad(tokens, vocab, dim, extra, offset, dy_dtype, grad):
+    opt = OneBitAdam([vocab * dim], 1, "bf16" if grad == torch.bfloat16 else "f32")
+    ids = _ids(tokens, vocab, 15)
+    dy, _ = _put(torch.randn(tokens, dim, generator=_gen(16)), dy_dtype, extra, offset)
+    grads = torch.full((1, opt.N), 3.0, dtype=grad, device=DEV)
+    opt.embedding_grad(0, 0, dim, ids.to(DEV), dy, grads, scale=1.7)
+    s = float(np.float32(1.7))
+    want, mag, count = ref.embedding_grad(ids.numpy(), _f64(dy), vocab)
+    bound = (count[:, None] + 2) * ref.U32 * s * mag
+    got = grads[0, : vocab * dim].view(vocab, dim)
+    _near(got, s * want, bound, grad)
+    again = torch.full_like(grads, 5.0)
+    opt.embedding_grad(0, 0, dim, ids.to(DEV), dy, again, scale=1.7)
+    assert torch.equal(again[0, : vocab * dim], grads[0, : vocab * dim])
+    old = _f64(got)
+    opt.embedding_grad(0, 0, dim, ids.to(DEV), dy, grads, scale=1.7, accumulate=True)
+    _near(got, old + s * want, bound + ref.U32 * (np.abs(old) + np.abs(s * want)), grad)
+
+
+@pytest.mark.parametrize("fill", [-1, 5])
+def test_embedding_grad_without_a_single_row(fill):
+    """All padding, or all past the table: a gradient of zeros, or what was there."""
+    opt = OneBitAdam([5 * 24], 1)
+    ids = torch.full((100,), fill, device=DEV)
+    dy = torch.full((100, 24), float("nan"), device=DEV)
+    grads = torch.full((1, opt.N), 3.0, device=DEV)
+    opt.embedding_grad(0, 0, 24, ids, dy, grads, accumulate=True)
+    assert (grads == 3.0).all()
+    opt.embedding_grad(0, 0, 24, ids, dy, grads)
+    assert (grads[0, :120] == 0).all() and (grads[0, 120:] == 3.0).all()
+
+
+def test_embedding_of_no_tokens():
+    opt = OneBitAdam([5 * 24], 1)
+    none = torch.empty(0, dtype=torch.int64, device=DEV)
+    empty = torch.empty(0, 24, device=DEV)
+    grads = torch.full((1, opt.N), 3.0, device=DEV)
+    opt.embedding_lookup(0, 24, none, torch.zeros(opt.N, device=DEV), empty)
+    opt.embedding_grad(0, 0, 24, none, empty, grads, accumulate=True)
+    assert (grads == 3.0).all()
+    opt.embedding_grad(0, 0, 24, none, empty, grads)
+    assert (grads[0, :120] == 0).all() and (grads[0, 120:] == 3.0).all()
+
+
+def test_embedding_grad_against_differences():
+    """The lookup is linear in the table: with whole numbers the change of
+    sum(dy * lookup) along a direction equals the gradient along it exactly."""
+    vocab, dim, tokens = 30, 40, 500
+    opt = OneBitAdam([vocab * dim], 1)
+    ids = _ids(tokens, vocab, 17, pad=0.2)
+    ids[ids >= vocab] = 3
+    ids = ids.to(DEV)
+    dy = torch.randint(-4, 5, (tokens, dim), generator=_gen(18)).float().to(DEV)
+    e = torch.randint(-5, 6, (opt.N,), generator=_gen(19)).float().to(DEV)
+    d = torch.randint(-5, 6, (opt.N,), generator=_gen(20)).float().to(DEV)
+    grads = torch.zeros(1, opt.N, device=DEV)
+    opt.embedding_grad(0, 0, dim, ids, dy, grads, scale=2.0)
+    out = torch.empty(tokens, dim, device=DEV)
+
+    def loss(table):
+        opt.embedding_lookup(0, dim, ids, table, out, scale=2.0)
+        return float((out.double() * dy.double()).sum())
+
+    n = vocab * dim
+    assert loss(e + d) - loss(e) == float((grads[0, :n].double() * d[:n].double()).sum())
+
+
+# ---------------------------------------------------------------------------
+# refusals, streams, graphs
+# ---------------------------------------------------------------------------
+def test_refusals():
+    opt = OneBitAdam([6 * 10, 6, 7], 2)
+    ck = ActCheckpoint(4, 10, device=DEV)
+    dy = torch.zeros(4, 6, device=DEV)
+    grads = torch.full((2, opt.N), 3.0, device=DEV)
+    lin = lambda **k: opt.linear_grad(**{**dict(worker=0, weight=0, bias=1, checkpoint=ck, dy=dy, grads=grads), **k})   # noqa: E731
+    small = torch.zeros(4, 10, device=DEV)
+    for bad in [dict(worker=2), dict(worker=-1), dict(weight=3), dict(weight=-1), dict(bias=2), dict(bias=0),
+                dict(weight=2), dict(dy=torch.zeros(4, 7, device=DEV)), dict(dy=torch.zeros(5, 6, device=DEV)),
+                dict(dy=dy.half()), dict(dy=dy.cpu()), dict(dy=torch.zeros(6, 4, device=DEV).t()),
+                dict(grads=grads[:1]), dict(grads=grads.bfloat16()), dict(checkpoint=ActCheckpoint(4, 11, device=DEV)),
+                dict(work=torch.empty(1, dtype=torch.uint8, device=DEV)), dict(work=torch.empty(9999, dtype=torch.uint8))]:
+        with pytest.raises(OneBitError):
+            lin(**bad)
+    ids = torch.zeros(4, dtype=torch.int64, device=DEV)
+    params = torch.zeros(opt.N, device=DEV)
+    look = lambda **k: opt.embedding_lookup(**{**dict(tensor=0, dim=10, ids=ids, params=params, out=small), **k})   # noqa: E731
+    for bad in [dict(tensor=3), dict(dim=7), dict(dim=0), dict(ids=ids.float()), dict(ids=ids.cpu()), dict(ids=ids[::2]),
+                dict(params=params[:-1]), dict(params=params.bfloat16()), dict(out=torch.zeros(4, 9, device=DEV)),
+                dict(out=torch.zeros(3, 10, device=DEV)), dict(scale=float("nan")), dict(scale=float("inf"))]:
+        with pytest.raises(OneBitError):
+            look(**bad)
+    grad = lambda **k: opt.embedding_grad(**{**dict(worker=0, tensor=0, dim=10, ids=ids, dy=small, grads=grads), **k})   # noqa: E731
+    for bad in [dict(worker=2), dict(tensor=-1), dict(dim=7), dict(dy=torch.zeros(4, 9, device=DEV)), dict(scale=float("nan")),
+                dict(grads=grads.bfloat16()), dict(work=torch.empty(16, dtype=torch.uint8, device=DEV))]:
+        with pytest.raises(OneBitError):
+            grad(**bad)
+    for bad in [lambda: ck.save(small, act="relu", y=small), lambda: ck.save(small, act="gelu"), lambda: ck.save(small, y=small),
+                lambda: ck.save(small, act="gelu", y=small.bfloat16()), lambda: ck.save(small.half()),
+                lambda: ck.load(torch.zeros(4, 11, device=DEV)), lambda: ck.act_backward("none", small, small),
+                lambda: ck.act_backward("gelu", small, small.bfloat16()),
+                lambda: ck.load(torch.zeros(10, device=DEV).expand(4, 10)),
+                lambda: ActCheckpoint(4, 10, codes=ck.codes[:3], scales=ck.scales)]:
+        with pytest.raises(OneBitError):
+            bad()
+    torch.cuda.synchronize()
+    assert (grads == 3.0).all() and (small == 0).all()
+
+
+def _chain(opt, ck, ids, x, y, dy, out, params, grads, work):
+    """Every operator once."""
+    opt.embedding_lookup(0, 48, ids, params, out, scale=2.0)
+    ck.save(x, act="gelu", y=y)
+    ck.act_backward("gelu", y, y)
+    opt.linear_grad(0, 1, 2, ck, dy, grads, work=work[0])
+    opt.embedding_grad(0, 0, 48, ids, out, grads, scale=2.0, work=work[1])
+
+
+def _chain_state(seed, rows=700):
+    opt = OneBitAdam([60 * 48, 80 * 48, 80], 1)
+    s = dict(opt=opt, ck=ActCheckpoint(rows, 48, "e4m3", device=DEV), ids=_ids(rows, 60, seed).clamp_max(59).to(DEV),
+             x=torch.randn(rows, 48, generator=_gen(seed)).to(DEV), y=torch.zeros(rows, 48, device=DEV),
+             dy=torch.randn(rows, 80, generator=_gen(seed + 1)).bfloat16().to(DEV), out=torch.zeros(rows, 48, device=DEV),
+             params=torch.randn(opt.N, generator=_gen(seed + 2)).to(DEV), grads=torch.zeros(1, opt.N, device=DEV))
+    s["work"] = [torch.empty(max(16, n), dtype=torch.uint8, device=DEV)
+                 for n in (opt.linear_grad_work(rows, 80, 48), opt.embedding_grad_work(rows, 48))]
+    return s
+
+
+def _results(s):
+    return [s[k].clone() for k in ("y", "out", "grads")] + [s["ck"].codes.clone(), s["ck"].scales.clone()]
+
+
+def _renew(s, seed):
+    rows = s["x"].shape[0]
+    s["x"].copy_(torch.randn(rows, 48, generator=_gen(seed)))
+    s["dy"].copy_(torch.randn(rows, 80, generator=_gen(seed + 1)))
+    s["ids"].copy_(_ids(rows, 60, seed).clamp_max(59))
+
+
+def test_side_streams():
+    """Two chains on two streams at once give what each gives alone."""
+    states = [_chain_state(30), _chain_state(40, rows=901)]
+    want = []
+    for s in states:
+        _chain(**s)
+        torch.cuda.synchronize()
+        want.append(_results(s))
+    for s in states:
+        for k in ("y", "out", "grads"):
+            s[k].zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, st in zip(states, streams):
+            with torch.cuda.stream(st):
+                _chain(**s)
+    torch.cuda.synchronize()
+    for s, w in zip(states, want):
+        assert all(torch.equal(a, b) for a, b in zip(_results(s), w))
+
+
+def test_stream_argument():
+    s = _chain_state(50)
+    _chain(**s)
+    torch.cuda.synchronize()
+    want = _results(s)
+    s["grads"].zero_()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    s["opt"].linear_grad(0, 1, 2, s["ck"], s["dy"], s["grads"], stream=st)
+    s["opt"].embedding_grad(0, 0, 48, s["ids"], s["out"], s["grads"], scale=2.0, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(s["grads"], want[2])
+
+
+def test_graphs_replay():
+    """Two captured chains that share one workspace, replayed in turn with new
+    inputs and eager work between, against the eager results."""
+    a, b = _chain_state(60), _chain_state(70)
+    b["work"] = a["work"]
+    for s in (a, b):
+        _chain(**s)
+    torch.cuda.synchronize()
+    graphs = []
+    for s in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _chain(**s)
+        graphs.append(g)
+    for k in range(4):
+        want = []
+        for s in (a, b):
+            _renew(s, 100 + 10 * k)
+            _chain(**s)
+            torch.cuda.synchronize()
+            want.append(_results(s))
+            for key in ("y", "out", "grads"):
+                s[key].fill_(9.0)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for s, w in zip((a, b), want):
+            got = _results(s)
+            got[2][0, :] = torch.where(got[2][0] == 9.0, w[2][0], got[2][0])     # padding keeps the fill
+            assert all(torch.equal(x, y) for x, y in zip(got, w)), k
+
+
+# ---------------------------------------------------------------------------
+# all together
+# ---------------------------------------------------------------------------
+def test_training_step_from_lookup_to_update():
+    """Two workers, a two-layer model: lookup, linear, gelu, linear, with its
+    hidden activations kept in 8 bits; the gradient rows against the formulas in
+    64 bits, then one compression step on them against the oracle."""
+    import oracle.onebit as ob
+    vocab, dim, hid, out, tokens, W = 50, 40, 72, 24, 333, 2
+    sizes = [vocab * dim, hid * dim, hid, out * hid, out]
+    opt = OneBitAdam(sizes, W)
+    off = opt.offsets
+    params = (torch.randn(opt.N, generator=_gen(80)) * 0.3).to(DEV)
+    grads = torch.zeros(W, opt.N, device=DEV)
+    part = lambda buf, t, shape: buf[off[t]: off[t] + sizes[t]].view(shape)   # noqa: E731
+    w1, b1, w2, b2 = part(params, 1, (hid, dim)), part(params, 2, (hid,)), part(params, 3, (out, hid)), part(params, 4, (out,))
+    for w in range(W):
+        ids = _ids(tokens, vocab, 81 + w, pad=0.05).clamp_max(vocab - 1).to(DEV)
+        x = torch.empty(tokens, dim, device=DEV)
+        opt.embedding_lookup(0, dim, ids, params, x, scale=1.5)
+        cx, ch, cy = (ActCheckpoint(tokens, n, "int8", device=DEV) for n in (dim, hid, hid))
+        cx.save(x)
+        h = x @ w1.t() + b1
+        y = torch.empty_like(h)
+        ch.save(h, act="gelu", y=y)
+        cy.save(y)
+        dz = torch.randn(tokens, out, generator=_gen(90 + w)).to(DEV)     # the loss's gradient
+        opt.linear_grad(w, 3, 4, cy, dz, grads)
+        dy = dz @ w2
+        dh = torch.empty_like(dy)
+        ch.act_backward("gelu", dy, dh)
+        opt.linear_grad(w, 1, 2, cx, dh, grads)
+        dx = dh @ w1
+        opt.embedding_grad(w, 0, dim, ids, dx, grads, scale=1.5)
+        torch.cuda.synchronize()
+        # the formulas in 64 bits, from the kept values
+        values = lambda c: ref.decoded(c.codes.cpu().numpy(), c.scales.cpu().numpy(), c.cols, "int8")   # noqa: E731
+        dz64 = _f64(dz)
+        dh64 = (dz64 @ _f64(w2)) * ref.act_slope(values(ch), "gelu")
+        emb, _, _ = ref.embedding_grad(ids.cpu().numpy(), dh64 @ _f64(w1), vocab)
+        want = [1.5 * emb, dh64.T @ values(cx), dh64.sum(0), dz64.T @ values(cy), dz64.sum(0)]
+        for t, v in enumerate(want):
+            got = _f64(grads[w, off[t]: off[t] + sizes[t]]).reshape(v.shape)
+            # 333 tokens and inner sums of at most 72 terms: a few hundred roundings of 2^-24
+            assert np.abs(got - v).max() <= 1e-4 * np.abs(v).max(), t
+    m, v = torch.zeros(opt.N, device=DEV), torch.full((opt.N,), 1e-4, device=DEV)
+    err_w, err_s = torch.zeros(W, opt.N, device=DEV), torch.zeros(opt.N, device=DEV)
+    bufs = opt.alloc(DEV)
+    before = params.cpu().numpy().copy()
+    opt.step(grads, m, v, params, err_w, err_s, bufs["packed_w"], bufs["scale_w"], bufs["packed_s"], bufs["scale_s"], 1e-3)
+    torch.cuda.synchronize()
+    for t, n in enumerate(sizes):
+        s = slice(off[t], off[t] + n)
+        z = np.zeros(n, np.float32)
+        st = ob.TensorState(before[s], z, np.full(n, 1e-4, np.float32), z, np.zeros((W, n), np.float32))
+        res = ob.compression_step(st, grads[:, s].cpu().numpy(), 0.9, 1e-3, 1e-8)
+        assert np.abs(params[s].cpu().numpy() - res.state.p).max() <= 1e-6
