@@ -64,23 +64,83 @@ __device__ __forceinline__ void split3(float x, uint32_t &h, uint32_t &m, uint32
   l = __float_as_uint(r2) >> 16;
 }
 
-// BM x BN tile of dW, 4 wavefronts 2 x 2, BK tokens a turn.  PARTS: bf16 parts
+// Writes a wavefront's results: to `part`, a matrix of its own, or rounded
+// into the gradient.  Lane: weight row lane % 16 of a fragment, four
+// consecutive columns.
+template <int BM, int BN, int WM, int WN, int FO, int FI>
+__device__ __forceinline__ void store_tile(const LinearArgs &a, const f32x4 (&acc)[FI][FO], int64_t m0, int64_t n0, int wm,
+                                           int wn, float *part) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
+  const bool quad = a.in % 4 == 0;
+#pragma unroll
+  for (int o = 0; o < FO; ++o) {
+    const int64_t row = m0 + (wm * FO + o) * 16 + li;
+    if (row >= a.out) continue;
+#pragma unroll
+    for (int i = 0; i < FI; ++i) {
+      const int64_t col = n0 + (wn * FI + i) * 16 + g * 4;
+      if (col >= a.in) continue;
+      const int64_t at = row * a.in + col;
+      f32x4 v = acc[i][o];
+      if (part) {
+        float *p = part + at;
+        if (quad) {
+          *reinterpret_cast<f32x4 *>(p) = v;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (col + k < a.in) p[k] = v[k];
+        }
+      } else if (a.grad_bf16) {
+        uint16_t *p = static_cast<uint16_t *>(a.dw) + at;
+        uint16_t r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (col + k < a.in) {
+            if (a.accumulate) v[k] += __uint_as_float(static_cast<uint32_t>(p[k]) << 16);
+            r[k] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[k]));
+          }
+        }
+        if (quad) {
+          __builtin_memcpy(__builtin_assume_aligned(p, 8), r, 8);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (col + k < a.in) p[k] = r[k];
+        }
+      } else {
+        float *p = static_cast<float *>(a.dw) + at;
+        if (quad) {
+          if (a.accumulate) v += *reinterpret_cast<const f32x4 *>(p);
+          *reinterpret_cast<f32x4 *>(p) = v;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (col + k < a.in) p[k] = a.accumulate ? p[k] + v[k] : v[k];
+        }
+      }
+    }
+  }
+}
+
+// BM x BN tile of dW, WM x WN wavefronts, BK tokens a turn.  PARTS: bf16 parts
 // of dY (1: bf16, 3: fp32).  VEC: 16-byte loads of dY (its rows start on 16
 // bytes and a turn's rows lie within 2 GB).
-template <int BM, int BN, int BK, int PARTS, int FMT, bool VEC>
-__global__ __launch_bounds__(256) void linear_grad_kernel(const LinearArgs a, int m_tiles, int n_tiles,
+template <int BM, int BN, int BK, int WM, int WN, int PARTS, int FMT, bool VEC>
+__global__ __launch_bounds__(64 * WM * WN) void linear_grad_kernel(const LinearArgs a, int m_tiles, int n_tiles,
                                                           int64_t turns_each, float *part) {
-  constexpr int FO = BM / 32, FI = BN / 32;          // 16-wide fragments of a wavefront
+  constexpr int NT = 64 * WM * WN;
+  constexpr int FO = BM / WM / 16, FI = BN / WN / 16;   // 16-wide fragments of a wavefront
   constexpr int A_BYTES = BK * BM * 2, B_BYTES = BK * BN, S_BYTES = BK / 32 * BN;
   constexpr int STAGE = PARTS * A_BYTES + B_BYTES + S_BYTES;
-  constexpr int CA = BM / 8, RA = 256 / CA, JA = BK / RA;     // dY: 8-element chunks a row, rows a step, steps
-  constexpr int CB = BN / 16, RB = 256 / CB, JB = BK / RB;    // codes: 16-byte chunks
-  constexpr int JS = (S_BYTES + 255) / 256;
+  constexpr int CA = BM / 8, RA = NT / CA, JA = BK / RA;     // dY: 8-element chunks a row, rows a step, steps
+  constexpr int CB = BN / 16, RB = NT / CB, JB = BK / RB;    // codes: 16-byte chunks
+  constexpr int JS = (S_BYTES + NT - 1) / NT;
   static_assert(JA >= 1 && JB >= 1 && BK % RA == 0 && BK % RB == 0, "tile too small");
   __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
   const int tile = blockIdx.x;
   const int nt = tile % n_tiles, mt = tile / n_tiles;
   const int64_t m0 = static_cast<int64_t>(mt) * BM, n0 = static_cast<int64_t>(nt) * BN;
@@ -141,7 +201,7 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(const LinearArgs a, in
     const auto srsrc = rest(a.scales, t0 / kActBlock * a.pitch + n0, act_blocks(a.rows) * a.pitch);
 #pragma unroll
     for (int j = 0; j < JS; ++j) {
-      const int at = tid + 256 * j;
+      const int at = tid + NT * j;
       rs[j] = at >= S_BYTES ? 0u : __builtin_amdgcn_raw_buffer_load_b8(srsrc, static_cast<int>(at / BN * a.pitch) + at % BN, 0, 0);
     }
   };
@@ -177,7 +237,7 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(const LinearArgs a, in
     // scales: [block][column % 16][column / 16], so a lane's fragments are adjacent
 #pragma unroll
     for (int j = 0; j < JS; ++j) {
-      const int at = tid + 256 * j, col = at % BN;
+      const int at = tid + NT * j, col = at % BN;
       if (at < S_BYTES) S[at / BN * BN + (col & 15) * (BN / 16) + (col >> 4)] = static_cast<unsigned char>(rs[j]);
     }
   };
@@ -186,107 +246,278 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(const LinearArgs a, in
   const int a_row = 8 * g + (li >> 2), a_sw = (li >> 2) | (g & 1) << 2;
   const int b_row = 8 * g + (li >> 1), b_sw = swizzle_b<BN>(b_row);
 
-  auto compute = [&](int buf) {
+  // One 32-token step: its operands as they come from LDS, and its products.
+  struct Step {
+    uint32_t s[FI / 4];
+    i32x2 c[FI];
+    s16x4 y[PARTS][FO][2];
+  };
+  auto fetch = [&](int buf, int kk, Step &f) {
     const unsigned char *A = lds + buf * STAGE, *B = A + PARTS * A_BYTES, *S = B + B_BYTES;
 #pragma unroll
-    for (int kk = 0; kk < BK / 32; ++kk) {
-      bf16x8 x[FI];
-      uint32_t sw[FI / 4];
+    for (int q = 0; q < FI / 4; ++q)
+      f.s[q] = *reinterpret_cast<const uint32_t *>(S + kk * BN + li * (BN / 16) + wn * FI + 4 * q);
 #pragma unroll
-      for (int q = 0; q < FI / 4; ++q)
-        sw[q] = *reinterpret_cast<const uint32_t *>(S + kk * BN + li * (BN / 16) + wn * FI + 4 * q);
+    for (int i = 0; i < FI; ++i) {
+      const int unit = (wn * FI + i) ^ b_sw;
+      f.c[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((OB_LDS i32x2 *)(B + (kk * 32 + b_row) * BN + (unit << 4) + (li & 1) * 8));
+    }
 #pragma unroll
-      for (int i = 0; i < FI; ++i) {
-        const int unit = (wn * FI + i) ^ b_sw;
-        const auto *p = B + (kk * 32 + b_row) * BN + (unit << 4) + (li & 1) * 8;
-        const i32x2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((OB_LDS i32x2 *)(p));
-        const float scale = act_scale_value((sw[i >> 2] >> (8 * (i & 3))) & 0xffu);
-        const bf16x2 d[4] = {act_decode2<FMT, false>(c[0], scale), act_decode2<FMT, true>(c[0], scale),
-                             act_decode2<FMT, false>(c[1], scale), act_decode2<FMT, true>(c[1], scale)};
+    for (int q = 0; q < PARTS; ++q) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[i][k] = d[k >> 1][k & 1];
+      for (int o = 0; o < FO; ++o) {
+        const int unit = (wm * FO + o) ^ a_sw;
+        const auto *p = A + q * A_BYTES + (kk * 32 + a_row) * (BM * 2) + (unit << 5) + (li & 3) * 8;
+        f.y[q][o][0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p));
+        f.y[q][o][1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p + 4 * BM * 2));
       }
+    }
+  };
+  auto multiply = [&](const Step &f) {
+    bf16x8 x[FI];
 #pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
+    for (int i = 0; i < FI; ++i) {
+      const float scale = act_scale_value((f.s[i >> 2] >> (8 * (i & 3))) & 0xffu);
+      const bf16x2 d[4] = {act_decode2<FMT, false>(f.c[i][0], scale), act_decode2<FMT, true>(f.c[i][0], scale),
+                           act_decode2<FMT, false>(f.c[i][1], scale), act_decode2<FMT, true>(f.c[i][1], scale)};
 #pragma unroll
-        for (int o = 0; o < FO; ++o) {
-          const int unit = (wm * FO + o) ^ a_sw;
-          const auto *p = A + q * A_BYTES + (kk * 32 + a_row) * (BM * 2) + (unit << 5) + (li & 3) * 8;
-          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p));
-          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p + 4 * BM * 2));
-          const bf16x8 y = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      for (int k = 0; k < 8; ++k) x[i][k] = d[k >> 1][k & 1];
+    }
 #pragma unroll
-          for (int i = 0; i < FI; ++i) acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y, acc[i][o], 0, 0, 0);
-        }
+    for (int q = 0; q < PARTS; ++q) {
+#pragma unroll
+      for (int o = 0; o < FO; ++o) {
+        const bf16x8 y = __builtin_bit_cast(bf16x8, __builtin_shufflevector(f.y[q][o][0], f.y[q][o][1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int i = 0; i < FI; ++i) acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y, acc[i][o], 0, 0, 0);
       }
     }
   };
 
+  // Each step's operands are read one step ahead.  Per turn one barrier, in
+  // its last step: behind it the turn's reads are done everywhere and the next
+  // turn's tile is in LDS.
+  constexpr int KK = BK / 32, UNROLL = KK == 1 ? 2 : 1;
   if (turns > 0) {
+    Step f[2];
     load(0);
     store(0);
     if (turns > 1) load(1);
     __syncthreads();
-    for (int64_t it = 0; it < turns; ++it) {
-      // the other buffer's readers are behind the barrier: fill it, start the loads after next
-      if (it + 1 < turns) store((it + 1) & 1);
-      if (it + 2 < turns) load(it + 2);
-      compute(it & 1);
-      __syncthreads();
-    }
-  }
-
-  // lane: weight row o = lane % 16 of a fragment, four consecutive columns
-  const bool quad = a.in % 4 == 0;
+    fetch(0, 0, f[0]);
+    for (int64_t it = 0; it < turns; it += UNROLL) {
 #pragma unroll
-  for (int o = 0; o < FO; ++o) {
-    const int64_t row = m0 + (wm * FO + o) * 16 + li;
-    if (row >= a.out) continue;
+      for (int u = 0; u < UNROLL; ++u) {
+        const int64_t t = it + u;
+        if (t >= turns) break;
+        const int buf = static_cast<int>(t & 1);
 #pragma unroll
-    for (int i = 0; i < FI; ++i) {
-      const int64_t col = n0 + (wn * FI + i) * 16 + g * 4;
-      if (col >= a.in) continue;
-      const int64_t at = row * a.in + col;
-      f32x4 v = acc[i][o];
-      if (part) {
-        float *p = part + static_cast<int64_t>(blockIdx.y) * a.out * a.in + at;
-        if (quad) {
-          *reinterpret_cast<f32x4 *>(p) = v;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (col + k < a.in) p[k] = v[k];
-        }
-      } else if (a.grad_bf16) {
-        uint16_t *p = static_cast<uint16_t *>(a.dw) + at;
-        uint16_t r[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (col + k < a.in) {
-            if (a.accumulate) v[k] += __uint_as_float(static_cast<uint32_t>(p[k]) << 16);
-            r[k] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[k]));
+        for (int kk = 0; kk < KK; ++kk) {
+          constexpr int kBar = 0;
+          const int cur = (u * KK + kk) & 1;
+          if (kk + 1 < KK) fetch(buf, kk + 1, f[cur ^ 1]);
+          if (kk == 0) {
+            if (t + 1 < turns) store(buf ^ 1);
+            if (t + 2 < turns) load(t + 2);
           }
-        }
-        if (quad) {
-          __builtin_memcpy(__builtin_assume_aligned(p, 8), r, 8);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (col + k < a.in) p[k] = r[k];
-        }
-      } else {
-        float *p = static_cast<float *>(a.dw) + at;
-        if (quad) {
-          if (a.accumulate) v += *reinterpret_cast<const f32x4 *>(p);
-          *reinterpret_cast<f32x4 *>(p) = v;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (col + k < a.in) p[k] = a.accumulate ? p[k] + v[k] : v[k];
+          if (kk + 1 == KK) {
+            __syncthreads();
+            if (t + 1 < turns) fetch(buf ^ 1, 0, f[cur ^ 1]);
+          }
+          __builtin_amdgcn_sched_barrier(kBar);
+          multiply(f[cur]);
+          __builtin_amdgcn_sched_barrier(kBar);
         }
       }
     }
   }
+
+  store_tile<BM, BN, WM, WN, FO, FI>(a, acc, m0, n0, wm, wn, part ? part + blockIdx.y * a.out * a.in : nullptr);
+}
+
+// ---------------------------------------------------------------------------
+// The large tile: bf16 dY whose rows start on 16 bytes.
+// ---------------------------------------------------------------------------
+#define OB_WAIT_VM(n) asm volatile("s_waitcnt vmcnt(" #n ")" ::: "memory")
+
+// Starts the copy of 16 bytes a lane, from its own offset, to 1 KB of LDS in
+// lane order.
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t from, OB_LDS unsigned char *to, int offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (OB_LDS void *)to, 16, offset, 0, 0, 0);
+}
+
+// A workgroup's place: consecutive workgroups go to the 8 XCDs in turn, so
+// the tiles are numbered such that each XCD (its own L2) gets a consecutive
+// range: one slice of the contraction where there are several, and within it
+// kGroup tiles along dY's columns times a run along X's, the shape that needs
+// the fewest bytes of both (dY has two bytes an element, X one).
+constexpr int kXcds = 8, kGroup = 4;
+struct Where {
+  int mt, nt, split;
+};
+__device__ __forceinline__ Where where(int m_tiles, int n_tiles, int splits) {
+  const uint32_t tiles = static_cast<uint32_t>(m_tiles) * n_tiles, total = tiles * splits;
+  const uint32_t id = blockIdx.x, xcd = id % kXcds, at = id / kXcds;
+  const uint32_t each = total / kXcds, more = total % kXcds;
+  const uint32_t lin = xcd * each + min(xcd, more) + at;
+  const uint32_t split = lin / tiles, t = lin - split * tiles;
+  const uint32_t band = t / (kGroup * n_tiles), in_band = t - band * kGroup * n_tiles;
+  const uint32_t high = min(static_cast<uint32_t>(kGroup), m_tiles - band * kGroup);
+  return Where{static_cast<int>(band * kGroup + in_band % high), static_cast<int>(in_band / high), static_cast<int>(split)};
+}
+
+template <int BM, int BN, int WM, int WN, int FMT>
+__global__ __launch_bounds__(64 * WM * WN) void linear_grad_wide_kernel(const LinearArgs a, int m_tiles, int n_tiles,
+                                                                       int splits, int64_t turns_each, float *part) {
+  constexpr int BK = 64, NW = WM * WN, NT = 64 * NW;
+  constexpr int FO = BM / WM / 16, FI = BN / WN / 16;
+  constexpr int A_BYTES = BK * BM * 2, B_BYTES = BK * BN, S_BYTES = 2 * BN;
+  constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
+  constexpr int JA = A_BYTES / 1024 / NW, JB = B_BYTES / 1024 / NW;   // 1 KB copies a wavefront makes each turn
+  constexpr int RA = 512 / BM, RB = 1024 / BN;                        // rows of one copy
+  static_assert(S_BYTES <= NT && FI % 4 == 0 && JA * NW * 1024 == A_BYTES && JB * NW * 1024 == B_BYTES, "tile shape");
+  static_assert(1 + JA + JB == 7, "the waits below count a turn's loads");
+  __shared__ __attribute__((aligned(1024))) unsigned char shared[3 * STAGE];
+  OB_LDS unsigned char *const lds = (OB_LDS unsigned char *)shared;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const Where at = where(m_tiles, n_tiles, splits);
+  const int64_t m0 = static_cast<int64_t>(at.mt) * BM, n0 = static_cast<int64_t>(at.nt) * BN;
+  const int64_t turn0 = at.split * turns_each;
+  const int turns = static_cast<int>(max(int64_t{0}, min(turns_each, (a.rows + BK - 1) / BK - turn0)));
+
+  f32x4 acc[FI][FO];
+#pragma unroll
+  for (int i = 0; i < FI; ++i)
+#pragma unroll
+    for (int o = 0; o < FO; ++o) acc[i][o] = f32x4{0, 0, 0, 0};
+
+  // where this lane's 16 bytes of each copy come from (the swizzle is applied
+  // to the source: the copies write LDS in order)
+  int from_a[JA], from_b[JB];
+#pragma unroll
+  for (int j = 0; j < JA; ++j) {
+    const int r = (wave * JA + j) * RA + lane / (BM / 8), c = lane % (BM / 8);
+    from_a[j] = static_cast<int>(r * a.lddy) * 2 + (((c >> 1) ^ swizzle_a(r)) << 5) + (c & 1) * 16;
+  }
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    const int r = (wave * JB + j) * RB + lane / (BN / 16), c = lane % (BN / 16);
+    from_b[j] = static_cast<int>(r * a.pitch) + ((c ^ swizzle_b<BN>(r)) << 4);
+  }
+  const int from_s = tid < S_BYTES ? static_cast<int>(tid / BN * a.pitch) + tid % BN : 0;
+  const int to_s = tid / BN * BN + (tid % BN & 15) * (BN / 16) + (tid % BN >> 4);
+  const int64_t dy_bytes = ((a.rows - 1) * a.lddy + a.out) * 2, code_bytes = a.rows * a.pitch,
+                scale_bytes = act_blocks(a.rows) * a.pitch;
+
+  // The loads of a turn; a turn past the last reads nothing and fills zeros.
+  auto load_scale = [&](int turn) -> uint32_t {
+    const int64_t t0 = (turn0 + turn) * BK;
+    const auto r = rest(a.scales, turn < turns ? t0 / kActBlock * a.pitch + n0 : scale_bytes, scale_bytes);
+    return __builtin_amdgcn_raw_buffer_load_b8(r, from_s, 0, 0);
+  };
+  auto copy = [&](int turn, OB_LDS unsigned char *dst) {
+    const int64_t t0 = (turn0 + turn) * BK;
+    const auto ra = rest(a.dy, turn < turns ? (t0 * a.lddy + m0) * 2 : (dy_bytes + 15) / 16 * 16, dy_bytes);
+    const auto rb = rest(a.codes, turn < turns ? t0 * a.pitch + n0 : code_bytes, code_bytes);
+#pragma unroll
+    for (int j = 0; j < JA; ++j)
+      copy16(ra, dst + (wave * JA + j) * 1024, from_a[j]);
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+      copy16(rb, dst + A_BYTES + (wave * JB + j) * 1024, from_b[j]);
+  };
+
+  const int g = lane >> 4, li = lane & 15;
+  const int a_row = 8 * g + (li >> 2), a_sw = (li >> 2) | (g & 1) << 2;
+  const int b_row = 8 * g + (li >> 1), b_sw = swizzle_b<BN>(b_row);
+
+  struct Step {
+    uint32_t s[FI / 4];
+    i32x2 c[FI];
+    s16x4 y[FO][2];
+  };
+  auto fetch = [&](OB_LDS const unsigned char *A, int kk, Step &f) {
+    OB_LDS const unsigned char *B = A + A_BYTES, *S = B + B_BYTES;
+#pragma unroll
+    for (int q = 0; q < FI / 4; ++q)
+      f.s[q] = *(OB_LDS const uint32_t *)(S + kk * BN + li * (BN / 16) + wn * FI + 4 * q);
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+      f.c[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+          (OB_LDS i32x2 *)(B + (kk * 32 + b_row) * BN + (((wn * FI + i) ^ b_sw) << 4) + (li & 1) * 8));
+#pragma unroll
+    for (int o = 0; o < FO; ++o) {
+      OB_LDS const unsigned char *p = A + (kk * 32 + a_row) * (BM * 2) + (((wm * FO + o) ^ a_sw) << 5) + (li & 3) * 8;
+      f.y[o][0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p));
+      f.y[o][1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p + 4 * BM * 2));
+    }
+  };
+  auto multiply = [&](const Step &f) {
+#pragma unroll
+    for (int i = 0; i < FI; ++i) {
+      const float scale = act_scale_value((f.s[i >> 2] >> (8 * (i & 3))) & 0xffu);
+      const bf16x2 d[4] = {act_decode2<FMT, false>(f.c[i][0], scale), act_decode2<FMT, true>(f.c[i][0], scale),
+                           act_decode2<FMT, false>(f.c[i][1], scale), act_decode2<FMT, true>(f.c[i][1], scale)};
+      bf16x8 x;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = d[k >> 1][k & 1];
+#pragma unroll
+      for (int o = 0; o < FO; ++o) {
+        const bf16x8 y = __builtin_bit_cast(bf16x8, __builtin_shufflevector(f.y[o][0], f.y[o][1], 0, 1, 2, 3, 4, 5, 6, 7));
+        acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, acc[i][o], 0, 0, 0);
+      }
+    }
+  };
+
+  Step f0, f1;
+  uint32_t s_reg;
+  // One turn on tile `cur`, tile t + 1 lying in `next`, tile t + 2 being
+  // copied to `dst`: three different stages, which __restrict says, so that
+  // the compiler does not hold the reads back for the copies; the waits and
+  // the barrier in the middle are what orders them.
+  auto turn = [&](int t, OB_LDS unsigned char *__restrict dst, OB_LDS unsigned char *__restrict cur,
+                  OB_LDS unsigned char *__restrict next) __attribute__((always_inline)) {
+    fetch(cur, 1, f1);
+    if (S_BYTES == NT || tid < S_BYTES) next[A_BYTES + B_BYTES + to_s] = static_cast<unsigned char>(s_reg);
+    s_reg = load_scale(t + 2);
+    copy(t + 2, dst);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(f0);
+    __builtin_amdgcn_sched_barrier(0);
+    // tile t + 1 has landed once only this turn's 7 loads are out; this
+    // wavefront's reads of tile t are back
+    asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    fetch(next, 0, f0);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(f1);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  if (turns > 0) {
+    const uint32_t s0 = load_scale(0);
+    copy(0, lds);
+    s_reg = load_scale(1);
+    copy(1, lds + STAGE);
+    if (S_BYTES == NT || tid < S_BYTES) lds[A_BYTES + B_BYTES + to_s] = static_cast<unsigned char>(s0);
+    asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    fetch(lds, 0, f0);
+    OB_LDS unsigned char *cur = lds, *next = lds + STAGE, *dst = lds + 2 * STAGE;
+    for (int t = 0; t < turns; ++t) {
+      turn(t, dst, cur, next);
+      OB_LDS unsigned char *const was = cur;
+      cur = next;
+      next = dst;
+      dst = was;
+    }
+    OB_WAIT_VM(0);   // no copy may land after the workgroup has ended
+  }
+  store_tile<BM, BN, WM, WN, FO, FI>(a, acc, m0, n0, wm, wn, part ? part + at.split * a.out * a.in : nullptr);
 }
 
 // Column sums of dY over slices of rows: lane per column, the four wavefronts
@@ -355,7 +586,7 @@ struct Plan {
 
 Plan plan_of(int64_t rows, int64_t out, int64_t in, bool dy_bf16, bool bias) {
   Plan p{};
-  p.bm = p.bn = 128;
+  p.bm = p.bn = dy_bf16 && ((out + 255) / 256) * ((in + 255) / 256) >= 128 ? 256 : 128;
   p.bk = dy_bf16 ? 64 : 32;
   p.m_tiles = static_cast<int>((out + p.bm - 1) / p.bm);
   p.n_tiles = static_cast<int>((in + p.bn - 1) / p.bn);
@@ -375,7 +606,7 @@ Plan plan_of(int64_t rows, int64_t out, int64_t in, bool dy_bf16, bool bias) {
 
 Plan plan_of(const LinearArgs &a) { return plan_of(a.rows, a.out, a.in, a.dy_bf16, a.db != nullptr); }
 
-template <int BM, int BN, int BK, int PARTS>
+template <int BM, int BN, int BK, int WM, int WN, int PARTS>
 void linear_one(const LinearArgs &a, const Plan &p, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.m_tiles) * p.n_tiles, p.splits);
   float *part = p.splits > 1 ? static_cast<float *>(a.work) : nullptr;
@@ -383,12 +614,22 @@ void linear_one(const LinearArgs &a, const Plan &p, hipStream_t s) {
   const bool vec = reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && a.lddy * size % 16 == 0 &&
                    (a.lddy * BK + a.out) * size < 0x7fffffff;
   if (a.fmt == kE4M3) {
-    if (vec) linear_grad_kernel<BM, BN, BK, PARTS, kE4M3, true><<<grid, 256, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
-    else linear_grad_kernel<BM, BN, BK, PARTS, kE4M3, false><<<grid, 256, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
+    if (vec) linear_grad_kernel<BM, BN, BK, WM, WN, PARTS, kE4M3, true><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
+    else linear_grad_kernel<BM, BN, BK, WM, WN, PARTS, kE4M3, false><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
   } else {
-    if (vec) linear_grad_kernel<BM, BN, BK, PARTS, kInt8, true><<<grid, 256, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
-    else linear_grad_kernel<BM, BN, BK, PARTS, kInt8, false><<<grid, 256, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
+    if (vec) linear_grad_kernel<BM, BN, BK, WM, WN, PARTS, kInt8, true><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
+    else linear_grad_kernel<BM, BN, BK, WM, WN, PARTS, kInt8, false><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
   }
+}
+
+template <int BM, int BN, int WM, int WN>
+void linear_wide(const LinearArgs &a, const Plan &p, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.m_tiles) * p.n_tiles * p.splits);
+  float *part = p.splits > 1 ? static_cast<float *>(a.work) : nullptr;
+  if (a.fmt == kE4M3)
+    linear_grad_wide_kernel<BM, BN, WM, WN, kE4M3><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.splits, p.turns_each, part);
+  else
+    linear_grad_wide_kernel<BM, BN, WM, WN, kInt8><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.splits, p.turns_each, part);
 }
 
 }  // namespace
@@ -406,8 +647,9 @@ size_t linear_work_bytes(int64_t rows, int64_t out, int64_t in, bool dy_bf16, bo
 
 void launch_linear_grad(const LinearArgs &a, hipStream_t s) {
   const Plan p = plan_of(a);
-  if (a.dy_bf16) linear_one<128, 128, 64, 1>(a, p, s);
-  else linear_one<128, 128, 32, 3>(a, p, s);
+  if (a.dy_bf16 && p.bm == 256) linear_wide<256, 256, 4, 2>(a, p, s);
+  else if (a.dy_bf16) linear_one<128, 128, 64, 2, 2, 1>(a, p, s);
+  else linear_one<128, 128, 32, 2, 2, 3>(a, p, s);
   if (a.db) {
     float *part = reinterpret_cast<float *>(static_cast<char *>(a.work) + p.weight_bytes);
     const dim3 grid(static_cast<unsigned>((a.out + 63) / 64), p.bias_slices);
