@@ -20,6 +20,8 @@
 #include "internal.h"
 #include "activation.h"
 
+#include <algorithm>
+
 #pragma clang fp contract(off)
 
 namespace ob {
@@ -41,16 +43,13 @@ __device__ __forceinline__ int swizzle_b(int r) {
   return BN >= 256 ? ((r & 7) | ((r >> 3) & 1) << 3) : (r & 7);
 }
 
-// A buffer over what is left of a matrix from byte0 on: reads past its end
-// give 0, which is what the missing tokens contribute.  The end is rounded up
-// to the 16 bytes that one load takes (all loads start on 16 bytes, so such a
-// load stays within memory that the matrix's last element lies in; what it
-// reads there belongs to columns that are dropped).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rest(const void *base, int64_t byte0, int64_t bytes) {
-  int64_t left = (bytes + 15) / 16 * 16 - byte0;
-  left = left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : left;
-  return __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<char *>(static_cast<const char *>(base) + (left ? byte0 : 0)), 0, static_cast<int>(left), 0x00020000);
+// A buffer of `bytes` from `base` on: reads past its end give 0, which is what
+// missing tokens contribute.  Its end is rounded up to the 16 bytes that one
+// load takes (all loads start on 16 bytes, so such a load stays within memory
+// that the matrix's last element lies in; what it reads there belongs to
+// columns that are dropped).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (bytes + 15) & ~15, 0x00020000);
 }
 
 // An fp32 value as three bf16 parts (truncated, so no part overflows).
@@ -62,6 +61,44 @@ __device__ __forceinline__ void split3(float x, uint32_t &h, uint32_t &m, uint32
   m = b1 >> 16;
   const float r2 = r1 - __uint_as_float(b1 & 0xffff0000u);
   l = __float_as_uint(r2) >> 16;
+}
+
+// Start the copy of 16 or 4 bytes a lane, from its own offset, to LDS in lane
+// order.
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t from, OB_LDS unsigned char *to, int offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (OB_LDS void *)to, 16, offset, 0, 0, 0);
+}
+
+__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t from, OB_LDS unsigned char *to, int offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (OB_LDS void *)to, 4, offset, 0, 0, 0);
+}
+
+// A workgroup's place: consecutive workgroups go to the 8 XCDs in turn, so
+// the tiles are numbered such that each XCD (its own L2) gets a consecutive
+// range: one slice of the contraction where there are several, and within it
+// kGroup tiles along dY's columns times a run along X's, the shape that needs
+// the fewest bytes of both (dY has two bytes an element, X one).
+constexpr int kXcds = 8, kGroup = 4;
+struct Split {
+  int m_tiles, n_tiles;
+  int splits;                // slices of the contraction; more than one: joined from the workspace
+  int64_t turns_each;
+};
+struct Where {
+  int mt, nt, split;
+};
+__device__ __forceinline__ Where where(const Split &sp) {
+  const uint32_t m_tiles = sp.m_tiles, n_tiles = sp.n_tiles;
+  const uint32_t tiles = m_tiles * n_tiles, total = tiles * sp.splits;
+  const uint32_t id = blockIdx.x, xcd = id % kXcds, at = id / kXcds;
+  const uint32_t each = total / kXcds, more = total % kXcds;
+  const uint32_t lin = xcd * each + min(xcd, more) + at;
+  const uint32_t split = lin / tiles, t = lin - split * tiles;
+  const uint32_t band = t / (kGroup * n_tiles), in_band = t - band * kGroup * n_tiles;
+  const uint32_t high = min(uint32_t{kGroup}, m_tiles - band * kGroup);
+  // uniform over the workgroup: kept in scalar registers
+  return Where{__builtin_amdgcn_readfirstlane(static_cast<int>(band * kGroup + in_band % high)),
+               __builtin_amdgcn_readfirstlane(static_cast<int>(in_band / high)), __builtin_amdgcn_readfirstlane(static_cast<int>(split))};
 }
 
 // Writes a wavefront's results: to `part`, a matrix of its own, or rounded
@@ -123,330 +160,241 @@ __device__ __forceinline__ void store_tile(const LinearArgs &a, const f32x4 (&ac
   }
 }
 
-// BM x BN tile of dW, WM x WN wavefronts, BK tokens a turn.  PARTS: bf16 parts
-// of dY (1: bf16, 3: fp32).  VEC: 16-byte loads of dY (its rows start on 16
-// bytes and a turn's rows lie within 2 GB).
-template <int BM, int BN, int BK, int WM, int WN, int PARTS, int FMT, bool VEC>
-__global__ __launch_bounds__(64 * WM * WN) void linear_grad_kernel(const LinearArgs a, int m_tiles, int n_tiles,
-                                                          int64_t turns_each, float *part) {
-  constexpr int NT = 64 * WM * WN;
-  constexpr int FO = BM / WM / 16, FI = BN / WN / 16;   // 16-wide fragments of a wavefront
-  constexpr int A_BYTES = BK * BM * 2, B_BYTES = BK * BN, S_BYTES = BK / 32 * BN;
-  constexpr int STAGE = PARTS * A_BYTES + B_BYTES + S_BYTES;
-  constexpr int CA = BM / 8, RA = NT / CA, JA = BK / RA;     // dY: 8-element chunks a row, rows a step, steps
-  constexpr int CB = BN / 16, RB = NT / CB, JB = BK / RB;    // codes: 16-byte chunks
-  constexpr int JS = (S_BYTES + NT - 1) / NT;
-  static_assert(JA >= 1 && JB >= 1 && BK % RA == 0 && BK % RB == 0, "tile too small");
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave / WN, wn = wave % WN;
-  const int tile = blockIdx.x;
-  const int nt = tile % n_tiles, mt = tile / n_tiles;
-  const int64_t m0 = static_cast<int64_t>(mt) * BM, n0 = static_cast<int64_t>(nt) * BN;
-  const int64_t turn0 = blockIdx.y * turns_each;
-  const int64_t all = (a.rows + BK - 1) / BK;
-  const int64_t turns = max(int64_t{0}, min(turns_each, all - turn0));
+// Sum of a lane's eight values of a dY fragment.
+__device__ __forceinline__ float fragment_sum(s16x4 lo, s16x4 hi) {
+  const i32x2 a = __builtin_bit_cast(i32x2, lo), b = __builtin_bit_cast(i32x2, hi);
+  const auto even = [](int w) { return __int_as_float(w << 16); };
+  const auto odd = [](int w) { return __int_as_float(w & static_cast<int>(0xffff0000u)); };
+  return ((even(a[0]) + odd(a[0])) + (even(a[1]) + odd(a[1]))) + ((even(b[0]) + odd(b[0])) + (even(b[1]) + odd(b[1])));
+}
 
-  f32x4 acc[FI][FO];
+// This workgroup's part of the bias gradient: one row of `part`.
+template <int FO, int WN>
+__device__ __forceinline__ void store_columns(const LinearArgs &a, float (&sum)[FO / WN], int64_t m0, int wm, int wn, float *part) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < FI; ++i)
-#pragma unroll
-    for (int o = 0; o < FO; ++o) acc[i][o] = f32x4{0, 0, 0, 0};
+  for (int o = 0; o < FO / WN; ++o) {
+    float v = sum[o];
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    const int64_t row = m0 + (wm * FO + wn * (FO / WN) + o) * 16 + lane;
+    if (lane < 16 && row < a.out) part[row] = v;
+  }
+}
 
-  // staging registers: one turn's dY, codes and scales
-  constexpr int ES = PARTS == 1 ? 2 : 4;
-  i32x4 ra[JA][ES / 2], rb[JB];
-  uint32_t rs[JS];
-  const int ca = tid % CA, r_a = tid / CA, cb = tid % CB, r_b = tid / CB;
+// Waits until at most N of this wavefront's loads are out and its LDS accesses
+// are done.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
 
-  auto load = [&](int64_t turn) {
-    const int64_t t0 = (turn0 + turn) * BK;
-    if constexpr (VEC) {
-      const auto rsrc = rest(a.dy, (t0 * a.lddy + m0) * ES, ((a.rows - 1) * a.lddy + a.out) * ES);
+// Drops the first `s` (0..7) of eight elements, N 32-bit words of them; zeros move in.
+template <int N>
+__device__ __forceinline__ void drop_front(uint32_t (&w)[N], int s) {
+  if (s & 4) {
 #pragma unroll
-      for (int j = 0; j < JA; ++j) {
-        const int off = static_cast<int>((r_a + RA * j) * a.lddy + ca * 8) * ES;
+    for (int k = 0; k < N; ++k) w[k] = k + N / 2 < N ? w[k + N / 2] : 0;
+  }
+  if (s & 2) {
 #pragma unroll
-        for (int h = 0; h < ES / 2; ++h) ra[j][h] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + 16 * h, 0, 0);
-      }
-    } else {
+    for (int k = 0; k < N; ++k) w[k] = k + N / 4 < N ? w[k + N / 4] : 0;
+  }
+  if (s & 1) {
 #pragma unroll
-      for (int j = 0; j < JA; ++j) {
-        const int64_t t = t0 + r_a + RA * j, m = m0 + ca * 8;
-        const int n = t < a.rows ? static_cast<int>(min(int64_t{8}, a.out - m)) : 0;
-        const char *p = static_cast<const char *>(a.dy) + (t * a.lddy + m) * ES;
-        if (n == 8) {
-          __builtin_memcpy(&ra[j][0], p, 8 * ES);
-        } else {
-          uint32_t w[2 * ES];
-#pragma unroll
-          for (int k = 0; k < 2 * ES; ++k) w[k] = 0;
-#pragma unroll
-          for (int k = 0; k < 7; ++k) {
-            if (k < n) {
-              if constexpr (ES == 4) w[k] = reinterpret_cast<const uint32_t *>(p)[k];
-              else w[k >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[k]) << (16 * (k & 1));
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 2 * ES; ++k) ra[j][k >> 2][k & 3] = static_cast<int>(w[k]);
-        }
-      }
-    }
-    const auto crsrc = rest(a.codes, t0 * a.pitch + n0, a.rows * a.pitch);
-#pragma unroll
-    for (int j = 0; j < JB; ++j)
-      rb[j] = __builtin_amdgcn_raw_buffer_load_b128(crsrc, static_cast<int>((r_b + RB * j) * a.pitch) + cb * 16, 0, 0);
-    const auto srsrc = rest(a.scales, t0 / kActBlock * a.pitch + n0, act_blocks(a.rows) * a.pitch);
-#pragma unroll
-    for (int j = 0; j < JS; ++j) {
-      const int at = tid + NT * j;
-      rs[j] = at >= S_BYTES ? 0u : __builtin_amdgcn_raw_buffer_load_b8(srsrc, static_cast<int>(at / BN * a.pitch) + at % BN, 0, 0);
-    }
-  };
-
-  auto store = [&](int buf) {
-    unsigned char *A = lds + buf * STAGE, *B = A + PARTS * A_BYTES, *S = B + B_BYTES;
-#pragma unroll
-    for (int j = 0; j < JA; ++j) {
-      const int r = r_a + RA * j;
-      unsigned char *p = A + r * (BM * 2) + (((ca >> 1) ^ swizzle_a(r)) << 5) + (ca & 1) * 16;
-      if constexpr (PARTS == 1) {
-        *reinterpret_cast<i32x4 *>(p) = ra[j][0];
-      } else {
-        i32x4 w[3];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h0, m0_, l0, h1, m1, l1;
-          split3(__int_as_float(ra[j][k >> 1][(2 * k) & 3]), h0, m0_, l0);
-          split3(__int_as_float(ra[j][k >> 1][(2 * k + 1) & 3]), h1, m1, l1);
-          w[0][k] = static_cast<int>(h0 | h1 << 16);
-          w[1][k] = static_cast<int>(m0_ | m1 << 16);
-          w[2][k] = static_cast<int>(l0 | l1 << 16);
-        }
-#pragma unroll
-        for (int q = 0; q < 3; ++q) *reinterpret_cast<i32x4 *>(p + q * A_BYTES) = w[q];
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < JB; ++j) {
-      const int r = r_b + RB * j;
-      *reinterpret_cast<i32x4 *>(B + r * BN + ((cb ^ swizzle_b<BN>(r)) << 4)) = rb[j];
-    }
-    // scales: [block][column % 16][column / 16], so a lane's fragments are adjacent
-#pragma unroll
-    for (int j = 0; j < JS; ++j) {
-      const int at = tid + NT * j, col = at % BN;
-      if (at < S_BYTES) S[at / BN * BN + (col & 15) * (BN / 16) + (col >> 4)] = static_cast<unsigned char>(rs[j]);
-    }
-  };
-
-  const int g = lane >> 4, li = lane & 15;
-  const int a_row = 8 * g + (li >> 2), a_sw = (li >> 2) | (g & 1) << 2;
-  const int b_row = 8 * g + (li >> 1), b_sw = swizzle_b<BN>(b_row);
-
-  // One 32-token step: its operands as they come from LDS, and its products.
-  struct Step {
-    uint32_t s[FI / 4];
-    i32x2 c[FI];
-    s16x4 y[PARTS][FO][2];
-  };
-  auto fetch = [&](int buf, int kk, Step &f) {
-    const unsigned char *A = lds + buf * STAGE, *B = A + PARTS * A_BYTES, *S = B + B_BYTES;
-#pragma unroll
-    for (int q = 0; q < FI / 4; ++q)
-      f.s[q] = *reinterpret_cast<const uint32_t *>(S + kk * BN + li * (BN / 16) + wn * FI + 4 * q);
-#pragma unroll
-    for (int i = 0; i < FI; ++i) {
-      const int unit = (wn * FI + i) ^ b_sw;
-      f.c[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((OB_LDS i32x2 *)(B + (kk * 32 + b_row) * BN + (unit << 4) + (li & 1) * 8));
-    }
-#pragma unroll
-    for (int q = 0; q < PARTS; ++q) {
-#pragma unroll
-      for (int o = 0; o < FO; ++o) {
-        const int unit = (wm * FO + o) ^ a_sw;
-        const auto *p = A + q * A_BYTES + (kk * 32 + a_row) * (BM * 2) + (unit << 5) + (li & 3) * 8;
-        f.y[q][o][0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p));
-        f.y[q][o][1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p + 4 * BM * 2));
-      }
-    }
-  };
-  auto multiply = [&](const Step &f) {
-    bf16x8 x[FI];
-#pragma unroll
-    for (int i = 0; i < FI; ++i) {
-      const float scale = act_scale_value((f.s[i >> 2] >> (8 * (i & 3))) & 0xffu);
-      const bf16x2 d[4] = {act_decode2<FMT, false>(f.c[i][0], scale), act_decode2<FMT, true>(f.c[i][0], scale),
-                           act_decode2<FMT, false>(f.c[i][1], scale), act_decode2<FMT, true>(f.c[i][1], scale)};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[i][k] = d[k >> 1][k & 1];
-    }
-#pragma unroll
-    for (int q = 0; q < PARTS; ++q) {
-#pragma unroll
-      for (int o = 0; o < FO; ++o) {
-        const bf16x8 y = __builtin_bit_cast(bf16x8, __builtin_shufflevector(f.y[q][o][0], f.y[q][o][1], 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-        for (int i = 0; i < FI; ++i) acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y, acc[i][o], 0, 0, 0);
-      }
-    }
-  };
-
-  // Each step's operands are read one step ahead.  Per turn one barrier, in
-  // its last step: behind it the turn's reads are done everywhere and the next
-  // turn's tile is in LDS.
-  constexpr int KK = BK / 32, UNROLL = KK == 1 ? 2 : 1;
-  if (turns > 0) {
-    Step f[2];
-    load(0);
-    store(0);
-    if (turns > 1) load(1);
-    __syncthreads();
-    fetch(0, 0, f[0]);
-    for (int64_t it = 0; it < turns; it += UNROLL) {
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int64_t t = it + u;
-        if (t >= turns) break;
-        const int buf = static_cast<int>(t & 1);
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-          constexpr int kBar = 0;
-          const int cur = (u * KK + kk) & 1;
-          if (kk + 1 < KK) fetch(buf, kk + 1, f[cur ^ 1]);
-          if (kk == 0) {
-            if (t + 1 < turns) store(buf ^ 1);
-            if (t + 2 < turns) load(t + 2);
-          }
-          if (kk + 1 == KK) {
-            __syncthreads();
-            if (t + 1 < turns) fetch(buf ^ 1, 0, f[cur ^ 1]);
-          }
-          __builtin_amdgcn_sched_barrier(kBar);
-          multiply(f[cur]);
-          __builtin_amdgcn_sched_barrier(kBar);
-        }
-      }
+    for (int k = 0; k < N; ++k) {
+      const uint32_t up = k + 1 < N ? w[k + 1] : 0;
+      w[k] = N == 8 ? up : (w[k] >> 16 | up << 16);
     }
   }
-
-  store_tile<BM, BN, WM, WN, FO, FI>(a, acc, m0, n0, wm, wn, part ? part + blockIdx.y * a.out * a.in : nullptr);
 }
 
-// ---------------------------------------------------------------------------
-// The large tile: bf16 dY whose rows start on 16 bytes.
-// ---------------------------------------------------------------------------
-#define OB_WAIT_VM(n) asm volatile("s_waitcnt vmcnt(" #n ")" ::: "memory")
-
-// Starts the copy of 16 bytes a lane, from its own offset, to 1 KB of LDS in
-// lane order.
-__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t from, OB_LDS unsigned char *to, int offset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (OB_LDS void *)to, 16, offset, 0, 0, 0);
-}
-
-// A workgroup's place: consecutive workgroups go to the 8 XCDs in turn, so
-// the tiles are numbered such that each XCD (its own L2) gets a consecutive
-// range: one slice of the contraction where there are several, and within it
-// kGroup tiles along dY's columns times a run along X's, the shape that needs
-// the fewest bytes of both (dY has two bytes an element, X one).
-constexpr int kXcds = 8, kGroup = 4;
-struct Where {
-  int mt, nt, split;
-};
-__device__ __forceinline__ Where where(int m_tiles, int n_tiles, int splits) {
-  const uint32_t tiles = static_cast<uint32_t>(m_tiles) * n_tiles, total = tiles * splits;
-  const uint32_t id = blockIdx.x, xcd = id % kXcds, at = id / kXcds;
-  const uint32_t each = total / kXcds, more = total % kXcds;
-  const uint32_t lin = xcd * each + min(xcd, more) + at;
-  const uint32_t split = lin / tiles, t = lin - split * tiles;
-  const uint32_t band = t / (kGroup * n_tiles), in_band = t - band * kGroup * n_tiles;
-  const uint32_t high = min(static_cast<uint32_t>(kGroup), m_tiles - band * kGroup);
-  return Where{static_cast<int>(band * kGroup + in_band % high), static_cast<int>(in_band / high), static_cast<int>(split)};
-}
-
-template <int BM, int BN, int WM, int WN, int FMT>
-__global__ __launch_bounds__(64 * WM * WN) void linear_grad_wide_kernel(const LinearArgs a, int m_tiles, int n_tiles,
-                                                                       int splits, int64_t turns_each, float *part) {
-  constexpr int BK = 64, NW = WM * WN, NT = 64 * NW;
-  constexpr int FO = BM / WM / 16, FI = BN / WN / 16;
-  constexpr int A_BYTES = BK * BM * 2, B_BYTES = BK * BN, S_BYTES = 2 * BN;
-  constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
-  constexpr int JA = A_BYTES / 1024 / NW, JB = B_BYTES / 1024 / NW;   // 1 KB copies a wavefront makes each turn
+// One workgroup's tile of dW over one slice of the contraction.
+//
+// BM x BN is the tile, WM x WN its wavefronts; a turn is BK tokens.  T is dY's
+// element (uint16_t: bf16; float: cut into three parts).  COPY: dY goes
+// straight from memory to LDS, 16 bytes a lane (bf16 whose rows start on 16
+// bytes); otherwise through registers, which costs them one turn of delay.
+// The codes always go straight to LDS.
+//
+// Stages.  At turn t the products run on tile t, tile t + 1 has arrived or is
+// arriving, and the copies of tile t + 2 start.  One barrier a turn: behind
+// it tile t + 1 is in LDS and nobody reads tile t any more.  Within a turn
+// every step's operands are read one step ahead of its products, so the
+// matrix unit has work while LDS answers.
+template <int BM, int BN, int BK, int WM, int WN, typename T, int FMT, bool COPY>
+__global__ __launch_bounds__(64 * WM * WN, 2) void linear_grad_kernel(const LinearArgs a, const Split sp, float *part, float *bias_part) {
+  constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
+  constexpr int NW = WM * WN, NT = 64 * NW, KK = BK / 32;
+  constexpr int FO = BM / WM / 16, FI = BN / WN / 16;                 // fragments of a wavefront
+  constexpr int A_BYTES = BK * BM * 2, B_BYTES = BK * BN, S_BYTES = KK * BN;
+  constexpr int A_STAGE = PARTS * A_BYTES, B_STAGE = B_BYTES + (S_BYTES + 255) / 256 * 256;
+  constexpr int STAGES = 3, A_STAGES = COPY ? STAGES : 2;         // through registers dY arrives a turn later
+  constexpr int JA = COPY ? A_BYTES / 1024 / NW : BK * BM / 8 / NT;   // dY: copies, or 8-element loads
+  constexpr int JB = B_BYTES / 1024 / NW;
   constexpr int RA = 512 / BM, RB = 1024 / BN;                        // rows of one copy
-  static_assert(S_BYTES <= NT && FI % 4 == 0 && JA * NW * 1024 == A_BYTES && JB * NW * 1024 == B_BYTES, "tile shape");
-  static_assert(1 + JA + JB == 7, "the waits below count a turn's loads");
-  __shared__ __attribute__((aligned(1024))) unsigned char shared[3 * STAGE];
+  static_assert(!COPY || PARTS == 1, "fp32 goes through registers");
+  static_assert(FI % 4 == 0 && FO % WN == 0 && JB * NW * 1024 == B_BYTES && JA >= 1, "tile shape");
+  static_assert(!COPY || JA * NW * 1024 == A_BYTES, "tile shape");
+  __shared__ __attribute__((aligned(1024))) unsigned char shared[A_STAGES * A_STAGE + STAGES * B_STAGE];
   OB_LDS unsigned char *const lds = (OB_LDS unsigned char *)shared;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const Where at = where(m_tiles, n_tiles, splits);
+  const Where at = where(sp);
   const int64_t m0 = static_cast<int64_t>(at.mt) * BM, n0 = static_cast<int64_t>(at.nt) * BN;
-  const int64_t turn0 = at.split * turns_each;
-  const int turns = static_cast<int>(max(int64_t{0}, min(turns_each, (a.rows + BK - 1) / BK - turn0)));
+  const int64_t turn0 = at.split * sp.turns_each;
+  const int turns = static_cast<int>(max(int64_t{0}, min(sp.turns_each, (a.rows + BK - 1) / BK - turn0)));
 
   f32x4 acc[FI][FO];
 #pragma unroll
   for (int i = 0; i < FI; ++i)
 #pragma unroll
     for (int o = 0; o < FO; ++o) acc[i][o] = f32x4{0, 0, 0, 0};
-
-  // where this lane's 16 bytes of each copy come from (the swizzle is applied
-  // to the source: the copies write LDS in order)
-  int from_a[JA], from_b[JB];
+  float columns[FO / WN];
 #pragma unroll
-  for (int j = 0; j < JA; ++j) {
-    const int r = (wave * JA + j) * RA + lane / (BM / 8), c = lane % (BM / 8);
-    from_a[j] = static_cast<int>(r * a.lddy) * 2 + (((c >> 1) ^ swizzle_a(r)) << 5) + (c & 1) * 16;
+  for (int o = 0; o < FO / WN; ++o) columns[o] = 0.0f;
+
+  // Where this lane's 16 bytes of each copy come from: the copies write LDS
+  // in lane order, so the swizzle is applied to the source.
+  int from_a[COPY ? JA : 1], from_b[JB];
+  if constexpr (COPY) {
+#pragma unroll
+    for (int j = 0; j < JA; ++j) {
+      const int r = (wave * JA + j) * RA + lane / (BM / 8), c = lane % (BM / 8);
+      from_a[j] = static_cast<int>(r * a.lddy) * 2 + (((c >> 1) ^ swizzle_a(r)) << 5) + (c & 1) * 16;
+    }
   }
 #pragma unroll
   for (int j = 0; j < JB; ++j) {
     const int r = (wave * JB + j) * RB + lane / (BN / 16), c = lane % (BN / 16);
     from_b[j] = static_cast<int>(r * a.pitch) + ((c ^ swizzle_b<BN>(r)) << 4);
   }
-  const int from_s = tid < S_BYTES ? static_cast<int>(tid / BN * a.pitch) + tid % BN : 0;
-  const int to_s = tid / BN * BN + (tid % BN & 15) * (BN / 16) + (tid % BN >> 4);
-  const int64_t dy_bytes = ((a.rows - 1) * a.lddy + a.out) * 2, code_bytes = a.rows * a.pitch,
-                scale_bytes = act_blocks(a.rows) * a.pitch;
+  // Scales, 256 bytes a copy: every wavefront makes one, several the same.
+  constexpr int SC = (S_BYTES + 255) / 256;
+  const int to_s = wave % SC * 256, from_s = (to_s + lane * 4) / BN * static_cast<int>(a.pitch) + (to_s + lane * 4) % BN;
+  // Where the next turn to be started reads, and how many rows it has: none
+  // past the last turn.
+  const int64_t row0 = turn0 * BK;
+  const char *dy_from = static_cast<const char *>(a.dy) + (row0 * a.lddy + m0) * static_cast<int>(sizeof(T));
+  const uint8_t *codes_from = a.codes + row0 * a.pitch + n0, *scales_from = a.scales + row0 / kActBlock * a.pitch + n0;
+  const int pitch = static_cast<int>(a.pitch);
+  int rows_left = static_cast<int>(min(a.rows - row0, static_cast<int64_t>(turns) * BK));
 
-  // The loads of a turn; a turn past the last reads nothing and fills zeros.
-  auto load_scale = [&](int turn) -> uint32_t {
-    const int64_t t0 = (turn0 + turn) * BK;
-    const auto r = rest(a.scales, turn < turns ? t0 / kActBlock * a.pitch + n0 : scale_bytes, scale_bytes);
-    return __builtin_amdgcn_raw_buffer_load_b8(r, from_s, 0, 0);
+  // What passes through registers, a turn at a time.
+  constexpr int CA = BM / 8, RT = NT / CA;             // chunks of a dY row, rows of one step
+  const int ca = tid % CA, ra = tid / CA;
+  uint32_t dy_reg[COPY ? 1 : JA][2 * sizeof(T)];
+
+  // dY through registers: a lane's eight elements are read wherever they lie,
+  // those past a row's end (dropped later) being the next row's.  Only at the
+  // very end of the matrix (of kFewRows elements at least) the read is moved
+  // back inside it, and settle() drops what came in front.
+  const int64_t dy_count = (a.rows - 1) * a.lddy + a.out;
+  const auto dy_at = [&](int64_t row) __attribute__((always_inline)) {
+    const int64_t m = m0 + ca * 8;
+    return row * a.lddy + (m < a.out ? m : 0);
   };
-  auto copy = [&](int turn, OB_LDS unsigned char *dst) {
-    const int64_t t0 = (turn0 + turn) * BK;
-    const auto ra = rest(a.dy, turn < turns ? (t0 * a.lddy + m0) * 2 : (dy_bytes + 15) / 16 * 16, dy_bytes);
-    const auto rb = rest(a.codes, turn < turns ? t0 * a.pitch + n0 : code_bytes, code_bytes);
+
+  // Starts the loads of the next turn.
+  auto start = [&](int turn, OB_LDS unsigned char *a_dst, OB_LDS unsigned char *b_dst) __attribute__((always_inline)) {
+    // its rows, and all ones or zeros by whether it has any
+    const int n = max(0, min(rows_left, BK)), any = -n >> 31;
+    rows_left -= BK;
+    const auto rs = buffer(scales_from, ((n + kActBlock - 1) / kActBlock * pitch - static_cast<int>(n0)) & any);
+    copy4(rs, b_dst + B_BYTES + to_s, from_s);
+    scales_from += KK * pitch;
+    if constexpr (COPY) {
+      const int ld = static_cast<int>(a.lddy);
+      const auto rd = buffer(dy_from, ((n - 1) * ld + static_cast<int>(a.out - m0)) * 2 & any);
 #pragma unroll
-    for (int j = 0; j < JA; ++j)
-      copy16(ra, dst + (wave * JA + j) * 1024, from_a[j]);
+      for (int j = 0; j < JA; ++j) copy16(rd, a_dst + (wave * JA + j) * 1024, from_a[j]);
+      dy_from += BK * a.lddy * 2;
+    } else {
 #pragma unroll
-    for (int j = 0; j < JB; ++j)
-      copy16(rb, dst + A_BYTES + (wave * JB + j) * 1024, from_b[j]);
+      for (int j = 0; j < JA; ++j) {
+        const int64_t e = min(dy_at(n > 0 ? row0 + turn * BK + ra + RT * j : 0), dy_count - 8);
+        __builtin_memcpy(dy_reg[j], static_cast<const T *>(a.dy) + e, 8 * sizeof(T));
+      }
+    }
+    const auto rc = buffer(codes_from, (n * pitch - static_cast<int>(n0)) & any);
+#pragma unroll
+    for (int j = 0; j < JB; ++j) copy16(rc, b_dst + (wave * JB + j) * 1024, from_b[j]);
+    codes_from += BK * pitch;
+  };
+  // Puts what came through registers for a turn into its tile.
+  auto settle = [&](int turn, OB_LDS unsigned char *a_to) __attribute__((always_inline)) {
+    if constexpr (!COPY) {
+      const int64_t t0 = row0 + turn * BK;
+      if (t0 + BK + 8 > a.rows) {          // the rows may end here
+#pragma unroll
+        for (int j = 0; j < JA; ++j) {
+          const int64_t row = t0 + ra + RT * j, e = dy_at(row);
+          if (row >= a.rows) {
+#pragma unroll
+            for (uint32_t &w : dy_reg[j]) w = 0;
+          } else if (e > dy_count - 8) {
+            drop_front(dy_reg[j], static_cast<int>(min(int64_t{7}, e - (dy_count - 8))));
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < JA; ++j) {
+        const int r = ra + RT * j;
+        OB_LDS unsigned char *p = a_to + r * (BM * 2) + (((ca >> 1) ^ swizzle_a(r)) << 5) + (ca & 1) * 16;
+        if constexpr (PARTS == 1) {
+          *(OB_LDS i32x4 *)p = i32x4{static_cast<int>(dy_reg[j][0]), static_cast<int>(dy_reg[j][1]),
+                                     static_cast<int>(dy_reg[j][2]), static_cast<int>(dy_reg[j][3])};
+        } else {
+          i32x4 w[3];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[2], m[2], l[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) split3(__uint_as_float(dy_reg[j][2 * k + e]), h[e], m[e], l[e]);
+            w[0][k] = static_cast<int>(h[0] | h[1] << 16);
+            w[1][k] = static_cast<int>(m[0] | m[1] << 16);
+            w[2][k] = static_cast<int>(l[0] | l[1] << 16);
+          }
+#pragma unroll
+          for (int q = 0; q < 3; ++q) *(OB_LDS i32x4 *)(p + q * A_BYTES) = w[q];
+        }
+      }
+    }
+  };
+  // The loads of turn t + 1 are done once only those of the turns after it are
+  // out (an access of 16 bytes is one load at least).
+  constexpr int kLoads = 1 + JA * (PARTS == 1 ? 1 : 2) + JB, kOut = (STAGES - 2) * kLoads;
+  auto arrived = [&]() __attribute__((always_inline)) {
+    wait_loads<kOut>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
 
   const int g = lane >> 4, li = lane & 15;
   const int a_row = 8 * g + (li >> 2), a_sw = (li >> 2) | (g & 1) << 2;
   const int b_row = 8 * g + (li >> 1), b_sw = swizzle_b<BN>(b_row);
 
-  struct Step {
-    uint32_t s[FI / 4];
+  // Operands of one 32-token step as they come from LDS: the codes with their
+  // scales, and dY (one of its parts).
+  struct Codes {
+    uint32_t s[FI];
     i32x2 c[FI];
+  };
+  struct Dy {
     s16x4 y[FO][2];
   };
-  auto fetch = [&](OB_LDS const unsigned char *A, int kk, Step &f) {
-    OB_LDS const unsigned char *B = A + A_BYTES, *S = B + B_BYTES;
+  auto fetch_codes = [&](OB_LDS const unsigned char *B, int kk, Codes &f) __attribute__((always_inline)) {
+    OB_LDS const unsigned char *S = B + B_BYTES;
 #pragma unroll
-    for (int q = 0; q < FI / 4; ++q)
-      f.s[q] = *(OB_LDS const uint32_t *)(S + kk * BN + li * (BN / 16) + wn * FI + 4 * q);
+    for (int i = 0; i < FI; ++i) f.s[i] = S[kk * BN + (wn * FI + i) * 16 + li];
 #pragma unroll
     for (int i = 0; i < FI; ++i)
       f.c[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
           (OB_LDS i32x2 *)(B + (kk * 32 + b_row) * BN + (((wn * FI + i) ^ b_sw) << 4) + (li & 1) * 8));
+  };
+  auto fetch_dy = [&](OB_LDS const unsigned char *A, int kk, Dy &f) __attribute__((always_inline)) {
 #pragma unroll
     for (int o = 0; o < FO; ++o) {
       OB_LDS const unsigned char *p = A + (kk * 32 + a_row) * (BM * 2) + (((wm * FO + o) ^ a_sw) << 5) + (li & 3) * 8;
@@ -454,112 +402,213 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_grad_wide_kernel(const Li
       f.y[o][1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p + 4 * BM * 2));
     }
   };
-  auto multiply = [&](const Step &f) {
+  auto decode = [&](const Codes &f, int i) __attribute__((always_inline)) -> bf16x8 {
+    const float scale = act_scale_value(f.s[i]);
+    const bf16x2 d[4] = {act_decode2<FMT, false>(f.c[i][0], scale), act_decode2<FMT, true>(f.c[i][0], scale),
+                         act_decode2<FMT, false>(f.c[i][1], scale), act_decode2<FMT, true>(f.c[i][1], scale)};
+    bf16x8 x;
 #pragma unroll
-    for (int i = 0; i < FI; ++i) {
-      const float scale = act_scale_value((f.s[i >> 2] >> (8 * (i & 3))) & 0xffu);
-      const bf16x2 d[4] = {act_decode2<FMT, false>(f.c[i][0], scale), act_decode2<FMT, true>(f.c[i][0], scale),
-                           act_decode2<FMT, false>(f.c[i][1], scale), act_decode2<FMT, true>(f.c[i][1], scale)};
-      bf16x8 x;
+    for (int k = 0; k < 8; ++k) x[k] = d[k >> 1][k & 1];
+    return x;
+  };
+  auto multiply = [&](const bf16x8 &x, const Dy &f, int i) __attribute__((always_inline)) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = d[k >> 1][k & 1];
+    for (int o = 0; o < FO; ++o) {
+      const bf16x8 y = __builtin_bit_cast(bf16x8, __builtin_shufflevector(f.y[o][0], f.y[o][1], 0, 1, 2, 3, 4, 5, 6, 7));
+      acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, acc[i][o], 0, 0, 0);
+    }
+  };
+  // Column sums of a step's dY: the WN wavefronts that share a fragment divide
+  // them.
+  auto add_columns = [&](const Dy &f) __attribute__((always_inline)) {
 #pragma unroll
-      for (int o = 0; o < FO; ++o) {
-        const bf16x8 y = __builtin_bit_cast(bf16x8, __builtin_shufflevector(f.y[o][0], f.y[o][1], 0, 1, 2, 3, 4, 5, 6, 7));
-        acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, acc[i][o], 0, 0, 0);
-      }
+    for (int o = 0; o < FO; ++o)
+      if (wn == o / (FO / WN)) columns[o % (FO / WN)] += fragment_sum(f.y[o][0], f.y[o][1]);
+  };
+  int sum_in = at.nt;              // turns until this workgroup's next share of the column sums
+
+  // Spreads the reads between the products: the wavefronts of a SIMD come out
+  // of the barrier together, and a run of reads would fill the LDS queue while
+  // the matrix unit stands still.
+  auto interleave = [&]() __attribute__((always_inline)) {
+    constexpr int kReads = 2 * FI + 2 * FO;
+#pragma unroll
+    for (int k = 0; k < kReads; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one product
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one read
     }
   };
 
-  Step f0, f1;
-  uint32_t s_reg;
-  // One turn on tile `cur`, tile t + 1 lying in `next`, tile t + 2 being
-  // copied to `dst`: three different stages, which __restrict says, so that
-  // the compiler does not hold the reads back for the copies; the waits and
-  // the barrier in the middle are what orders them.
-  auto turn = [&](int t, OB_LDS unsigned char *__restrict dst, OB_LDS unsigned char *__restrict cur,
-                  OB_LDS unsigned char *__restrict next) __attribute__((always_inline)) {
-    fetch(cur, 1, f1);
-    if (S_BYTES == NT || tid < S_BYTES) next[A_BYTES + B_BYTES + to_s] = static_cast<unsigned char>(s_reg);
-    s_reg = load_scale(t + 2);
-    copy(t + 2, dst);
+  // One turn.  The stages differ, which __restrict says: the compiler would
+  // otherwise hold every read back until all copies have landed.  The
+  // scheduling fences keep the reads ahead of the products before them.
+  // bf16: two steps, the first one's operands in (c, p) and the next turn's
+  // left there again.
+  auto turn_bf16 = [&](int t, Codes &c, Codes &d, Dy &p, Dy &q, OB_LDS unsigned char *__restrict a_dst,
+                       OB_LDS unsigned char *__restrict a_cur, OB_LDS unsigned char *__restrict a_next,
+                       OB_LDS unsigned char *__restrict b_dst, OB_LDS unsigned char *__restrict b_cur,
+                       OB_LDS unsigned char *__restrict b_next) __attribute__((always_inline)) {
+    const bool sums = bias_part != nullptr && sum_in == 0;
+    sum_in = sum_in == 0 ? sp.n_tiles - 1 : sum_in - 1;
+    settle(t + 1, a_next);
+    start(t + STAGES - 1, a_dst, b_dst);
+    if (sums) add_columns(p);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(f0);
+    fetch_codes(b_cur, 1, d);
+    fetch_dy(a_cur, 1, q);
+#pragma unroll
+    for (int i = 0; i < FI; ++i) multiply(decode(c, i), p, i);
+    interleave();
     __builtin_amdgcn_sched_barrier(0);
-    // tile t + 1 has landed once only this turn's 7 loads are out; this
-    // wavefront's reads of tile t are back
-    asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    fetch(next, 0, f0);
+    arrived();
+    if (sums) add_columns(q);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(f1);
+    fetch_codes(b_next, 0, c);
+    fetch_dy(a_next, 0, p);
+#pragma unroll
+    for (int i = 0; i < FI; ++i) multiply(decode(d, i), q, i);
+    interleave();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // fp32: one step in three parts, the first one's operands in (c, p), the
+  // next turn's left in (c, q).
+  auto turn_f32 = [&](int t, Codes &c, Dy &p, Dy &q, OB_LDS unsigned char *__restrict a_cur,
+                      OB_LDS unsigned char *__restrict a_next, OB_LDS unsigned char *__restrict b_dst,
+                      OB_LDS unsigned char *__restrict b_next) __attribute__((always_inline)) {
+    const bool sums = bias_part != nullptr && sum_in == 0;
+    sum_in = sum_in == 0 ? sp.n_tiles - 1 : sum_in - 1;
+    bf16x8 x[FI];
+#pragma unroll
+    for (int i = 0; i < FI; ++i) x[i] = decode(c, i);
+    fetch_dy(a_cur + A_BYTES, 0, q);
+    settle(t + 1, a_next);
+    start(t + STAGES - 1, nullptr, b_dst);
+    __builtin_amdgcn_sched_barrier(0);
+    if (sums) add_columns(p);
+#pragma unroll
+    for (int i = 0; i < FI; ++i) multiply(x[i], p, i);
+    fetch_dy(a_cur + 2 * A_BYTES, 0, p);
+    __builtin_amdgcn_sched_barrier(0);
+    if (sums) add_columns(q);
+#pragma unroll
+    for (int i = 0; i < FI; ++i) multiply(x[i], q, i);
+    __builtin_amdgcn_sched_barrier(0);
+    arrived();
+    fetch_codes(b_next, 0, c);
+    fetch_dy(a_next, 0, q);
+    __builtin_amdgcn_sched_barrier(0);
+    if (sums) add_columns(p);
+#pragma unroll
+    for (int i = 0; i < FI; ++i) multiply(x[i], p, i);
     __builtin_amdgcn_sched_barrier(0);
   };
 
   if (turns > 0) {
-    const uint32_t s0 = load_scale(0);
-    copy(0, lds);
-    s_reg = load_scale(1);
-    copy(1, lds + STAGE);
-    if (S_BYTES == NT || tid < S_BYTES) lds[A_BYTES + B_BYTES + to_s] = static_cast<unsigned char>(s0);
-    asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    fetch(lds, 0, f0);
-    OB_LDS unsigned char *cur = lds, *next = lds + STAGE, *dst = lds + 2 * STAGE;
-    for (int t = 0; t < turns; ++t) {
-      turn(t, dst, cur, next);
-      OB_LDS unsigned char *const was = cur;
-      cur = next;
-      next = dst;
-      dst = was;
+    // stages by turn: cur, next and the one that the copies started now go to
+    int a_at = 0, b_at = 0;
+    const auto a_stage = [&](int k) __attribute__((always_inline)) {
+      const int n = a_at + k;
+      return lds + (n >= A_STAGES ? n - A_STAGES : n) * A_STAGE;
+    };
+    const auto b_stage = [&](int k) __attribute__((always_inline)) {
+      const int n = b_at + k;
+      return lds + A_STAGES * A_STAGE + (n >= STAGES ? n - STAGES : n) * B_STAGE;
+    };
+    const auto rotate = [&]() __attribute__((always_inline)) {
+      a_at = a_at + 1 == A_STAGES ? 0 : a_at + 1;
+      b_at = b_at + 1 == STAGES ? 0 : b_at + 1;
+    };
+    Codes c0;
+    Dy y0, y1;
+    start(0, a_stage(0), b_stage(0));
+    settle(0, a_stage(0));
+#pragma unroll
+    for (int k = 1; k < STAGES - 1; ++k) start(k, a_stage(k), b_stage(k));
+    arrived();
+    fetch_codes(b_stage(0), 0, c0);
+    fetch_dy(a_stage(0), 0, y0);
+    if constexpr (PARTS == 1) {
+      static_assert(PARTS != 1 || KK == 2, "two steps a turn");
+      Codes c1;
+      for (int t = 0; t < turns; ++t) {
+        turn_bf16(t, c0, c1, y0, y1, a_stage(A_STAGES - 1), a_stage(0), a_stage(1), b_stage(STAGES - 1), b_stage(0), b_stage(1));
+        rotate();
+      }
+    } else {
+      static_assert(PARTS == 1 || KK == 1, "one step a turn");
+      for (int t = 0; t < turns; t += 2) {
+        turn_f32(t, c0, y0, y1, a_stage(0), a_stage(1), b_stage(STAGES - 1), b_stage(1));
+        rotate();
+        if (t + 1 >= turns) break;
+        turn_f32(t + 1, c0, y1, y0, a_stage(0), a_stage(1), b_stage(STAGES - 1), b_stage(1));
+        rotate();
+      }
     }
-    OB_WAIT_VM(0);   // no copy may land after the workgroup has ended
+    wait_loads<0>();   // no copy may land after the workgroup has ended
   }
   store_tile<BM, BN, WM, WN, FO, FI>(a, acc, m0, n0, wm, wn, part ? part + at.split * a.out * a.in : nullptr);
+  if (bias_part) store_columns<FO, WN>(a, columns, m0, wm, wn, bias_part + (at.split * sp.n_tiles + at.nt) * a.out);
 }
 
-// Column sums of dY over slices of rows: lane per column, the four wavefronts
-// take every fourth row of the slice, added in order.
-template <typename T>
-__global__ __launch_bounds__(256) void bias_kernel(const LinearArgs a, float *part, int64_t rows_each) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  const int64_t r0 = blockIdx.y * rows_each, r1 = min(a.rows, r0 + rows_each);
-  float sum = 0.0f;
-  if (col < a.out) {
-#pragma unroll 8
-    for (int64_t r = r0 + wave; r < r1; r += 4) {
-      const T v = static_cast<const T *>(a.dy)[r * a.lddy + col];
-      if constexpr (sizeof(T) == 4) sum += v;
-      else sum += __uint_as_float(static_cast<uint32_t>(v) << 16);
+// A few rows: an outer product or little more, bound by writing dW.  A thread
+// holds four columns of one weight row; the first one of a row its bias too.
+constexpr int kFewRows = 8;      // fewer than this
+template <typename T, typename G, int FMT>
+__global__ __launch_bounds__(kBlock) void linear_grad_few_kernel(const LinearArgs a, uint32_t quads) {
+  const uint32_t id = blockIdx.x * kBlock + threadIdx.x;
+  const uint32_t o = id / quads, i = (id - o * quads) * 4;
+  if (o >= a.out) return;
+  uint32_t s = 0, c[kFewRows - 1];
+  float y[kFewRows - 1];
+  if (a.rows > 0) s = *reinterpret_cast<const uint32_t *>(a.scales + i);
+#pragma unroll
+  for (int r = 0; r < kFewRows - 1; ++r) {
+    c[r] = 0;
+    y[r] = 0.0f;
+    if (r < a.rows) {
+      c[r] = *reinterpret_cast<const uint32_t *>(a.codes + r * a.pitch + i);
+      const T v = static_cast<const T *>(a.dy)[r * a.lddy + o];
+      if constexpr (sizeof(T) == 4) y[r] = v;
+      else y[r] = __uint_as_float(static_cast<uint32_t>(v) << 16);
     }
   }
-  __shared__ float s[4][64];
-  s[wave][lane] = sum;
-  __syncthreads();
-  if (wave == 0 && col < a.out)
-    part[blockIdx.y * a.out + col] = ((s[0][lane] + s[1][lane]) + s[2][lane]) + s[3][lane];
+  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b = 0.0f;
+#pragma unroll
+  for (int r = 0; r < kFewRows - 1; ++r) {
+    if (r < a.rows) {
+      const bf16x2 lo = act_decode2<FMT, false>(c[r], 1.0f), hi = act_decode2<FMT, true>(c[r], 1.0f);
+      const float x[4] = {static_cast<float>(lo[0]), static_cast<float>(lo[1]), static_cast<float>(hi[0]), static_cast<float>(hi[1])};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = __builtin_fmaf(y[r], x[k] * act_scale_value((s >> (8 * k)) & 0xffu), w[k]);
+      b += y[r];
+    }
+  }
+  const auto put = [&](G *p, float v) {
+    if constexpr (sizeof(G) == 4) *p = a.accumulate ? *p + v : v;
+    else *p = __builtin_bit_cast(uint16_t, static_cast<__bf16>(a.accumulate ? __uint_as_float(static_cast<uint32_t>(*p) << 16) + v : v));
+  };
+  G *p = static_cast<G *>(a.dw) + static_cast<int64_t>(o) * a.in + i;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (i + k < a.in) put(p + k, w[k]);
+  if (a.db && i == 0) put(static_cast<G *>(a.db) + o, b);
 }
 
-// out[e] = (accumulate ? out[e] : 0) + sum of the parts in order.
+// out[e] = (accumulate ? out[e] : 0) + sum of its parts in order, for the
+// weight (first `weight_blocks` workgroups) and the bias.
 template <typename G>
-__global__ __launch_bounds__(kBlock) void join_parts_kernel(const float *part, int parts, int64_t n, void *out,
-                                                            bool accumulate) {
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x) * 4;
+__device__ __forceinline__ void join_parts(const float *part, int64_t parts, int64_t n, G *out, bool accumulate, int64_t first) {
   if (first >= n) return;
-  G *p = static_cast<G *>(out) + first;
-  const bool quad = n % 4 == 0;
+  G *p = out + first;
   f32x4 v = {0, 0, 0, 0};
-  for (int s = 0; s < parts; ++s) {
-    const float *q = part + s * n + first;
-    if (quad) {
-      v += *reinterpret_cast<const f32x4 *>(q);
-    } else {
+  if (n % 4 == 0) {
+#pragma unroll 4
+    for (int64_t s = 0; s < parts; ++s) v += *reinterpret_cast<const f32x4 *>(part + s * n + first);
+  } else {
+    for (int64_t s = 0; s < parts; ++s) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (first + k < n) v[k] += q[k];
+        if (first + k < n) v[k] += part[s * n + first + k];
     }
   }
 #pragma unroll
@@ -573,103 +622,130 @@ __global__ __launch_bounds__(kBlock) void join_parts_kernel(const float *part, i
   }
 }
 
-constexpr int kBiasRows = 512;
+template <typename G>
+__global__ __launch_bounds__(kBlock) void join_kernel(const LinearArgs a, const float *part, int64_t parts, int64_t weight_blocks,
+                                                      const float *bias_part, int64_t bias_parts) {
+  const int64_t b = blockIdx.x;
+  if (b < weight_blocks)
+    join_parts<G>(part, parts, a.out * a.in, static_cast<G *>(a.dw), a.accumulate, (b * kBlock + threadIdx.x) * 4);
+  else
+    join_parts<G>(bias_part, bias_parts, a.out, static_cast<G *>(a.db), a.accumulate, ((b - weight_blocks) * kBlock + threadIdx.x) * 4);
+}
 
 struct Plan {
-  int bm, bn, bk;
-  int m_tiles, n_tiles;
-  int64_t turns_each;
-  int splits;                // parts of the contraction; > 1: joined from the workspace
-  int bias_slices;
+  int tile;                  // 256 or 128: both sides of the tile
+  Split sp;
   size_t weight_bytes, bias_bytes;
 };
 
-Plan plan_of(int64_t rows, int64_t out, int64_t in, bool dy_bf16, bool bias) {
+// Tile and number of slices with the least estimated time, in microseconds.
+// A launch runs in rounds of as many workgroups as the 256 CUs hold: one of
+// the large tile each, two of the small one.  Measured on MI355X (e4m3, bf16
+// dY): a 64-token turn of the large tile 1.55 us, of one small tile on a CU
+// 0.82, of two together 1.07; a workgroup's start and end 11 and 5 us; a slice
+// costs the writing and reading of its fp32 part at about 3 TB/s, and the
+// join.  16384 x 2048 x 2048: large tile in 4 slices 126 us, small in 2 146 us;
+// 4096 x 4096 x 1024: 52.3 against 51.9; 16384 x 8192 x 2048: large tile whole
+// 411 us (in 2 slices 465), small 549.  Where dY is not copied (or fp32) only
+// the small tile is built: the large one's registers would not hold a turn of
+// dY as well (it measured 236-277 us against 192 at 16384 x 2048 x 2048).
+Plan plan_of(int64_t rows, int64_t out, int64_t in, bool dy_bf16, bool copies, bool bias) {
   Plan p{};
-  p.bm = p.bn = dy_bf16 && ((out + 255) / 256) * ((in + 255) / 256) >= 128 ? 256 : 128;
-  p.bk = dy_bf16 ? 64 : 32;
-  p.m_tiles = static_cast<int>((out + p.bm - 1) / p.bm);
-  p.n_tiles = static_cast<int>((in + p.bn - 1) / p.bn);
-  const int64_t turns = (rows + p.bk - 1) / p.bk;
-  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  // enough workgroups for the 256 CUs, at least 8 turns each
-  int64_t splits = tiles >= 256 ? 1 : (512 + tiles - 1) / tiles;
-  splits = splits > turns / 8 ? turns / 8 : splits;
-  if (splits < 1) splits = 1;
-  p.turns_each = turns ? (turns + splits - 1) / splits : 0;
-  p.splits = static_cast<int>(turns ? (turns + p.turns_each - 1) / p.turns_each : 1);
-  p.bias_slices = bias ? static_cast<int>(rows ? (rows + kBiasRows - 1) / kBiasRows : 1) : 0;
-  p.weight_bytes = p.splits > 1 ? (static_cast<size_t>(p.splits) * out * in * 4 + 255) / 256 * 256 : 0;
-  p.bias_bytes = static_cast<size_t>(p.bias_slices) * out * 4;
+  if (rows < kFewRows) return p;
+  const int64_t bk = dy_bf16 ? 64 : 32, turns = (rows + bk - 1) / bk;
+  const double join = 2.0, part = static_cast<double>(out) * in * 4 / 3e6;
+  double best = 0.0;
+  for (const int tile : {256, 128}) {
+    if (tile == 256 && !copies) continue;
+    const int64_t m = (out + tile - 1) / tile, n = (in + tile - 1) / tile;
+    for (int64_t want = 1; want <= std::min<int64_t>(turns, 64); ++want) {
+      const int64_t each = (turns + want - 1) / want, splits = (turns + each - 1) / each, groups = m * n * splits;
+      if (splits != want || groups > kMaxGrid / 2) continue;
+      double t = splits > 1 ? join + splits * part : 0.0;
+      if (tile == 256) t += 11.0 + static_cast<double>((groups + 255) / 256) * each * 1.55;
+      else if (groups <= 256) t += 5.0 + each * 0.82;
+      else t += 5.0 + static_cast<double>((groups + 511) / 512) * each * 1.07;
+      if (p.tile == 0 || t < best) {
+        best = t;
+        p.tile = tile;
+        p.sp = Split{static_cast<int>(m), static_cast<int>(n), static_cast<int>(splits), each};
+      }
+    }
+  }
+  p.weight_bytes = p.sp.splits > 1 ? (static_cast<size_t>(p.sp.splits) * out * in * 4 + 255) / 256 * 256 : 0;
+  p.bias_bytes = bias ? static_cast<size_t>(p.sp.splits) * p.sp.n_tiles * out * 4 : 0;
   return p;
 }
 
-Plan plan_of(const LinearArgs &a) { return plan_of(a.rows, a.out, a.in, a.dy_bf16, a.db != nullptr); }
-
-template <int BM, int BN, int BK, int WM, int WN, int PARTS>
-void linear_one(const LinearArgs &a, const Plan &p, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.m_tiles) * p.n_tiles, p.splits);
-  float *part = p.splits > 1 ? static_cast<float *>(a.work) : nullptr;
-  const int64_t size = PARTS == 1 ? 2 : 4;
-  const bool vec = reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && a.lddy * size % 16 == 0 &&
-                   (a.lddy * BK + a.out) * size < 0x7fffffff;
-  if (a.fmt == kE4M3) {
-    if (vec) linear_grad_kernel<BM, BN, BK, WM, WN, PARTS, kE4M3, true><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
-    else linear_grad_kernel<BM, BN, BK, WM, WN, PARTS, kE4M3, false><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
-  } else {
-    if (vec) linear_grad_kernel<BM, BN, BK, WM, WN, PARTS, kInt8, true><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
-    else linear_grad_kernel<BM, BN, BK, WM, WN, PARTS, kInt8, false><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.turns_each, part);
-  }
+// Copies to LDS need bf16 rows that start on 16 bytes, a turn of them within 2 GB.
+bool copies_dy(const LinearArgs &a) {
+  return a.dy_bf16 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && a.lddy % 8 == 0 && (a.lddy * 64 + a.out) * 2 < 0x7fffffff;
 }
 
-template <int BM, int BN, int WM, int WN>
-void linear_wide(const LinearArgs &a, const Plan &p, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.m_tiles) * p.n_tiles * p.splits);
-  float *part = p.splits > 1 ? static_cast<float *>(a.work) : nullptr;
-  if (a.fmt == kE4M3)
-    linear_grad_wide_kernel<BM, BN, WM, WN, kE4M3><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.splits, p.turns_each, part);
-  else
-    linear_grad_wide_kernel<BM, BN, WM, WN, kInt8><<<grid, 64 * WM * WN, 0, s>>>(a, p.m_tiles, p.n_tiles, p.splits, p.turns_each, part);
+Plan plan_of(const LinearArgs &a) { return plan_of(a.rows, a.out, a.in, a.dy_bf16, copies_dy(a), a.db != nullptr); }
+
+float *weight_parts(const LinearArgs &a, const Plan &p) { return p.sp.splits > 1 ? static_cast<float *>(a.work) : nullptr; }
+float *bias_parts(const LinearArgs &a, const Plan &p) {
+  return a.db ? reinterpret_cast<float *>(static_cast<char *>(a.work) + p.weight_bytes) : nullptr;
+}
+
+template <int BM, int BN, int BK, int WM, int WN, typename T, int FMT, bool COPY>
+void linear_one(const LinearArgs &a, const Plan &p, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.sp.m_tiles) * p.sp.n_tiles * p.sp.splits);
+  linear_grad_kernel<BM, BN, BK, WM, WN, T, FMT, COPY><<<grid, 64 * WM * WN, 0, s>>>(a, p.sp, weight_parts(a, p), bias_parts(a, p));
+}
+
+template <typename T, int FMT>
+void linear_few(const LinearArgs &a, hipStream_t s) {
+  const int64_t quads = (a.in + 3) / 4;
+  const dim3 grid(static_cast<unsigned>((a.out * quads + kBlock - 1) / kBlock));
+  if (a.grad_bf16) linear_grad_few_kernel<T, uint16_t, FMT><<<grid, kBlock, 0, s>>>(a, static_cast<uint32_t>(quads));
+  else linear_grad_few_kernel<T, float, FMT><<<grid, kBlock, 0, s>>>(a, static_cast<uint32_t>(quads));
+}
+
+template <int FMT>
+void linear_by_type(const LinearArgs &a, const Plan &p, hipStream_t s) {
+  if (a.rows < kFewRows) {
+    if (a.dy_bf16) linear_few<uint16_t, FMT>(a, s);
+    else linear_few<float, FMT>(a, s);
+    return;
+  }
+  if (!a.dy_bf16) linear_one<128, 128, 32, 2, 2, float, FMT, false>(a, p, s);
+  else if (!copies_dy(a)) linear_one<128, 128, 64, 2, 2, uint16_t, FMT, false>(a, p, s);
+  else if (p.tile == 256) linear_one<256, 256, 64, 2, 4, uint16_t, FMT, true>(a, p, s);
+  else linear_one<128, 128, 64, 2, 2, uint16_t, FMT, true>(a, p, s);
 }
 
 }  // namespace
 
 bool linear_fits(int64_t rows, int64_t out, int64_t in) {
-  // a turn's codes lie within 2 GB; tiles and row slices within the grid's limits
+  // a turn's codes lie within 2 GB; a thread for every four elements, or 256 for a tile, fit the grid
   return in <= (int64_t{1} << 24) && out <= (int64_t{1} << 31) && rows <= (int64_t{1} << 24) &&
-         ((out + 127) / 128) * ((in + 127) / 128) <= kMaxGrid;
+         out * ((in + 3) / 4) <= kMaxGrid * kBlock - kBlock && ((out + 127) / 128) * ((in + 127) / 128) <= kMaxGrid / 2;
 }
 
 size_t linear_work_bytes(int64_t rows, int64_t out, int64_t in, bool dy_bf16, bool bias) {
-  const Plan p = plan_of(rows, out, in, dy_bf16, bias);
-  return p.weight_bytes + p.bias_bytes;
+  // of the two plans that a call may take by dY's alignment, the larger
+  const Plan p = plan_of(rows, out, in, dy_bf16, dy_bf16, bias), q = plan_of(rows, out, in, dy_bf16, false, bias);
+  return std::max(p.weight_bytes + p.bias_bytes, q.weight_bytes + q.bias_bytes);
 }
 
 void launch_linear_grad(const LinearArgs &a, hipStream_t s) {
   const Plan p = plan_of(a);
-  if (a.dy_bf16 && p.bm == 256) linear_wide<256, 256, 4, 2>(a, p, s);
-  else if (a.dy_bf16) linear_one<128, 128, 64, 2, 2, 1>(a, p, s);
-  else linear_one<128, 128, 32, 2, 2, 3>(a, p, s);
-  if (a.db) {
-    float *part = reinterpret_cast<float *>(static_cast<char *>(a.work) + p.weight_bytes);
-    const dim3 grid(static_cast<unsigned>((a.out + 63) / 64), p.bias_slices);
-    if (a.dy_bf16) bias_kernel<uint16_t><<<grid, 256, 0, s>>>(a, part, kBiasRows);
-    else bias_kernel<float><<<grid, 256, 0, s>>>(a, part, kBiasRows);
-  }
+  if (a.fmt == kE4M3) linear_by_type<kE4M3>(a, p, s);
+  else linear_by_type<kInt8>(a, p, s);
 }
 
-bool linear_needs_join(const LinearArgs &a) { return a.db != nullptr || plan_of(a).splits > 1; }
+bool linear_needs_join(const LinearArgs &a) { return a.rows >= kFewRows && (a.db != nullptr || plan_of(a).sp.splits > 1); }
 
 void launch_linear_join(const LinearArgs &a, hipStream_t s) {
   const Plan p = plan_of(a);
-  const auto join = [&](const float *part, int parts, int64_t n, void *out) {
-    const dim3 grid(static_cast<unsigned>((n + 4 * kBlock - 1) / (4 * kBlock)));
-    if (a.grad_bf16) join_parts_kernel<uint16_t><<<grid, kBlock, 0, s>>>(part, parts, n, out, a.accumulate);
-    else join_parts_kernel<float><<<grid, kBlock, 0, s>>>(part, parts, n, out, a.accumulate);
-  };
-  if (p.splits > 1) join(static_cast<const float *>(a.work), p.splits, a.out * a.in, a.dw);
-  if (a.db)
-    join(reinterpret_cast<const float *>(static_cast<const char *>(a.work) + p.weight_bytes), p.bias_slices, a.out, a.db);
+  const auto blocks = [](int64_t n) { return (n + 4 * kBlock - 1) / (4 * kBlock); };
+  const int64_t weight = p.sp.splits > 1 ? blocks(a.out * a.in) : 0, bias = a.db ? blocks(a.out) : 0;
+  const dim3 grid(static_cast<unsigned>(weight + bias));
+  const int64_t bias_count = static_cast<int64_t>(p.sp.splits) * p.sp.n_tiles;
+  if (a.grad_bf16) join_kernel<uint16_t><<<grid, kBlock, 0, s>>>(a, weight_parts(a, p), p.sp.splits, weight, bias_parts(a, p), bias_count);
+  else join_kernel<float><<<grid, kBlock, 0, s>>>(a, weight_parts(a, p), p.sp.splits, weight, bias_parts(a, p), bias_count);
 }
 
 }  // namespace ob

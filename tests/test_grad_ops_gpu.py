@@ -264,14 +264,15 @@ def _others_untouched(opt, grads, worker, tensors, keep=3.0):
 
 
 LINEAR_SHAPES = [(1, 1, 1), (1, 64, 64), (3, 17, 33), (32, 128, 128), (33, 129, 127), (64, 100, 257), (700, 130, 70),
-                 (513, 260, 390), (2500, 64, 40)]
+                 (513, 260, 390), (2500, 64, 40), (7, 40, 30), (8, 1, 1), (9, 3, 5), (130, 8, 264), (8200, 24, 16),
+                 (64, 1024, 4096)]
 
 
 @pytest.mark.parametrize("rows,out,inp", LINEAR_SHAPES)
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("dy_dtype", TYPES)
 def test_linear_grad_of_whole_numbers(rows, out, inp, fmt, dy_dtype):
-    """Sums of at most 2500 * 8 * 4 = 80000: exact in fp32, so bit for bit."""
+    """Sums of at most 8200 * 8 * 4 = 262400: exact in fp32, so bit for bit."""
     opt, ck, dy, grads = _linear_case(rows, out, inp, dy_dtype, torch.float32, fmt, True, whole=True)
     opt.linear_grad(1, 1, 2, ck, dy, grads)
     xhat = ref.decoded(ck.codes.cpu().numpy(), ck.scales.cpu().numpy(), inp, fmt)
@@ -516,9 +517,14 @@ def test_refusals():
                 dict(weight=2), dict(dy=torch.zeros(4, 7, device=DEV)), dict(dy=torch.zeros(5, 6, device=DEV)),
                 dict(dy=dy.half()), dict(dy=dy.cpu()), dict(dy=torch.zeros(6, 4, device=DEV).t()),
                 dict(grads=grads[:1]), dict(grads=grads.bfloat16()), dict(checkpoint=ActCheckpoint(4, 11, device=DEV)),
-                dict(work=torch.empty(1, dtype=torch.uint8, device=DEV)), dict(work=torch.empty(9999, dtype=torch.uint8))]:
+                dict(work=torch.empty(9999, dtype=torch.uint8))]:
         with pytest.raises(OneBitError):
             lin(**bad)
+    # a few rows need no scratch; more do, and 1 byte is too little
+    assert opt.linear_grad_work(4, 6, 10) == 0 and opt.linear_grad_work(9, 6, 10) > 1
+    with pytest.raises(OneBitError):
+        lin(checkpoint=ActCheckpoint(9, 10, device=DEV), dy=torch.zeros(9, 6, device=DEV),
+            work=torch.empty(1, dtype=torch.uint8, device=DEV))
     ids = torch.zeros(4, dtype=torch.int64, device=DEV)
     params = torch.zeros(opt.N, device=DEV)
     look = lambda **k: opt.embedding_lookup(**{**dict(tensor=0, dim=10, ids=ids, params=params, out=small), **k})   # noqa: E731
