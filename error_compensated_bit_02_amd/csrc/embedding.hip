@@ -9,18 +9,26 @@
 //
 // Gradient.  Tokens are ordered by (id, t) and summed run by run: no atomic
 // touches a sum, so results repeat bit for bit.
-//  1. order: each workgroup sorts one tile of kSortTile tokens in LDS (a
-//     bitonic network on id and position packed in one key, so the order is
-//     total), while the other workgroups of the same launch zero the
-//     gradient, which has to be written whole and usually takes longer;
-//  2. merge: runs of sorted tiles are merged kMergeWays at a time; an
-//     element's place is its index in its own run plus its rank in each
-//     other run, found by binary search;
-//  3. sum: one wavefront sums kRun consecutive sorted tokens of one slice
-//     of columns in fp32; a run of equal ids inside the chunk is written out,
-//     the parts of a run that crosses chunks go to the workspace;
+//  1. order: each workgroup sorts one tile of kSortTile tokens by id in LDS,
+//     four bits a pass (stable, so equal ids stay in token order);
+//  2. merge: kMergeWays sorted runs become one; an element's place is its
+//     index in its own run plus its rank in each other run, found by binary
+//     search;
+//  3. sum: one wavefront sums a chunk of consecutive sorted tokens of one
+//     slice of columns in fp32; a run of equal ids inside the chunk is
+//     written out, the parts of a run that crosses chunks go to the workspace.
+//     dY is read once, by loads that bypass the caches (kept in them it
+//     pushed out the gradient's lines: 58 us for 32768 x 2048, 35 without);
 //  4. join: the chunk where such a run begins adds its parts in order.
+// A gradient that is not accumulated is written whole, rows without a token as
+// zeros: further workgroups of the order launch zero all of it while it sorts
+// (a sort alone takes 13 us, the gradient of 50257 x 2048 in bf16 28 us).
+// Rows that have a token are then written twice; finding those that have none
+// and zeroing only them, beside the sums, was slower: 97 us against 94 for
+// 32768 tokens into that gradient, 44 against 35 for 4096 into 30522 x 1024.
 #include "internal.h"
+
+#include <algorithm>
 
 #pragma clang fp contract(off)
 
@@ -30,8 +38,8 @@ namespace {
 constexpr int kSortTile = 4096;
 constexpr int kSortThreads = 1024;
 constexpr int kSortShift = 12;          // log2(kSortTile)
-constexpr int kMergeWays = 16;
-constexpr int kRun = 32;                // sorted tokens summed by one wavefront
+constexpr int kMergeWays = 8;
+constexpr int kLeastChunk = 8;          // sorted tokens summed by one wavefront, at least
 constexpr uint32_t kNoId = 0xffffffffu; // sorts last, never summed
 
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
@@ -43,10 +51,35 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
-// N consecutive elements as fp32 and back: one vector access each where N > 1
-// (the caller has checked alignment).
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
+// N consecutive elements as fp32 and back: 16-byte accesses where N > 1 (the
+// caller has checked alignment).  read_once: loads that leave the caches to
+// others.
 template <typename T, int N>
 struct Vec {
+  static __device__ __forceinline__ void read_once(const T *p, float (&v)[N]) {
+    if constexpr (N == 1) {
+      const T x = __builtin_nontemporal_load(p);
+      if constexpr (sizeof(T) == 4) v[0] = x;
+      else v[0] = __uint_as_float(static_cast<uint32_t>(x) << 16);
+    } else {
+      constexpr int kEach = 16 / sizeof(T);
+#pragma unroll
+      for (int k = 0; k < N; k += kEach) {
+        const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + k));
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if constexpr (sizeof(T) == 4) {
+            v[k + h] = __uint_as_float(w[h]);
+          } else {
+            v[k + 2 * h] = __uint_as_float(w[h] << 16);
+            v[k + 2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
+          }
+        }
+      }
+    }
+  }
   static __device__ __forceinline__ void load(const T *p, float (&v)[N]) {
     if constexpr (N == 1) {
       if constexpr (sizeof(T) == 4) v[0] = *p;
@@ -124,9 +157,19 @@ struct Order {
   uint32_t *key[2];      // ids in sorted order, kNoId for those without a row
   uint32_t *pos[2];      // their tokens
   float *part;           // [chunks][2][dim] parts of runs that cross chunks
+  int chunk;             // sorted tokens of a chunk
   int64_t chunks;
   int passes;            // merge passes; the result is in key/pos[passes & 1]
 };
+
+// Sorted tokens a wavefront sums.  More of them mean fewer parts to join,
+// fewer of them more wavefronts: the most that still leaves a few thousand.
+int chunk_of(int64_t tokens, int64_t dim) {
+  const int64_t slices = (dim + 511) / 512;
+  int chunk = 32;
+  while (chunk > kLeastChunk && tokens * slices / chunk < 4096) chunk /= 2;
+  return chunk;
+}
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -143,95 +186,164 @@ Order order_of(const EmbedArgs &a) {
     p += 2 * b;
   }
   o.part = reinterpret_cast<float *>(p);
-  o.chunks = (a.tokens + kRun - 1) / kRun;
+  o.chunk = chunk_of(a.tokens, a.dim);
+  o.chunks = (a.tokens + o.chunk - 1) / o.chunk;
   return o;
 }
 
+// Inclusive sum over the lanes of a wavefront: within rows of 16 lanes, then
+// across the rows.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += shifted<0x111, 0xf>(v);   // from 1, 2, 4 and 8 lanes below in the row
+  v += shifted<0x112, 0xf>(v);
+  v += shifted<0x114, 0xf>(v);
+  v += shifted<0x118, 0xf>(v);
+  v += shifted<0x142, 0xa>(v);   // the last lane of a row to the next, rows 1 and 3
+  v += shifted<0x143, 0xc>(v);   // lane 31 to rows 2 and 3
+  return v;
+}
+
 // K: uint32_t while an id and a place in the tile fit in 32 bits, else uint64_t.
+// `bits`: of an id, the one behind the table's last included.
 template <typename K>
-__global__ __launch_bounds__(kSortThreads) void order_kernel(const EmbedArgs a, uint32_t *key, uint32_t *pos,
+__global__ __launch_bounds__(kSortThreads) void order_kernel(const EmbedArgs a, uint32_t *key, uint32_t *pos, int bits,
                                                              int sort_blocks, int64_t zero_bytes) {
+  const int tid = threadIdx.x;
   if (static_cast<int>(blockIdx.x) >= sort_blocks) {   // zero the gradient
     const int64_t n = zero_bytes / 16;
     uint4 *g = static_cast<uint4 *>(a.grad);
     const int64_t step = static_cast<int64_t>(gridDim.x - sort_blocks) * kSortThreads;
-    const int64_t first = static_cast<int64_t>(blockIdx.x - sort_blocks) * kSortThreads + threadIdx.x;
+    const int64_t first = static_cast<int64_t>(blockIdx.x - sort_blocks) * kSortThreads + tid;
     for (int64_t i = first; i < n; i += step) g[i] = make_uint4(0, 0, 0, 0);
     // the last bytes of a gradient that ends inside 16 bytes, two at a time (padding stays untouched)
     if (first < (zero_bytes - n * 16) / 2) reinterpret_cast<uint16_t *>(g + n)[first] = 0;
     return;
   }
+  // Element e = j * kSortThreads + tid.  A group is the 64 elements of one j
+  // and wavefront; group j * kSortWaves + wave holds the e's in order.  A
+  // pass counts each digit in each group, scans the counts digit by digit and
+  // group by group, and moves every element to its digit's and group's start
+  // plus its rank among the group's equals.  Two sets of counts: while one is
+  // in use the other is cleared.
+  constexpr int kPer = kSortTile / kSortThreads, kSortWaves = kSortThreads / 64, kGroups = kPer * kSortWaves;
+  static_assert(kGroups == 64 && 16 * kGroups == kSortThreads, "one count a thread, one digit a wavefront");
   __shared__ K s[kSortTile];
+  __shared__ uint32_t counts[2][16 * kGroups], total[16];
+  const int lane = tid & 63, wave = tid >> 6;
   const int64_t base = static_cast<int64_t>(blockIdx.x) * kSortTile;
   const int len = static_cast<int>(min(static_cast<int64_t>(kSortTile), a.tokens - base));
-  int n2 = 64;
-  while (n2 < len) n2 *= 2;
-  const K none = static_cast<K>(a.vocab);   // the id behind the table's last
-  for (int i = threadIdx.x; i < n2; i += kSortThreads) {
-    K k = ~K{0};
-    if (i < len) {
-      const int64_t id = id_at(a, base + i);
-      k = ((id >= 0 && id < a.vocab ? static_cast<K>(id) : none) << kSortShift) | static_cast<K>(i);
+  const int per = (len + kSortThreads - 1) / kSortThreads;    // j's in use
+  const K none = static_cast<K>(a.vocab);   // the id behind the table's last; also of elements past the end, which stay behind
+  K k[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int e = j * kSortThreads + tid;
+    K id = none;
+    if (e < len) {
+      const int64_t v = id_at(a, base + e);
+      if (v >= 0 && v < a.vocab) id = static_cast<K>(v);
     }
-    s[i] = k;
+    k[j] = (id << kSortShift) | static_cast<K>(e);
   }
+  counts[0][tid] = 0;
   __syncthreads();
-  for (int size = 2; size <= n2; size *= 2) {
-    for (int stride = size / 2; stride > 0; stride /= 2) {
-      for (int p = threadIdx.x; p < n2 / 2; p += kSortThreads) {
-        const int i = 2 * stride * (p / stride) + (p & (stride - 1));
-        const K x = s[i], y = s[i + stride];
-        if ((x > y) == ((i & size) == 0)) {
-          s[i] = y;
-          s[i + stride] = x;
+  for (int shift = kSortShift, side = 0; shift < kSortShift + bits; shift += 4, side ^= 1) {
+    uint32_t *const count = counts[side];
+    counts[side ^ 1][tid] = 0;
+    uint32_t rank[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (j < per) {
+        const uint32_t digit = static_cast<uint32_t>(k[j] >> shift) & 15u;
+        uint32_t same_lo = ~0u, same_hi = ~0u;    // lanes with the same digit
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t bit = static_cast<uint32_t>(__builtin_amdgcn_sbfe(static_cast<int>(digit), b, 1));   // all ones or zeros
+          const uint64_t set = __ballot(bit != 0);
+          same_lo &= ~(static_cast<uint32_t>(set) ^ bit);
+          same_hi &= ~(static_cast<uint32_t>(set >> 32) ^ bit);
         }
+        rank[j] = __builtin_amdgcn_mbcnt_hi(same_hi, __builtin_amdgcn_mbcnt_lo(same_lo, 0));
+        if (rank[j] == 0)
+          count[digit * kGroups + j * kSortWaves + wave] = static_cast<uint32_t>(__popc(same_lo) + __popc(same_hi));
       }
-      __syncthreads();
     }
+    __syncthreads();
+    const uint32_t mine = count[tid];        // digit `wave`, group `lane`
+    const uint32_t upto = wave_scan(mine);
+    if (lane == 63) total[wave] = upto;
+    __syncthreads();
+    uint32_t start = upto - mine;
+#pragma unroll
+    for (int w = 0; w < 16; ++w)
+      if (w < wave) start += total[w];
+    count[tid] = start;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (j < per) {
+        const uint32_t digit = static_cast<uint32_t>(k[j] >> shift) & 15u;
+        s[count[digit * kGroups + j * kSortWaves + wave] + rank[j]] = k[j];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (j < per) k[j] = s[j * kSortThreads + tid];
+    // the next pass writes s only behind its barriers
   }
-  for (int i = threadIdx.x; i < len; i += kSortThreads) {
-    const K k = s[i];
-    const K id = k >> kSortShift;
-    key[base + i] = id == none ? kNoId : static_cast<uint32_t>(id);
-    pos[base + i] = static_cast<uint32_t>(base) + static_cast<uint32_t>(k & (kSortTile - 1));
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int e = j * kSortThreads + tid;
+    if (e < len) {
+      const K id = k[j] >> kSortShift;
+      key[base + e] = id == none ? kNoId : static_cast<uint32_t>(id);
+      pos[base + e] = static_cast<uint32_t>(base) + static_cast<uint32_t>(k[j] & (kSortTile - 1));
+    }
   }
 }
 
-// Merges kMergeWays sorted runs of `run` elements each.
+// Merges kMergeWays sorted runs of `run` elements each.  Searching in memory
+// (L2) took 9 us for 32768 tokens, with the group's keys put into LDS first 16.
 __global__ __launch_bounds__(kBlock) void merge_kernel(const uint32_t *key, const uint32_t *pos, uint32_t *key_out,
                                                        uint32_t *pos_out, int64_t tokens, int64_t run) {
   const int64_t j = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+  // runs and groups hold whole workgroups of elements
+  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kBlock / run, first = mine / kMergeWays * kMergeWays;
+  const int64_t group = first * run;
+  const uint32_t *from = key + group;
   if (j >= tokens) return;
   const uint32_t k = key[j];
-  const int64_t mine = j / run, first = mine / kMergeWays * kMergeWays;
   int64_t place = j - (mine - first) * run;
   uint32_t top = 1;                        // smallest power of two past the run's length
   while (top <= run) top *= 2;
-#pragma unroll 1
-  for (int h = 0; h < kMergeWays; h += 8) {
-    int64_t start[8];
-    uint32_t len[8], below[8];
+  uint32_t start[kMergeWays], len[kMergeWays], below[kMergeWays];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int64_t b = first + h + u;
-      start[u] = b * run;
-      const int64_t left = tokens - start[u];
-      len[u] = b == mine || left <= 0 ? 0u : static_cast<uint32_t>(min(left, run));
-      below[u] = 0;                        // elements known to come before (k, this run)
-    }
-    for (uint32_t step = top / 2; step > 0; step /= 2) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t probe = below[u] + step;
-        if (probe <= len[u]) {
-          const uint32_t other = key[start[u] + probe - 1];
-          if (first + h + u < mine ? other <= k : other < k) below[u] = probe;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) place += below[u];
+  for (int u = 0; u < kMergeWays; ++u) {
+    const int64_t left = tokens - group - u * run;
+    len[u] = first + u == mine || left <= 0 ? 0u : static_cast<uint32_t>(min(left, run));
+    start[u] = len[u] ? static_cast<uint32_t>(u * run) : 0u;
+    below[u] = 0;                          // elements known to come before (k, this run)
   }
+  // every probe reads, inside its run (or the group's first key), so that the
+  // searches' reads overlap
+  for (uint32_t step = top / 2; step > 0; step /= 2) {
+    uint32_t other[kMergeWays];
+#pragma unroll
+    for (int u = 0; u < kMergeWays; ++u) other[u] = from[start[u] + max(min(below[u] + step, len[u]), 1u) - 1];
+#pragma unroll
+    for (int u = 0; u < kMergeWays; ++u) {
+      const uint32_t probe = below[u] + step;
+      const bool before = first + u < mine ? other[u] <= k : other[u] < k;
+      below[u] = probe <= len[u] && before ? probe : below[u];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kMergeWays; ++u) place += below[u];
   key_out[place] = k;
   pos_out[place] = pos[j];
 }
@@ -256,15 +368,15 @@ __device__ __forceinline__ void write_row(const EmbedArgs &a, uint32_t id, int64
 
 template <typename T, typename G, int N>
 __global__ __launch_bounds__(kBlock) void sum_kernel(const EmbedArgs a, const uint32_t *key, const uint32_t *pos,
-                                                     float *part, int64_t chunks, int slices) {
+                                                     float *part, int run, int64_t chunks, int slices) {
   const int lane = threadIdx.x & 63;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (unit >= chunks * slices) return;
   const int64_t chunk = unit / slices;
   const int64_t c = (static_cast<int64_t>(unit - chunk * slices) * 64 + lane) * N;
   const bool live = c < a.dim;
-  const int64_t j0 = chunk * kRun;
-  const int len = static_cast<int>(min(static_cast<int64_t>(kRun), a.tokens - j0));
+  const int64_t j0 = chunk * run;
+  const int len = static_cast<int>(min(static_cast<int64_t>(run), a.tokens - j0));
   uint32_t lk = kNoId, lp = 0;
   if (lane < len) {
     lk = key[j0 + lane];
@@ -281,8 +393,8 @@ __global__ __launch_bounds__(kBlock) void sum_kernel(const EmbedArgs a, const ui
     float v[8][N];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const uint32_t p = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(lp), (b + u) & (kRun - 1)));
-      Vec<T, N>::load(dy + static_cast<int64_t>(p) * a.lddy, v[u]);   // absent tokens read token 0, unused
+      const uint32_t p = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(lp), (b + u) & 31));
+      Vec<T, N>::read_once(dy + static_cast<int64_t>(p) * a.lddy, v[u]);   // absent tokens read token 0, unused
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -314,9 +426,9 @@ __global__ __launch_bounds__(kBlock) void sum_kernel(const EmbedArgs a, const ui
 // consecutive ranges, and the ranges' sums added in order.
 template <typename G, int N>
 __global__ __launch_bounds__(kBlock) void join_kernel(const EmbedArgs a, const uint32_t *key, const float *part,
-                                                      int64_t chunks, int slices) {
+                                                      int run, int slices) {
   const int64_t chunk = blockIdx.x / slices;
-  const int64_t j0 = chunk * kRun, j1 = j0 + kRun;
+  const int64_t j0 = chunk * run, j1 = j0 + run;
   if (j1 >= a.tokens) return;
   const uint32_t k = key[j1 - 1];
   if (k == kNoId || key[j1] != k) return;
@@ -324,13 +436,14 @@ __global__ __launch_bounds__(kBlock) void join_kernel(const EmbedArgs a, const u
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (static_cast<int64_t>(blockIdx.x - chunk * slices) * 64 + lane) * N;
   const bool live = c < a.dim;
-  int64_t lo = j1, hi = a.tokens;                            // first position past the run
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (key[mid] == k) lo = mid + 1;
-    else hi = mid;
+  // later chunks that hold a part: those that begin with the run's id, 64 at a look
+  int64_t parts = 0;
+  for (;;) {
+    const int64_t j = j1 + (parts + lane) * run;
+    const uint64_t same = __ballot(j < a.tokens && key[j] == k);
+    parts += __popcll(same);
+    if (~same) break;
   }
-  const int64_t parts = (lo - 1) / kRun - chunk;             // later chunks that hold a part
   const int64_t each = (parts + kWaves - 1) / kWaves;
   const int64_t p0 = min(parts, wave * each), p1 = min(parts, p0 + each);
   const float *src = part + (chunk + 1) * 2 * a.dim + (live ? c : 0);
@@ -363,9 +476,9 @@ void sum_one(const EmbedArgs &a, hipStream_t s) {
   const int slices = static_cast<int>((a.dim + 64 * N - 1) / (64 * N));
   const int side = o.passes & 1;
   const int64_t units = o.chunks * slices;
-  sum_kernel<T, G, N><<<dim3((units + kWaves - 1) / kWaves), kBlock, 0, s>>>(a, o.key[side], o.pos[side], o.part,
+  sum_kernel<T, G, N><<<dim3((units + kWaves - 1) / kWaves), kBlock, 0, s>>>(a, o.key[side], o.pos[side], o.part, o.chunk,
                                                                              o.chunks, slices);
-  if (o.chunks > 1) join_kernel<G, N><<<dim3(units), kBlock, 0, s>>>(a, o.key[side], o.part, o.chunks, slices);
+  if (o.chunks > 1) join_kernel<G, N><<<dim3(units), kBlock, 0, s>>>(a, o.key[side], o.part, o.chunk, slices);
 }
 
 template <typename T, typename G>
@@ -380,15 +493,16 @@ void sum_by_width(const EmbedArgs &a, hipStream_t s) {
 bool embed_fits(int64_t tokens, int64_t vocab, int64_t dim) {
   // ids are 32-bit; the lookup has a workgroup a token at most, the join one per chunk and slice
   const int64_t slices = (dim + 63) / 64;
-  return tokens <= kMaxGrid && vocab < (int64_t{1} << 31) && dim < (int64_t{1} << 31) &&
-         (tokens + kRun - 1) / kRun <= kMaxGrid / slices;
+  return tokens <= kMaxGrid && vocab < (int64_t{1} << 31) - 1 && dim < (int64_t{1} << 31) &&
+         (tokens + kLeastChunk - 1) / kLeastChunk <= kMaxGrid / 2 / slices;
 }
 
 size_t embed_work_bytes(int64_t tokens, int64_t dim) {
   if (tokens == 0) return 0;
+  const int chunk = chunk_of(tokens, dim);
   const size_t b = up256(static_cast<size_t>(tokens) * 4);
   return 2 * b * (tokens > kSortTile ? 2 : 1) +
-         up256(static_cast<size_t>((tokens + kRun - 1) / kRun) * 2 * static_cast<size_t>(dim) * 4);
+         up256(static_cast<size_t>((tokens + chunk - 1) / chunk) * 2 * static_cast<size_t>(dim) * 4);
 }
 
 void launch_embed_lookup(const EmbedArgs &a, hipStream_t s) {
@@ -414,12 +528,13 @@ void launch_embed_order(const EmbedArgs &a, hipStream_t s) {
   const int64_t zero_bytes = a.accumulate ? 0 : a.vocab * a.dim * (a.grad_bf16 ? 2 : 4);
   const int64_t want = (zero_bytes / 16 + kSortThreads - 1) / kSortThreads;
   const int zero_blocks = zero_bytes == 0 ? 0 : static_cast<int>(want < 1 ? 1 : want > 1024 ? 1024 : want);
-  if (sort_blocks + zero_blocks == 0) return;
   const dim3 grid(static_cast<unsigned>(sort_blocks + zero_blocks));
-  if ((a.vocab + 1) < (int64_t{1} << (32 - kSortShift)))
-    order_kernel<uint32_t><<<grid, kSortThreads, 0, s>>>(a, o.key[0], o.pos[0], sort_blocks, zero_bytes);
+  int bits = 1;
+  while ((a.vocab >> bits) > 0) ++bits;
+  if (bits <= 32 - kSortShift)
+    order_kernel<uint32_t><<<grid, kSortThreads, 0, s>>>(a, o.key[0], o.pos[0], bits, sort_blocks, zero_bytes);
   else
-    order_kernel<uint64_t><<<grid, kSortThreads, 0, s>>>(a, o.key[0], o.pos[0], sort_blocks, zero_bytes);
+    order_kernel<uint64_t><<<grid, kSortThreads, 0, s>>>(a, o.key[0], o.pos[0], bits, sort_blocks, zero_bytes);
   int64_t run = kSortTile;
   for (int p = 0; p < o.passes; ++p, run *= kMergeWays)
     merge_kernel<<<dim3((a.tokens + kBlock - 1) / kBlock), kBlock, 0, s>>>(

@@ -411,13 +411,14 @@ def test_embedding_lookup(tokens, vocab, dim, extra, offset, dtype, idt):
 
 
 EMBED_SHAPES = [(1, 1, 1), (1, 50, 24), (31, 7, 8), (32, 7, 8), (33, 7, 8), (64, 3, 40), (257, 40, 520), (1000, 999, 33),
-                (4096, 50, 16), (4097, 50, 16), (9001, 20, 8), (70001, 300, 8), (5000, 1 << 20, 1), (3000, 2, 1032)]
+                (4096, 50, 16), (4097, 50, 16), (9001, 20, 8), (70001, 300, 8), (5000, 1 << 20, 1), (3000, 2, 1032),
+                (8193, (1 << 20) - 1, 1), (40000, 5000, 16), (300000, 777, 2), (33000, 1, 8)]
 
 
 @pytest.mark.parametrize("tokens,vocab,dim", EMBED_SHAPES)
 @pytest.mark.parametrize("dy_dtype,idt", [(torch.float32, torch.int64), (torch.bfloat16, torch.int32)])
 def test_embedding_grad_of_whole_numbers(tokens, vocab, dim, dy_dtype, idt):
-    """Sums of at most 70001 * 4: exact in fp32, so bit for bit."""
+    """Sums of at most 300000 * 4: exact in fp32, so bit for bit."""
     opt = OneBitAdam([70, vocab * dim, 4], 2)
     ids = _ids(tokens, vocab, 13, dtype=idt)
     dy = torch.randint(-4, 5, (tokens, dim), generator=_gen(14)).to(dy_dtype).to(DEV)
