@@ -92,23 +92,36 @@ __device__ __forceinline__ float act_slope(float x) {
   }
 }
 
-// Eight consecutive elements as fp32: one or two 16-byte accesses where the
-// row allows it and all eight exist, single elements otherwise (absent ones
-// read as 0).
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  bf16x2 r;
+  r[0] = static_cast<__bf16>(a);
+  r[1] = static_cast<__bf16>(b);
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// Eight consecutive elements as fp32: 16-byte accesses where the row allows
+// them and all eight exist, single elements otherwise (absent ones read as 0).
+// Everything is streamed once, so the accesses are non-temporal: 5-12% faster
+// at 16384 x 8192 in bf16 (save and load with gelu_tanh 210 -> 184 us, gelu_tanh's
+// backward 146 -> 136 us; most of it from the stores).
 template <typename T, bool VEC>
 __device__ __forceinline__ void load8(const T *p, int n, float (&v)[8]) {
   if (VEC && n >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = *reinterpret_cast<const float4 *>(p);
-      const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4 *>(p);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    constexpr int kEach = 16 / sizeof(T);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(w[k] << 16);
-        v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    for (int k = 0; k < 8; k += kEach) {
+      const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + k));
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if constexpr (sizeof(T) == 4) {
+          v[k + h] = __uint_as_float(w[h]);
+        } else {
+          v[k + 2 * h] = __uint_as_float(w[h] << 16);
+          v[k + 2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
+        }
       }
     }
   } else {
@@ -123,22 +136,19 @@ __device__ __forceinline__ void load8(const T *p, int n, float (&v)[8]) {
   }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  bf16x2 r;
-  r[0] = static_cast<__bf16>(a);
-  r[1] = static_cast<__bf16>(b);
-  return __builtin_bit_cast(uint32_t, r);
-}
-
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T *p, int n, const float (&v)[8]) {
   if (VEC && n >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                 pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    constexpr int kEach = 16 / sizeof(T);
+#pragma unroll
+    for (int k = 0; k < 8; k += kEach) {
+      u32x4 w;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if constexpr (sizeof(T) == 4) w[h] = __float_as_uint(v[k + h]);
+        else w[h] = pack_bf16(v[k + 2 * h], v[k + 2 * h + 1]);
+      }
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p + k));
     }
   } else {
 #pragma unroll
@@ -266,19 +276,20 @@ __device__ __forceinline__ void load_scales(const ActArgs &a, const Place &at, f
 }
 
 template <int FMT>
-__device__ __forceinline__ void decode8(uint2 w, const float (&s)[8], float (&x)[8]) {
+__device__ __forceinline__ void decode8(u32x2 w, const float (&s)[8], float (&x)[8]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t c = h ? w.y : w.x;
+    const uint32_t c = w[h];
     if constexpr (FMT == kE4M3) {
-      x[4 * h] = __builtin_amdgcn_cvt_f32_fp8(c, 0) * s[4 * h];
-      x[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8(c, 1) * s[4 * h + 1];
-      x[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8(c, 2) * s[4 * h + 2];
-      x[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8(c, 3) * s[4 * h + 3];
+      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(c, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
+      x[4 * h] = lo[0] * s[4 * h];
+      x[4 * h + 1] = lo[1] * s[4 * h + 1];
+      x[4 * h + 2] = hi[0] * s[4 * h + 2];
+      x[4 * h + 3] = hi[1] * s[4 * h + 3];
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        x[4 * h + k] = static_cast<float>(static_cast<int8_t>(c >> (8 * k))) * s[4 * h + k];
+        x[4 * h + k] = static_cast<float>(static_cast<int>(__builtin_amdgcn_sbfe(c, 8 * k, 8))) * s[4 * h + k];
     }
   }
 }
@@ -290,11 +301,12 @@ __global__ __launch_bounds__(kBlock) void act_read_kernel(const ActArgs a) {
   if (!place(a, at) || at.n <= 0) return;
   float s[8];
   load_scales<FMT>(a, at, s);
-  uint2 w[kRowsPerLane];
+  u32x2 w[kRowsPerLane];
 #pragma unroll
   for (int j = 0; j < kRowsPerLane; ++j) {
     const int64_t r = at.row + 4 * j;
-    w[j] = r < a.rows ? *reinterpret_cast<const uint2 *>(a.codes_in + r * a.pitch + at.col) : make_uint2(0, 0);
+    w[j] = u32x2{0, 0};
+    if (r < a.rows) w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(a.codes_in + r * a.pitch + at.col));
   }
   float g[kRowsPerLane][8];
   if constexpr (ACT != kActNone) {
@@ -308,6 +320,7 @@ __global__ __launch_bounds__(kBlock) void act_read_kernel(const ActArgs a) {
   for (int j = 0; j < kRowsPerLane; ++j) {
     const int64_t r = at.row + 4 * j;
     if (r >= a.rows) break;
+    __builtin_amdgcn_sched_barrier(0);    // a row at a time: decoding all rows first takes registers for nothing
     float x[8];
     decode8<FMT>(w[j], s, x);
     if constexpr (ACT != kActNone) {

@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kSortThreads) void order_kernel(const EmbedArgs a, 
         uint32_t same_lo = ~0u, same_hi = ~0u;    // lanes with the same digit
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const uint32_t bit = static_cast<uint32_t>(__builtin_amdgcn_sbfe(static_cast<int>(digit), b, 1));   // all ones or zeros
+          const uint32_t bit = __builtin_amdgcn_sbfe(digit, b, 1);   // all ones or zeros
           const uint64_t set = __ballot(bit != 0);
           same_lo &= ~(static_cast<uint32_t>(set) ^ bit);
           same_hi &= ~(static_cast<uint32_t>(set >> 32) ^ bit);
