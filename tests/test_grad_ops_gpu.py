@@ -315,6 +315,20 @@ def test_linear_grad(rows, out, inp, extra, offset, fmt, dy_dtype, grad, bias):
     _near(grads[0, a: a + out * inp].view(out, inp), old + dw, n * mw + ref.U32 * (np.abs(old) + np.abs(dw)), grad)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,out,inp,extra", [(1500, 2056, 4100, 0), (9000, 520, 264, 8), (4100, 1032, 1028, 3)])
+def test_linear_grad_of_many_tiles(rows, out, inp, extra, fmt):
+    """Sizes that take large tiles, many slices, and slices through registers;
+    whole numbers (sums of at most 9000 * 8 * 4 = 288000), so bit for bit."""
+    opt, ck, dy, grads = _linear_case(rows, out, inp, torch.bfloat16, torch.float32, fmt, True, extra, whole=True, workers=1)
+    opt.linear_grad(0, 1, 2, ck, dy, grads)
+    xhat = ref.decoded(ck.codes.cpu().numpy(), ck.scales.cpu().numpy(), inp, fmt)
+    dy64, a, b = _f64(dy), opt.offsets[1], opt.offsets[2]
+    assert np.array_equal(_f64(grads[0, a: a + out * inp]).reshape(out, inp), dy64.T @ xhat)
+    assert np.array_equal(_f64(grads[0, b: b + out]), dy64.sum(axis=0))
+    _others_untouched(opt, grads, 0, [1, 2])
+
+
 def test_linear_grad_fp32_keeps_small_parts():
     """An fp32 dY whose low bits carry the answer: 1 + 2^-20 against -1, and
     values near both ends of the range."""
@@ -648,6 +662,54 @@ def test_graphs_replay():
             got = _results(s)
             got[2][0, :] = torch.where(got[2][0] == 9.0, w[2][0], got[2][0])     # padding keeps the fill
             assert all(torch.equal(x, y) for x, y in zip(got, w)), k
+
+
+def test_graph_with_its_own_workspace():
+    """Captured without `work`: the scratch then belongs to the graph."""
+    s = _chain_state(80)
+    s["work"] = [None, None]
+    _chain(**s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _chain(**s)
+    for k in range(3):
+        _renew(s, 200 + 10 * k)
+        _chain(**s)
+        torch.cuda.synchronize()
+        want = _results(s)
+        s["grads"].fill_(9.0)
+        noise = [torch.full((1 << 20,), float("nan"), device=DEV) for _ in range(4)]   # eager work in between
+        g.replay()
+        torch.cuda.synchronize()
+        got = _results(s)
+        got[2][0, :] = torch.where(got[2][0] == 9.0, want[2][0], got[2][0])
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), k
+        del noise
+
+
+def test_operators_leave_the_step_scratch_alone():
+    """The step's results do not change for gradients computed in between."""
+    sizes = [48 * 60, 80 * 48, 80]
+    runs = []
+    for between in (False, True):
+        opt = OneBitAdam(sizes, 1)
+        st = {k: torch.zeros(opt.N, device=DEV) for k in ("m", "err_s")}
+        p, v = torch.ones(opt.N, device=DEV), torch.full((opt.N,), 1e-4, device=DEV)
+        err_w, bufs = torch.zeros(1, opt.N, device=DEV), opt.alloc(DEV)
+        for k in range(3):
+            g = torch.randn(1, opt.N, generator=_gen(300 + k)).to(DEV)
+            if between:
+                s = _chain_state(310 + k)
+                s["opt"] = opt
+                s["params"] = torch.zeros(opt.N, device=DEV)
+                s["grads"] = torch.zeros(1, opt.N, device=DEV)
+                _chain(**s)
+            opt.step_residual(k == 0, g, st["m"], v, p, err_w, st["err_s"], bufs["packed_w"], bufs["scale_w"],
+                              bufs["packed_s"], bufs["scale_s"], 1e-3)
+        torch.cuda.synchronize()
+        runs.append(p.clone())
+    assert torch.equal(runs[0], runs[1])
 
 
 # ---------------------------------------------------------------------------
