@@ -2,7 +2,9 @@
 // same pass), load, and the activation's backward from the checkpoint.  The
 // format and its reasons are in activation.h.
 //
-// All three are bound by HBM.  One wavefront handles one scale block (32 rows)
+// All three are bound by HBM: gelu's backward of 16384 x 8192 in bf16 moves 675
+// MB in 136 us (5.0 TB/s, a plain copy's rate), with the 30-odd vector
+// instructions an element of its derivative close behind.  One wavefront handles one scale block (32 rows)
 // of 128 columns: lane l owns the 8 columns 8*(l%16) of rows l/16 + 4*j,
 // j < 8, so every row access is a full 16-byte vector per lane, a block's
 // scales are read or formed once per 8 rows, and the largest magnitude of a

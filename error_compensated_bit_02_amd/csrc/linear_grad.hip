@@ -17,6 +17,18 @@
 // converted after the read, one scale per lane and 32 tokens.  X is the
 // instruction's first operand, so a lane's four results are four consecutive
 // i of one weight row, stored as one vector.
+//
+// Precision.  Sums are fp32 throughout, the parts of a split contraction too;
+// the only rounding to fewer bits is the one to the gradient's type at the end.
+//
+// Measured on MI355X (bias included).  8192 x 2048 over 16384 tokens, bf16 dY:
+// 402 us with e4m3 (1366 TFLOP/s; the library's bf16 product of that shape,
+// X in bf16 and no bias, 457 us), 480 us with int8, whose conversion takes
+// five vector instructions for two elements instead of one.  With constant
+// inputs it takes 336 us: the card lowers its clock under load.  Of the 390 us
+// of the contraction, copies cost 70 (left out: 320) and the reads of LDS 65.
+// 1024 x 1024 over 4096 tokens 30 us: 256 workgroups of 16 turns, whose start,
+// end and join are half of it.  1000 x 2048 over 777 in fp32 35 us.
 #include "internal.h"
 #include "activation.h"
 
