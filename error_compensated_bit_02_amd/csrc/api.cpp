@@ -976,7 +976,7 @@ int ob_embedding_grad(ob_ctx *c, int32_t worker, int32_t tensor, int64_t dim, in
   a.accumulate = accumulate != 0;
   a.work = work;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (tokens > 0 || !a.accumulate) st = timed_free(c, ob::K_EMBED_ORDER, s, [&] { ob::launch_embed_order(a, s); });
+  if (!ob::embed_few(a) || !a.accumulate) st = timed_free(c, ob::K_EMBED_ORDER, s, [&] { ob::launch_embed_order(a, s); });
   if (st == OB_OK && tokens > 0) st = timed_free(c, ob::K_EMBED_SUM, s, [&] { ob::launch_embed_sum(a, s); });
   return st;
 }

@@ -284,6 +284,7 @@ size_t embed_work_bytes(int64_t tokens, int64_t dim);
 void launch_embed_lookup(const EmbedArgs &a, hipStream_t s);
 void launch_embed_order(const EmbedArgs &a, hipStream_t s);   // sorted positions; zeroes the gradient
 void launch_embed_sum(const EmbedArgs &a, hipStream_t s);     // one sum per row present
+bool embed_few(const EmbedArgs &a);                           // so few tokens that the sum needs no order
 
 // Weight and bias gradient from a checkpoint (linear_grad.hip).
 struct LinearArgs {

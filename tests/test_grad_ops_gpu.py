@@ -470,6 +470,30 @@ def test_embedding_grad(tokens, vocab, dim, extra, offset, dy_dtype, grad):
     _near(got, old + s * want, bound + ref.U32 * (np.abs(old) + np.abs(s * want)), grad)
 
 
+@pytest.mark.parametrize("tokens", [2, 15, 17, 63, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("vocab,dim", [(9000, 8), (5, 1032), (300, 33)])
+@pytest.mark.parametrize("ids_of", ["one row", "own rows", "mixed"])
+def test_embedding_grad_of_few_tokens(tokens, vocab, dim, ids_of):
+    """Sums of at most 129 * 4 are exact in fp32 and rounded once."""
+    ids = {"one row": torch.full((tokens,), vocab - 1), "own rows": torch.arange(tokens).flip(0) % vocab,
+           "mixed": _ids(tokens, vocab, 23)}[ids_of]
+    dy = torch.randint(-4, 5, (tokens, dim), generator=_gen(24)).float().to(DEV)
+    dy[ids.to(DEV) < 0] = float("nan")                             # padding is never read into a sum
+    want, _, _ = ref.embedding_grad(ids.numpy(), np.nan_to_num(_f64(dy)), vocab)
+    for kind in TYPES:
+        opt = OneBitAdam([70, vocab * dim, 4], 2, "bf16" if kind == torch.bfloat16 else "f32")
+        grads = torch.full((2, opt.N), 3.0, device=DEV, dtype=kind)
+        opt.embedding_grad(1, 1, dim, ids.to(DEV), dy, grads, scale=0.5)
+        a = opt.offsets[1]
+        got = grads[1, a: a + vocab * dim].view(vocab, dim)
+        assert np.array_equal(_f64(got), _f64(torch.from_numpy(0.5 * want).to(kind)))
+        _others_untouched(opt, grads, 1, [1])
+        got.fill_(2.0)
+        opt.embedding_grad(1, 1, dim, ids.to(DEV), dy, grads, scale=-1.0, accumulate=True)
+        assert np.array_equal(_f64(got), _f64(torch.from_numpy(2.0 - want).to(kind)))
+        _others_untouched(opt, grads, 1, [1])
+
+
 @pytest.mark.parametrize("fill", [-1, 5])
 def test_embedding_grad_without_a_single_row(fill):
     """All padding, or all past the table: a gradient of zeros, or what was there."""
