@@ -802,6 +802,7 @@ int ob_act_save(int32_t format, int32_t fn, int64_t rows, int64_t cols, int32_t 
   if (!matrix_ok(rows, cols, ldx) || (fn != OB_FN_NONE && !matrix_ok(rows, cols, ldy))) return OB_ERR_INVALID;
   if (rows == 0) return OB_OK;
   if (fn == OB_FN_NONE && y != nullptr) return OB_ERR_INVALID;
+  if (rows > 1 && y == x && ldy != ldx) return OB_ERR_INVALID;   // rows would overwrite others not yet read
   int st = check_elements(x, dtype_size(dtype));
   if (st == OB_OK && fn != OB_FN_NONE) st = check_elements(y, dtype_size(dtype));
   if (st == OB_OK) st = check_ptrs(codes, scales);
@@ -843,6 +844,7 @@ int ob_act_backward(int32_t format, int32_t fn, int64_t rows, int64_t cols, cons
   if (!act_format_ok(format) || !act_fn_ok(fn) || fn == OB_FN_NONE || !dtype_ok(dtype) || !act_shape_ok(rows, cols))
     return OB_ERR_INVALID;
   if (!matrix_ok(rows, cols, lddy) || !matrix_ok(rows, cols, lddx)) return OB_ERR_INVALID;
+  if (rows > 1 && dx == dy && lddx != lddy) return OB_ERR_INVALID;
   if (rows == 0) return OB_OK;
   int st = check_elements(dy, dtype_size(dtype));
   if (st == OB_OK) st = check_elements(dx, dtype_size(dtype));

@@ -393,8 +393,8 @@ int ob_cltk_step(ob_ctx *ctx, int64_t step, const void *grads, float *memory, in
 int ob_act_layout(int64_t rows, int64_t cols, int64_t *pitch, int64_t *code_bytes, int64_t *scale_bytes);
 
 /* Writes x's checkpoint and, with fn != OB_FN_NONE, y = fn(x) in the same
- * pass.  x and y have type dtype; y may be x itself (same ld), and is NULL
- * with OB_FN_NONE. */
+ * pass.  x and y have type dtype; y may be x itself (with the same ld),
+ * and is NULL with OB_FN_NONE. */
 int ob_act_save(int32_t format, int32_t fn, int64_t rows, int64_t cols, int32_t dtype, const void *x, int64_t ldx,
                 void *y, int64_t ldy, uint8_t *codes, uint8_t *scales, void *stream);
 
@@ -402,7 +402,7 @@ int ob_act_save(int32_t format, int32_t fn, int64_t rows, int64_t cols, int32_t 
 int ob_act_load(int32_t format, int64_t rows, int64_t cols, const uint8_t *codes, const uint8_t *scales, int32_t dtype,
                 void *out, int64_t ldo, void *stream);
 
-/* dx = dy * fn'(checkpoint's values); dx may be dy itself (same ld).  fn is
+/* dx = dy * fn'(checkpoint's values); dx may be dy itself (with the same ld).  fn is
  * not OB_FN_NONE. */
 int ob_act_backward(int32_t format, int32_t fn, int64_t rows, int64_t cols, const uint8_t *codes, const uint8_t *scales,
                     int32_t dtype, const void *dy, int64_t lddy, void *dx, int64_t lddx, void *stream);

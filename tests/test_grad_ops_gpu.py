@@ -589,6 +589,20 @@ def test_refusals():
     assert (grads == 3.0).all() and (small == 0).all()
 
 
+def test_in_place_needs_the_same_stride():
+    """Results over the inputs' start with another row stride would overwrite rows not yet read."""
+    ck = ActCheckpoint(4, 10, device=DEV)
+    buf = torch.ones(4 * 16, device=DEV)
+    near, far = buf[:40].view(4, 10), buf.view(4, 16)[:, :10]
+    for bad in [lambda: ck.save(near, act="gelu", y=far), lambda: ck.act_backward("silu", far, near)]:
+        with pytest.raises(OneBitError):
+            bad()
+    torch.cuda.synchronize()
+    assert (buf == 1).all()
+    ck.save(far, act="silu", y=far)
+    assert (buf.view(4, 16)[:, 10:] == 1).all() and (far != 1).all()
+
+
 def _chain(opt, ck, ids, x, y, dy, out, params, grads, work):
     """Every operator once."""
     opt.embedding_lookup(0, 48, ids, params, out, scale=2.0)
