@@ -920,8 +920,7 @@ int ob_embedding_lookup(ob_ctx *c, int32_t tensor, int64_t dim, int64_t tokens, 
   if (c == nullptr || tensor < 0 || tensor >= c->T || dim < 1 || tokens < 0 || !dtype_ok(out_dtype) ||
       (id_dtype != OB_ID_I32 && id_dtype != OB_ID_I64) || !std::isfinite(scale))
     return OB_ERR_INVALID;
-  if (c->numel[tensor] % dim != 0 || !ob::embed_fits(tokens, c->numel[tensor] / dim, dim) ||
-      !matrix_ok(tokens, dim, ldo))
+  if (c->numel[tensor] % dim != 0 || !ob::lookup_fits(tokens) || !matrix_ok(tokens, dim, ldo))
     return OB_ERR_INVALID;
   if (tokens == 0) return OB_OK;
   int st = check_ptr(params);
@@ -944,7 +943,7 @@ int ob_embedding_lookup(ob_ctx *c, int32_t tensor, int64_t dim, int64_t tokens, 
 }
 
 int ob_embedding_grad_work(int64_t tokens, int64_t dim, int64_t *work_bytes) {
-  if (work_bytes == nullptr || tokens < 0 || dim < 1 || !ob::embed_fits(tokens, 1, dim)) return OB_ERR_INVALID;
+  if (work_bytes == nullptr || tokens < 0 || dim < 1 || !ob::embed_grad_fits(tokens, 1, dim)) return OB_ERR_INVALID;
   *work_bytes = static_cast<int64_t>(ob::embed_work_bytes(tokens, dim));
   return OB_OK;
 }
@@ -955,7 +954,7 @@ int ob_embedding_grad(ob_ctx *c, int32_t worker, int32_t tensor, int64_t dim, in
   if (c == nullptr || worker < 0 || worker >= c->W || tensor < 0 || tensor >= c->T || dim < 1 || tokens < 0 ||
       !dtype_ok(dy_dtype) || (id_dtype != OB_ID_I32 && id_dtype != OB_ID_I64) || !std::isfinite(scale))
     return OB_ERR_INVALID;
-  if (c->numel[tensor] % dim != 0 || !ob::embed_fits(tokens, c->numel[tensor] / dim, dim) ||
+  if (c->numel[tensor] % dim != 0 || !ob::embed_grad_fits(tokens, c->numel[tensor] / dim, dim) ||
       !matrix_ok(tokens, dim, lddy))
     return OB_ERR_INVALID;
   int st = check_ptr(grads);

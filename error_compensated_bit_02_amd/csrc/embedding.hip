@@ -579,11 +579,14 @@ void sum_by_width(const EmbedArgs &a, hipStream_t s) {
 
 }  // namespace
 
-bool embed_fits(int64_t tokens, int64_t vocab, int64_t dim) {
-  // ids are 32-bit; the lookup has a workgroup a token at most, the join one per chunk and slice
-  const int64_t slices = (dim + 63) / 64;
-  return tokens <= kMaxGrid && vocab < (int64_t{1} << 31) - 1 && dim < (int64_t{1} << 31) &&
-         (tokens + kLeastChunk - 1) / kLeastChunk <= kMaxGrid / 2 / slices;
+bool lookup_fits(int64_t tokens) { return tokens <= kMaxGrid; }   // a workgroup a token at most
+
+bool embed_grad_fits(int64_t tokens, int64_t vocab, int64_t dim) {
+  // Sorted ids are 32-bit, the largest standing for none; the join has a workgroup per chunk and slice, which is
+  // 64 columns wide where rows are not vectors.  Chunks are shorter than 32 tokens only where tokens times slices
+  // of 512 columns stay below 2^17 (chunk_of), and those make far fewer workgroups than the limit.
+  return tokens <= kMaxGrid && vocab < (int64_t{1} << 31) && dim <= (int64_t{1} << 30) &&
+         (tokens + 31) / 32 * ((dim + 63) / 64) <= kMaxGrid;
 }
 
 bool embed_few(const EmbedArgs &a) { return a.tokens <= kFewTokens; }

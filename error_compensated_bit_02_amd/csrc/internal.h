@@ -278,8 +278,9 @@ struct EmbedArgs {
   bool accumulate;
   void *work;
 };
-// Whether launch sizes and 32-bit positions hold these counts.
-bool embed_fits(int64_t tokens, int64_t vocab, int64_t dim);
+// Whether launch sizes and 32-bit ids and positions hold these counts.
+bool lookup_fits(int64_t tokens);
+bool embed_grad_fits(int64_t tokens, int64_t vocab, int64_t dim);
 size_t embed_work_bytes(int64_t tokens, int64_t dim);
 void launch_embed_lookup(const EmbedArgs &a, hipStream_t s);
 void launch_embed_order(const EmbedArgs &a, hipStream_t s);   // sorted positions; zeroes the gradient

@@ -421,14 +421,16 @@ int ob_linear_grad(ob_ctx *ctx, int32_t worker, int32_t weight, int32_t bias, in
                    void *stream);
 
 /* Embedding lookup: out[t] = fp32(scale) * E[ids[t]], with tensor `tensor` of
- * params [N] as the table E [numel/dim][dim] (at most 2^31 - 1 rows; at most
- * 16,777,215 tokens).  A negative id is padding and gives a row of zeros; an id
+ * params [N] as the table E [numel/dim][dim], and at most 16,777,215 tokens.
+ * A negative id is padding and gives a row of zeros; an id
  * past the table gives a row of NaN.  out is [tokens][dim] of out_dtype. */
 int ob_embedding_lookup(ob_ctx *ctx, int32_t tensor, int64_t dim, int64_t tokens, const void *ids, int32_t id_dtype,
                         const float *params, double scale, int32_t out_dtype, void *out, int64_t ldo, void *stream);
 
 /* Its gradient: dE[v] = fp32(scale) * (sum over t with ids[t] = v of dy[t]);
- * ids outside the table contribute nothing.  dy is [tokens][dim] of dy_dtype. */
+ * ids outside the table contribute nothing.  dy is [tokens][dim] of dy_dtype.
+ * At most 16,777,215 tokens, 2^31 - 1 rows and 2^30 columns, and
+ * ceil(tokens/32) * ceil(dim/64) at most 16,777,215. */
 int ob_embedding_grad_work(int64_t tokens, int64_t dim, int64_t *work_bytes);
 int ob_embedding_grad(ob_ctx *ctx, int32_t worker, int32_t tensor, int64_t dim, int64_t tokens, const void *ids,
                       int32_t id_dtype, double scale, int32_t dy_dtype, const void *dy, int64_t lddy,

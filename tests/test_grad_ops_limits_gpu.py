@@ -1,0 +1,118 @@
+"""The gradient-making operators on the GPU at the ends of their ranges: the
+largest sizes, element counts past 2^31, and the choices by size that smaller
+tests do not reach.  Comparisons with torch run on the GPU, slice by slice."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import grad_ops as ref
+import test_grad_ops_gpu as base
+from error_compensated_bit_02_amd import ActCheckpoint, OneBitAdam, OneBitError
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+INVALID, ALIGN = 1, 2
+TYPES = [torch.float32, torch.bfloat16]
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    yield
+    torch.cuda.empty_cache()      # some cases take tens of GB
+
+
+# ---------------------------------------------------------------------------
+# sizes
+# ---------------------------------------------------------------------------
+def test_lookup_sizes_accepted():
+    """Whether sizes fit is decided before the output's alignment: an address off its element tells which
+    without a launch."""
+    opt = OneBitAdam([8 * 4096], 1)
+    ids = torch.zeros(16, dtype=torch.int32, device=DEV)
+    params = torch.zeros(opt.N, device=DEV)
+
+    def status(tokens, dim):
+        return opt.lib.ob_embedding_lookup(opt._ctx, 0, dim, tokens, ids.data_ptr(), 0, params.data_ptr(), 1.0, 1,
+                                           params.data_ptr() + 1, dim, None)
+
+    assert status((1 << 24) - 1, 4096) == ALIGN and status(1 << 20, 4096) == ALIGN and status((1 << 24) - 1, 8 * 4096) == ALIGN
+    assert status(1 << 24, 1) == INVALID and status(4, 4095) == INVALID
+
+
+@pytest.mark.parametrize("extra", [0, 1])
+def test_lookup_past_2_to_the_32_elements(extra):
+    """Vectors, and single elements where the row stride leaves 16 bytes."""
+    tokens, vocab, dim = (1 << 20) + 3, 100, 4096
+    opt = OneBitAdam([vocab * dim], 1)
+    params = torch.randn(opt.N, generator=base._gen(1)).to(DEV)
+    ids = base._ids(tokens, vocab, 2, dtype=torch.int32).clamp_max(vocab - 1).to(DEV)
+    out = torch.full((tokens, dim + extra), 7.0, dtype=torch.bfloat16, device=DEV)
+    opt.embedding_lookup(0, dim, ids, params, out[:, :dim], scale=2.0)
+    table = torch.cat([params[: vocab * dim].view(vocab, dim) * 2.0, torch.zeros(1, dim, device=DEV)]).bfloat16()
+    rows = torch.where(ids >= 0, ids, vocab).long()
+    for a in range(0, tokens, 1 << 17):
+        part = out[a: a + (1 << 17)]
+        assert torch.equal(part[:, :dim], table[rows[a: a + (1 << 17)]])
+        assert (part[:, dim:] == 7.0).all()
+
+
+@pytest.mark.parametrize("tokens", [100, 700])
+def test_table_of_the_most_rows(tokens):
+    """2^31 - 1 rows of one column: the last id an int32 can name and the id behind it; few tokens and sorted ones."""
+    vocab = (1 << 31) - 1
+    opt = OneBitAdam([vocab], 1)
+    ids = torch.randint(0, vocab, (tokens,), generator=base._gen(3))
+    ids[:9] = torch.tensor([vocab - 1, 0, vocab, vocab - 1, -1, 1, vocab - 2, vocab + 5, 0])
+    params = torch.zeros(opt.N, device=DEV)
+    inside = (ids >= 0) & (ids < vocab)
+    rows = ids[inside].to(DEV)
+    params[rows] = torch.arange(1.0, len(rows) + 1, device=DEV)     # of a row named twice, either
+    out = torch.full((tokens, 1), 7.0, device=DEV)
+    opt.embedding_lookup(0, 1, ids.to(DEV), params, out, scale=0.5)
+    assert torch.equal(out[inside.to(DEV), 0], params[rows] * 0.5)
+    assert torch.isnan(out[ids >= vocab]).all() and (out[ids < 0] == 0).all()
+    del params
+    dy = torch.randint(-4, 5, (tokens, 1), generator=base._gen(4)).float()
+    dy[~inside] = float("nan")
+    grads = torch.full((1, opt.N), 3.0, device=DEV)
+    opt.embedding_grad(0, 0, 1, ids.to(DEV), dy.to(DEV), grads)
+    distinct, at = torch.unique(ids[inside], return_inverse=True)
+    want = torch.zeros(len(distinct)).index_add_(0, at, dy[inside, 0])
+    assert torch.equal(grads[0, distinct.to(DEV)].cpu(), want)
+    assert int((grads[0, :vocab] != 0).sum()) == int((want != 0).sum()) and float(grads[0, vocab]) == 3.0
+
+
+def test_embedding_grad_of_the_most_tokens():
+    """2^24 - 1 tokens, a third of them of one row, with values -1..1: sums of at most 2^24, exact in fp32."""
+    tokens, vocab, dim = (1 << 24) - 1, 1000, 8
+    opt = OneBitAdam([vocab * dim], 1)
+    ids = base._ids(tokens, vocab, 5, dtype=torch.int32).to(DEV)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(6)
+    dy = torch.randint(-1, 2, (tokens, dim), generator=gen, device=DEV).float()
+    grads = torch.full((1, opt.N), 3.0, device=DEV)
+    opt.embedding_grad(0, 0, dim, ids, dy, grads)
+    inside = (ids >= 0) & (ids < vocab)
+    want = torch.zeros(vocab, dim, dtype=torch.float64, device=DEV)
+    want.index_add_(0, ids[inside].long(), dy[inside].double())
+    assert torch.equal(grads[0, : vocab * dim].view(vocab, dim).double(), want)
+
+
+def test_embedding_grad_past_2_to_the_31_elements():
+    """dY of 2^20 + 1 rows of 2056 columns in bf16: zero but for every 1009th
+    row, so the reference is small; whole numbers, exact in fp32."""
+    tokens, vocab, dim = (1 << 20) + 1, 40, 2056
+    opt = OneBitAdam([vocab * dim], 1)
+    ids = base._ids(tokens, vocab, 7, pad=0.0).clamp_max(vocab - 1)
+    some = torch.arange(tokens - 1, -1, -1009)
+    part = torch.randint(-4, 5, (len(some), dim), generator=base._gen(8)).float()
+    dy = torch.zeros(tokens, dim, dtype=torch.bfloat16, device=DEV)
+    dy[some.to(DEV)] = part.bfloat16().to(DEV)
+    grads = torch.full((1, opt.N), 3.0, device=DEV)
+    opt.embedding_grad(0, 0, dim, ids.to(DEV), dy, grads)
+    want = torch.zeros(vocab, dim).index_add_(0, ids[some], part)
+    assert torch.equal(grads[0, : vocab * dim].view(vocab, dim).cpu(), want)
