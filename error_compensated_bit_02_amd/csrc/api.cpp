@@ -918,7 +918,7 @@ int ob_linear_grad(ob_ctx *c, int32_t worker, int32_t weight, int32_t bias, int6
 int ob_embedding_lookup(ob_ctx *c, int32_t tensor, int64_t dim, int64_t tokens, const void *ids, int32_t id_dtype,
                         const float *params, double scale, int32_t out_dtype, void *out, int64_t ldo, void *stream) {
   if (c == nullptr || tensor < 0 || tensor >= c->T || dim < 1 || tokens < 0 || !dtype_ok(out_dtype) ||
-      (id_dtype != OB_ID_I32 && id_dtype != OB_ID_I64) || !std::isfinite(scale))
+      (id_dtype != OB_ID_I32 && id_dtype != OB_ID_I64) || !std::isfinite(static_cast<float>(scale)))
     return OB_ERR_INVALID;
   if (c->numel[tensor] % dim != 0 || !ob::lookup_fits(tokens) || !matrix_ok(tokens, dim, ldo))
     return OB_ERR_INVALID;
@@ -952,7 +952,7 @@ int ob_embedding_grad(ob_ctx *c, int32_t worker, int32_t tensor, int64_t dim, in
                       int32_t id_dtype, double scale, int32_t dy_dtype, const void *dy, int64_t lddy,
                       int32_t accumulate, void *grads, void *work, int64_t work_bytes, void *stream) {
   if (c == nullptr || worker < 0 || worker >= c->W || tensor < 0 || tensor >= c->T || dim < 1 || tokens < 0 ||
-      !dtype_ok(dy_dtype) || (id_dtype != OB_ID_I32 && id_dtype != OB_ID_I64) || !std::isfinite(scale))
+      !dtype_ok(dy_dtype) || (id_dtype != OB_ID_I32 && id_dtype != OB_ID_I64) || !std::isfinite(static_cast<float>(scale)))
     return OB_ERR_INVALID;
   if (c->numel[tensor] % dim != 0 || !ob::embed_grad_fits(tokens, c->numel[tensor] / dim, dim) ||
       !matrix_ok(tokens, dim, lddy))

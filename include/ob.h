@@ -421,9 +421,9 @@ int ob_linear_grad(ob_ctx *ctx, int32_t worker, int32_t weight, int32_t bias, in
                    void *stream);
 
 /* Embedding lookup: out[t] = fp32(scale) * E[ids[t]], with tensor `tensor` of
- * params [N] as the table E [numel/dim][dim], and at most 16,777,215 tokens.
- * A negative id is padding and gives a row of zeros; an id
- * past the table gives a row of NaN.  out is [tokens][dim] of out_dtype. */
+ * params [N] as the table E [numel/dim][dim], and at most 16,777,215 tokens;
+ * fp32(scale) is finite.  A negative id is padding and gives a row of zeros;
+ * an id past the table gives a row of NaN.  out is [tokens][dim] of out_dtype. */
 int ob_embedding_lookup(ob_ctx *ctx, int32_t tensor, int64_t dim, int64_t tokens, const void *ids, int32_t id_dtype,
                         const float *params, double scale, int32_t out_dtype, void *out, int64_t ldo, void *stream);
 

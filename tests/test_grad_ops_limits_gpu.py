@@ -116,3 +116,31 @@ def test_embedding_grad_past_2_to_the_31_elements():
     opt.embedding_grad(0, 0, dim, ids.to(DEV), dy, grads)
     want = torch.zeros(vocab, dim).index_add_(0, ids[some], part)
     assert torch.equal(grads[0, : vocab * dim].view(vocab, dim).cpu(), want)
+
+
+# ---------------------------------------------------------------------------
+# arguments
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("scale", [1e39, -1e39, 3.41e38, float("inf"), float("nan")])
+def test_a_scale_past_fp32_is_refused(scale):
+    """Finite as a double, infinite as the fp32 that multiplies: zeros would become NaN."""
+    opt = OneBitAdam([6 * 8], 1)
+    ids = torch.zeros(4, dtype=torch.int64, device=DEV)
+    params, rows = torch.zeros(opt.N, device=DEV), torch.zeros(4, 8, device=DEV)
+    grads = torch.full((1, opt.N), 3.0, device=DEV)
+    for call in (lambda: opt.embedding_lookup(0, 8, ids, params, rows, scale=scale),
+                 lambda: opt.embedding_grad(0, 0, 8, ids, rows, grads, scale=scale)):
+        with pytest.raises(OneBitError) as e:
+            call()
+        assert e.value.status == INVALID
+    torch.cuda.synchronize()
+    assert (grads == 3.0).all() and (rows == 0).all()
+
+
+def test_the_largest_scale():
+    top = float(np.finfo(np.float32).max)
+    opt = OneBitAdam([6 * 8], 1)
+    ids = torch.zeros(4, dtype=torch.int64, device=DEV)
+    params, rows = torch.full((opt.N,), 0.5, device=DEV), torch.zeros(4, 8, device=DEV)
+    opt.embedding_lookup(0, 8, ids, params, rows, scale=top)
+    assert (rows == top / 2).all()
