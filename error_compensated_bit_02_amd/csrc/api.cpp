@@ -892,6 +892,7 @@ int ob_linear_grad(ob_ctx *c, int32_t worker, int32_t weight, int32_t bias, int6
   if (st == OB_OK && rows > 0) st = check_ptrs(codes, scales);
   if (st == OB_OK) st = check_work(need, work, work_bytes);
   if (st) return st;
+  if (rows == 0 && accumulate) return OB_OK;   // nothing to add: not even +0, which would turn a -0 into +0
   ob::LinearArgs a{};
   a.rows = rows;
   a.out = out_features;

@@ -144,3 +144,18 @@ def test_the_largest_scale():
     params, rows = torch.full((opt.N,), 0.5, device=DEV), torch.zeros(4, 8, device=DEV)
     opt.embedding_lookup(0, 8, ids, params, rows, scale=top)
     assert (rows == top / 2).all()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_adding_no_rows_leaves_every_bit(kind):
+    """Negative zeros and a NaN with a payload stay what they are."""
+    opt = OneBitAdam([6 * 10, 6], 1, "bf16" if kind == torch.bfloat16 else "f32")
+    grads = torch.full((1, opt.N), -0.0, dtype=kind, device=DEV)
+    bits = grads.view(torch.int16 if kind == torch.bfloat16 else torch.int32)
+    bits[0, 3] = 0x7FA5 if kind == torch.bfloat16 else 0x7FC12345
+    before = bits.clone()
+    none = ActCheckpoint(0, 10, device=DEV)
+    opt.linear_grad(0, 0, 1, none, torch.empty(0, 6, device=DEV), grads, accumulate=True)
+    opt.embedding_grad(0, 0, 10, torch.empty(0, dtype=torch.int64, device=DEV), torch.empty(0, 10, device=DEV), grads,
+                       accumulate=True)
+    assert torch.equal(bits, before)
