@@ -206,27 +206,44 @@ def act_layout(rows: int, cols: int):
 class ActCheckpoint:
     """An 8-bit checkpoint of an activation [rows][cols] (format in include/ob.h):
     codes uint8 [rows][pitch] and scales uint8 [ceil(rows/32)][pitch], allocated
-    here on `device` or the caller's own contiguous tensors.
+    here on `device` or the caller's own contiguous tensors.  Shape, format and
+    tensors are fixed: a checkpoint of something else is another object.
     """
 
     def __init__(self, rows: int, cols: int, fmt: str = "e4m3", device=None, codes=None, scales=None):
         if fmt not in ACT_FORMATS:
             raise OneBitError(f"unknown format {fmt!r}, expected one of {tuple(ACT_FORMATS)}")
         self.lib = load_library()
-        self.rows, self.cols, self.fmt = int(rows), int(cols), fmt
-        self.pitch, code_bytes, scale_bytes = act_layout(self.rows, self.cols)
+        self._rows, self._cols, self._fmt = int(rows), int(cols), fmt
+        self._pitch, self._code_bytes, self._scale_bytes = act_layout(self._rows, self._cols)
         if (codes is None) != (scales is None):
             raise OneBitError("codes and scales are given together or not at all")
         if codes is None:
             device = torch.device("cuda" if device is None else device)
-            codes = torch.empty(self.rows, self.pitch, dtype=torch.uint8, device=device)
-            scales = torch.empty(scale_bytes // self.pitch, self.pitch, dtype=torch.uint8, device=device)
+            codes = torch.empty(self._rows, self._pitch, dtype=torch.uint8, device=device)
+            scales = torch.empty(self._scale_bytes // self._pitch, self._pitch, dtype=torch.uint8, device=device)
+        self._codes, self._scales, self._device = codes, scales, codes.device
+        self._format = ACT_FORMATS[fmt]
         u8 = (torch.uint8,)
-        self._codes, self._scales = _ptr(codes, u8, code_bytes, "codes"), _ptr(scales, u8, scale_bytes, "scales")
+        self._addresses = _ptr(codes, u8, self._code_bytes, "codes"), _ptr(scales, u8, self._scale_bytes, "scales")
         if codes.device != scales.device:
             raise OneBitError(f"codes are on {codes.device}, scales on {scales.device}")
-        self.codes, self.scales, self.device = codes, scales, codes.device
-        self._format = ACT_FORMATS[fmt]
+
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+    fmt = property(lambda self: self._fmt)
+    pitch = property(lambda self: self._pitch)
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    device = property(lambda self: self._device)
+
+    def _pointers(self):
+        """Addresses of codes and scales, refused if the tensors have been given other memory or sizes since."""
+        c, s = self._codes, self._scales
+        now = c.data_ptr(), s.data_ptr()
+        if now != self._addresses or c.numel() != self._code_bytes or s.numel() != self._scale_bytes:
+            raise OneBitError("the checkpoint's codes or scales were resized or moved")
+        return now
 
     @staticmethod
     def _fn(act: str) -> int:
@@ -245,16 +262,18 @@ class ActCheckpoint:
             yp, ydtype, ldy = _matrix(y, self.rows, self.cols, self.device, "y")
             if ydtype != dtype:
                 raise OneBitError(f"y has dtype {y.dtype}, x {x.dtype}")
+        codes, scales = self._pointers()
         with _on(self.device):
             st = self.lib.ob_act_save(self._format, fn, self.rows, self.cols, dtype, xp, ldx, yp, ldy,
-                                      self._codes, self._scales, _stream_on(stream, self.device))
+                                      codes, scales, _stream_on(stream, self.device))
         _check(st, "ob_act_save")
 
     def load(self, out, stream=None) -> None:
         """Write the kept values (exact in float32 and in bfloat16)."""
         op, dtype, ldo = _matrix(out, self.rows, self.cols, self.device, "out")
+        codes, scales = self._pointers()
         with _on(self.device):
-            st = self.lib.ob_act_load(self._format, self.rows, self.cols, self._codes, self._scales, dtype, op, ldo,
+            st = self.lib.ob_act_load(self._format, self.rows, self.cols, codes, scales, dtype, op, ldo,
                                       _stream_on(stream, self.device))
         _check(st, "ob_act_load")
 
@@ -265,8 +284,9 @@ class ActCheckpoint:
         xp, xdtype, lddx = _matrix(dx, self.rows, self.cols, self.device, "dx")
         if xdtype != dtype:
             raise OneBitError(f"dx has dtype {dx.dtype}, dy {dy.dtype}")
+        codes, scales = self._pointers()
         with _on(self.device):
-            st = self.lib.ob_act_backward(self._format, fn, self.rows, self.cols, self._codes, self._scales, dtype,
+            st = self.lib.ob_act_backward(self._format, fn, self.rows, self.cols, codes, scales, dtype,
                                           gp, lddy, xp, lddx, _stream_on(stream, self.device))
         _check(st, "ob_act_backward")
 
@@ -506,11 +526,12 @@ class OneBitAdam:
         self._on_device(checkpoint.codes, "checkpoint")
         gp, gdt, lddy = _matrix(dy, rows, out, self.device, "dy")
         self._on_device(grads, "grads")
+        codes, scales = checkpoint._pointers()
         work, have = _work(work, self.linear_grad_work(rows, out, cols, dy.dtype, bias >= 0), stream, self.device)
         with _on(self.device):
             st = self.lib.ob_linear_grad(
-                self._ctx, int(worker), weight, bias, rows, out, cols, checkpoint._format, checkpoint._codes,
-                checkpoint._scales, gdt, gp, lddy, 1 if accumulate else 0, self._grad_ptr(grads),
+                self._ctx, int(worker), weight, bias, rows, out, cols, checkpoint._format, codes, scales, gdt,
+                gp, lddy, 1 if accumulate else 0, self._grad_ptr(grads),
                 None if work is None else work.data_ptr(), have, _stream_on(stream, self.device))
         _check(st, "ob_linear_grad")
 

@@ -2,8 +2,9 @@
 import ctypes
 
 import pytest
+import torch
 
-from error_compensated_bit_02_amd import binding
+from error_compensated_bit_02_amd import ActCheckpoint, OneBitError, binding
 
 INVALID = 1
 
@@ -23,3 +24,82 @@ def test_embedding_grad_work_to_its_limit(lib, tokens, dim, fits):
     assert (lib.ob_embedding_grad_work(tokens, dim, ctypes.byref(n)) == 0) == fits
     # a chunk of at most 32 tokens leaves two rows of fp32 sums
     assert not fits or n.value >= 8 * tokens + -(-tokens // 32) * 2 * dim * 4
+
+
+class DeviceBytes:
+    """A stand-in for a device tensor of bytes; nothing here reads its address."""
+    dtype, is_cuda, device = torch.uint8, True, torch.device("cuda", 0)
+
+    def __init__(self, n, address):
+        self.n, self.address = n, address
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.n
+
+    def data_ptr(self):
+        return self.address
+
+
+class DeviceMatrix(DeviceBytes):
+    dtype = torch.float32
+    shape = (40, 70)
+
+    def dim(self):
+        return 2
+
+    def stride(self, d):
+        return (70, 1)[d]
+
+
+def _checkpoint_of_stand_ins():
+    codes, scales = DeviceBytes(40 * 128, 1 << 20), DeviceBytes(2 * 128, 1 << 24)
+    return codes, scales, ActCheckpoint(40, 70, codes=codes, scales=scales)
+
+
+@pytest.mark.parametrize("name", ["rows", "cols", "fmt", "pitch", "codes", "scales", "device"])
+def test_a_checkpoint_cannot_be_made_another(name):
+    """Kernels take the shape and the addresses from it: exchanging one of them alone would let them run past the others."""
+    _, _, ck = _checkpoint_of_stand_ins()
+    before = getattr(ck, name)
+    with pytest.raises(AttributeError):
+        setattr(ck, name, 1 << 20)
+    assert getattr(ck, name) is before
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("change", [dict(n=0, address=0), dict(address=1 << 28), dict(n=64)])
+def test_a_checkpoint_whose_memory_changed_is_refused(monkeypatch, which, change):
+    """Resized or moved in place since: refused before the library is called."""
+    *tensors, ck = _checkpoint_of_stand_ins()
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or 0
+
+    class Here:
+        def __init__(self, device):
+            pass
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *exc):
+            pass
+
+    monkeypatch.setattr(ck, "lib", Library())
+    monkeypatch.setattr(binding, "_on", Here)
+    monkeypatch.setattr(binding, "_stream_on", lambda stream, device: 0)
+    x = DeviceMatrix(40 * 70, 1 << 26)
+    for call in (lambda: ck.save(x), lambda: ck.load(x), lambda: ck.act_backward("silu", x, x)):
+        call()
+    assert calls == ["ob_act_save", "ob_act_load", "ob_act_backward"]
+    for k, v in change.items():
+        setattr(tensors[which], k, v)
+    for call in (lambda: ck.save(x), lambda: ck.load(x), lambda: ck.act_backward("silu", x, x)):
+        with pytest.raises(OneBitError, match="resized or moved"):
+            call()
+    assert len(calls) == 3

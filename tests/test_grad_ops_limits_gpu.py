@@ -159,3 +159,18 @@ def test_adding_no_rows_leaves_every_bit(kind):
     opt.embedding_grad(0, 0, 10, torch.empty(0, dtype=torch.int64, device=DEV), torch.empty(0, 10, device=DEV), grads,
                        accumulate=True)
     assert torch.equal(bits, before)
+
+
+def test_a_checkpoint_resized_in_place_is_refused():
+    opt = OneBitAdam([6 * 10, 6], 1)
+    grads, dy, x = torch.full((1, opt.N), 3.0, device=DEV), torch.zeros(40, 6, device=DEV), torch.zeros(40, 10, device=DEV)
+    for name in ("codes", "scales"):
+        ck = ActCheckpoint(40, 10, device=DEV)
+        ck.save(x)
+        getattr(ck, name).resize_(0)
+        for call in (lambda: opt.linear_grad(0, 0, 1, ck, dy, grads), lambda: ck.save(x), lambda: ck.load(x),
+                     lambda: ck.act_backward("gelu", x, x)):
+            with pytest.raises(OneBitError, match="resized or moved"):
+                call()
+    torch.cuda.synchronize()
+    assert (grads == 3.0).all()
