@@ -4,8 +4,10 @@
 #include "ob.h"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <new>
 #include <utility>
 #include <vector>
@@ -54,9 +56,12 @@ struct ob_ctx {
   double2 *chunk_partials = nullptr;   // W x num_tiles * kChunksPerTile (chunked worker passes)
   void *static_scratch = nullptr;  // the device's static no-allocation scratch (null if unresolved)
   size_t static_need = 0;          // bytes of it the no-allocation step uses for this list
-  bool profiling = false;
   bool launched = false;             // some kernel was enqueued, on last_stream the latest
   hipStream_t last_stream = nullptr;
+  // Kernel timing.  The gradient-making calls may come from several threads at
+  // once, so the event lists have a lock of their own (taken with profiling on only).
+  std::atomic<bool> profiling{false};
+  std::mutex events_lock;
   std::vector<EventPair> pending[ob::K_NUM_KINDS];
   std::vector<EventPair> pool;
 };
@@ -102,11 +107,19 @@ template <typename F>
 int timed(ob_ctx *c, ob::Kind kind, hipStream_t s, F &&launch, bool events = true, bool own_tables = true) {
   EventPair ev;
   const bool profiling = events && c->profiling;
+  const auto give_back = [&] {
+    const std::lock_guard<std::mutex> hold(c->events_lock);
+    c->pool.push_back(ev);
+  };
   if (profiling) {
-    if (!c->pool.empty()) {
-      ev = c->pool.back();
-      c->pool.pop_back();
-    } else {
+    {
+      const std::lock_guard<std::mutex> hold(c->events_lock);
+      if (!c->pool.empty()) {
+        ev = c->pool.back();
+        c->pool.pop_back();
+      }
+    }
+    if (ev.start == nullptr) {
       if (hipEventCreate(&ev.start) != hipSuccess) return OB_ERR_DEVICE;
       if (hipEventCreate(&ev.stop) != hipSuccess) {
         (void)hipEventDestroy(ev.start);
@@ -114,7 +127,7 @@ int timed(ob_ctx *c, ob::Kind kind, hipStream_t s, F &&launch, bool events = tru
       }
     }
     if (hipEventRecord(ev.start, s) != hipSuccess) {
-      c->pool.push_back(ev);
+      give_back();
       return OB_ERR_DEVICE;
     }
   }
@@ -126,9 +139,10 @@ int timed(ob_ctx *c, ob::Kind kind, hipStream_t s, F &&launch, bool events = tru
   const bool launched = hipGetLastError() == hipSuccess;
   if (profiling) {
     if (!launched || hipEventRecord(ev.stop, s) != hipSuccess) {
-      c->pool.push_back(ev);
+      give_back();
       return OB_ERR_DEVICE;
     }
+    const std::lock_guard<std::mutex> hold(c->events_lock);
     c->pending[kind].push_back(ev);
   }
   return launched ? OB_OK : OB_ERR_DEVICE;
@@ -998,6 +1012,7 @@ const char *ob_profile_kind_name(int32_t kind) {
 
 int ob_profile_read(ob_ctx *c, double *total_ms, int64_t *launches, int32_t reset) {
   if (c == nullptr || total_ms == nullptr || launches == nullptr) return OB_ERR_INVALID;
+  const std::lock_guard<std::mutex> hold(c->events_lock);
   for (int k = 0; k < ob::K_NUM_KINDS; ++k) {
     double sum = 0.0;
     for (auto &e : c->pending[k]) {

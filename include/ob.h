@@ -56,7 +56,8 @@
  * calls must pass buffers and a stream of that device, with it current.
  * Results are visible to later work on that stream.  Concurrent calls on one
  * context from several host threads, or on several streams at once, race on
- * the context's scratch and are not allowed.
+ * the context's scratch and are not allowed (but for the calls that fill a
+ * gradient row, below, which use none of it).
  *
  * Errors.  Calls return OB_OK or an ob_status code.  Argument errors are
  * detected before anything is enqueued.  A failed launch returns
@@ -368,9 +369,12 @@ int ob_cltk_step(ob_ctx *ctx, int64_t step, const void *grads, float *memory, in
  * `work` is the caller's scratch of at least the bytes that the matching
  * *_work call gives (host only; NULL when that is 0): each call writes what it
  * reads there, so it needs no clearing and may be reused by the next call on
- * the stream.  These calls use no scratch of the context: calls on different
- * streams may overlap as long as their buffers and work do not.  They allocate
- * nothing and may be captured into a HIP graph.
+ * the stream.  These calls use no scratch of the context: unlike its other
+ * calls, those on different streams may overlap, and several host threads may
+ * make them on one context at once, as long as their buffers and work do not
+ * overlap (the context is neither destroyed nor given another profiling
+ * setting meanwhile).  With profiling off they allocate nothing and may be
+ * captured into a HIP graph.
  * ------------------------------------------------------------------------ */
 
 /* Source: the jarxiv page on "Activations and Gradients Compression for

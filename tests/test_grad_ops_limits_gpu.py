@@ -2,6 +2,7 @@
 largest sizes, element counts past 2^31, and the choices by size that smaller
 tests do not reach.  Comparisons with torch run on the GPU, slice by slice."""
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -175,3 +176,69 @@ def test_a_checkpoint_resized_in_place_is_refused():
                 call()
     torch.cuda.synchronize()
     assert (grads == 3.0).all()
+
+
+# ---------------------------------------------------------------------------
+# one context, several streams and threads
+# ---------------------------------------------------------------------------
+def test_one_context_on_two_streams():
+    """Two chains of calls on one context, each on a stream and with buffers of its own, give what each gives alone."""
+    states = [base._chain_state(30), base._chain_state(40, rows=901)]
+    states[1]["opt"] = states[0]["opt"]
+    want = []
+    for s in states:
+        base._chain(**s)
+        torch.cuda.synchronize()
+        want.append(base._results(s))
+    for s in states:
+        for k in ("y", "out", "grads"):
+            s[k].zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, st in zip(states, streams):
+            with torch.cuda.stream(st):
+                base._chain(**s)
+    torch.cuda.synchronize()
+    for s, w in zip(states, want):
+        assert all(torch.equal(a, b) for a, b in zip(base._results(s), w))
+
+
+def test_one_context_in_four_threads_with_profiling():
+    """Every launch is counted once, and the results are those of the calls one after the other."""
+    calls, threads = 200, 4
+    states = [base._chain_state(50 + 10 * k, rows=300 + 77 * k) for k in range(threads)]
+    opt = states[0]["opt"]
+    want = []
+    for s in states:
+        s["opt"] = opt
+        base._chain(**s)
+        torch.cuda.synchronize()
+        want.append(base._results(s))
+        for k in ("y", "out", "grads"):
+            s[k].zero_()
+    torch.cuda.synchronize()
+    opt.profile(True)
+    errors = []
+
+    def work(s):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(calls):
+                    base._chain(**s)
+        except Exception as e:      # noqa: BLE001
+            errors.append(e)
+
+    runs = [threading.Thread(target=work, args=(s,)) for s in states]
+    for r in runs:
+        r.start()
+    for r in runs:
+        r.join()
+    torch.cuda.synchronize()
+    opt.profile(False)
+    counts = {k: n for k, (_, n) in opt.profile_read().items()}
+    assert not errors
+    for kind in ("embedding_lookup", "embedding_order", "embedding_sum", "linear_grad", "linear_join"):
+        assert counts[kind] == calls * threads, kind
+    for s, w in zip(states, want):
+        assert all(torch.equal(a, b) for a, b in zip(base._results(s), w))
