@@ -398,7 +398,8 @@ int ob_act_layout(int64_t rows, int64_t cols, int64_t *pitch, int64_t *code_byte
 
 /* Writes x's checkpoint and, with fn != OB_FN_NONE, y = fn(x) in the same
  * pass.  x and y have type dtype; y may be x itself (with the same ld),
- * and is NULL with OB_FN_NONE. */
+ * and is NULL with OB_FN_NONE.  In fp32 a value of fn is off by at most 2^-20
+ * of itself (16 half steps; below 2^-126 it may be 0). */
 int ob_act_save(int32_t format, int32_t fn, int64_t rows, int64_t cols, int32_t dtype, const void *x, int64_t ldx,
                 void *y, int64_t ldy, uint8_t *codes, uint8_t *scales, void *stream);
 
@@ -407,7 +408,8 @@ int ob_act_load(int32_t format, int64_t rows, int64_t cols, const uint8_t *codes
                 void *out, int64_t ldo, void *stream);
 
 /* dx = dy * fn'(checkpoint's values); dx may be dy itself (with the same ld).  fn is
- * not OB_FN_NONE. */
+ * not OB_FN_NONE.  In fp32 fn' = F + x*F' is off by at most 2^-19 of the larger
+ * of its two terms. */
 int ob_act_backward(int32_t format, int32_t fn, int64_t rows, int64_t cols, const uint8_t *codes, const uint8_t *scales,
                     int32_t dtype, const void *dy, int64_t lddy, void *dx, int64_t lddx, void *stream);
 

@@ -242,3 +242,114 @@ def test_one_context_in_four_threads_with_profiling():
         assert counts[kind] == calls * threads, kind
     for s, w in zip(states, want):
         assert all(torch.equal(a, b) for a, b in zip(base._results(s), w))
+
+
+# ---------------------------------------------------------------------------
+# fp32 activations
+# ---------------------------------------------------------------------------
+# Error counted in units u = 2^-24 (half a step of fp32, relative).  A rounded
+# operation costs 1; the hardware's exponential is off by one step, 2; its
+# argument's rounding is carried along, which costs one more product and leaves
+# nothing else: e = exp(-|a|) is off by 3.  A reciprocal with a Newton step: 1.1.
+#
+#   sigma = 1/(1 + e) for a > 0, e/(1 + e) below; e weighs e/(1 + e) <= 1/2 in the former:
+#     above 1.5 + 1 (sum) + 1.1 = 3.6, below 3 + 1 + 1.1 + 1 = 6.1; times x, 1 more.
+#   Phi, |x| >= 1.25: t (two roundings' 2.1) weighs at most 2 in P, P's own
+#     evaluation 3 and fit 0.7, e 3, two products 2: 12.9 below; above, that is
+#     weighed tail/(1 - tail) <= 0.12, and 1 more for the difference.
+#   Phi, |x| < 1.25: x*Q is off by 2 (evaluation) and 0.8 (fit), the sum by 1:
+#     below 2.8 * 0.394/0.106 + 1 = 11.4, for x >= -1 2.8 * 0.341/0.159 + 1 = 7.0,
+#     above 2.8 * 0.394/0.894 + 1 = 2.3.  Times x, 1 more.
+def _value_units(x, fn):
+    if fn == "gelu":
+        return np.where(x >= 0, 4.0, np.where(x >= -1, 8.0, 16.0))
+    return np.where(x >= 0, 5.0, 8.0)
+
+
+def _slope_error(x, fn):
+    """Both terms of act'(x): Phi or sigma as above, and x*gauss/sqrt(2 pi) (x/sqrt(2 pi) 2,
+    e 3, product fused) or sigma*(1 - sigma)*v'(x)*x (e 3, two reciprocals and sums 4.2, two
+    products 2; for gelu_tanh x*v' 5 more); the sum 1."""
+    if fn == "gelu":
+        s, units = ref._phi(x), 6.0
+    else:
+        s = ref._sigmoid(ref.C * (x + ref.K * x ** 3) if fn == "gelu_tanh" else x)
+        units = 10.0 if fn == "silu" else 15.0
+    slope = ref.act_slope(x, fn)
+    return (_value_units(x, fn) * s + units * np.abs(slope - s) + np.abs(slope)) * ref.U32
+
+
+def _dense(seed):
+    """Both signs, every size from 2^-20 to 12, most of them where most values lie."""
+    g = base._gen(seed)
+    x = torch.cat([torch.rand(60000, generator=g) * 24 - 12, torch.rand(60000, generator=g) * 2 - 1,
+                   torch.exp2(torch.rand(8000, generator=g) * 20 - 20) * (torch.randint(0, 2, (8000,), generator=g) * 2 - 1)])
+    return x.view(1000, 128)
+
+
+@pytest.mark.parametrize("fn", base.FNS)
+def test_fp32_activation_to_its_last_bits(fn):
+    x = _dense(60).to(DEV)
+    y = torch.empty_like(x)
+    ActCheckpoint(1000, 128, device=DEV).save(x, act=fn, y=y)
+    x64 = base._f64(x)
+    want = ref.act(x64, fn)
+    lim = np.abs(want) * _value_units(x64, fn) * ref.U32 + np.abs(x64) * 2.0 ** -126      # sigma below 2^-126 may be 0
+    off = np.abs(base._f64(y) - want)
+    assert (off <= lim).all(), (float((off / lim).max()), x64.flat[(off / lim).argmax()])
+
+
+@pytest.mark.parametrize("fn", base.FNS)
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_fp32_backward_to_its_last_bits(fn, fmt):
+    ck = ActCheckpoint(1000, 128, fmt, device=DEV)
+    ck.save(_dense(61).to(DEV))
+    xhat = ref.decoded(ck.codes.cpu().numpy(), ck.scales.cpu().numpy(), 128, fmt)
+    dy = torch.randn(1000, 128, generator=base._gen(62)).to(DEV)
+    dx = torch.empty_like(dy)
+    ck.act_backward(fn, dy, dx)
+    dy64, slope = base._f64(dy), ref.act_slope(xhat, fn)
+    # one rounding more for dy; what a factor below 2^-126 loses, times at most 2|x|(1 + 3*0.044715 x^2)
+    lim = np.abs(dy64) * (_slope_error(xhat, fn) + np.abs(slope) * ref.U32
+                          + 2.0 ** -126 * (1 + 2 * np.abs(xhat) * (1 + 3 * ref.K * xhat * xhat)))
+    off = np.abs(base._f64(dx) - dy64 * slope)
+    assert (off <= lim).all(), (float((off / lim).max()), xhat.flat[(off / lim).argmax()])
+
+
+@pytest.mark.parametrize("fn", base.FNS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_activation_of_infinities_and_huge_values(fn, dtype):
+    x = torch.tensor([[float("inf"), float("nan"), 3e38, 1e30, 1e15, 200.0, 64.0, 0.0, -64.0, -200.0, -1e15, -1e30, -3e38]],
+                     device=DEV).to(dtype)
+    y = torch.empty_like(x)
+    ActCheckpoint(1, x.shape[1], device=DEV).save(x, act=fn, y=y)
+    assert torch.equal(y[0, 2:8], x[0, 2:8]) and torch.isnan(y[0, 1]) and float(y[0, 0]) == float("inf")
+    assert (y[0, 9:] == 0).all()
+    assert float(y[0, 8].abs()) <= 1.04e-26      # silu: 64 * exp(-64) = 1.027e-26, half a bf16 step more 1.031e-26
+
+
+def test_save_of_more_tiles_than_one_launch_dimension():
+    """2^29 + 5 rows of one column are 2^24 + 1 tiles; the rows at both ends as
+    those of a matrix of their own."""
+    rows, n = (1 << 29) + 5, 4096 + 5
+    x = torch.zeros(rows, 1, device=DEV)
+    ends = torch.randn(2, n, 1, generator=base._gen(63)).to(DEV)
+    x[:n], x[-n:] = ends[0], ends[1]
+    ck = ActCheckpoint(rows, 1, "int8", device=DEV)
+    y = torch.full((rows, 1), 7.0, device=DEV)
+    ck.save(x, act="silu", y=y)
+    small = ActCheckpoint(n, 1, "int8", device=DEV)
+    out = torch.empty(n, 1, device=DEV)
+    for part, end in ((slice(0, n), ends[0]), (slice(rows - n, rows), ends[1])):
+        small.save(end, act="silu", y=out)
+        assert torch.equal(y[part], out)
+        # whole blocks of 32 rows: those of the small matrix begin at the same rows
+        at = 0 if part.start == 0 else part.start // 32
+        assert torch.equal(ck.codes[part, :1], small.codes[:, :1])
+        assert torch.equal(ck.scales[at: at + (n + 31) // 32, :1], small.scales[:, :1])
+    assert (y[n:-n] == 0).all()
+    dy = y
+    dy.fill_(1.0)
+    ck.act_backward("silu", dy, dy)
+    small.act_backward("silu", torch.ones(n, 1, device=DEV), out)
+    assert torch.equal(dy[-n:], out) and (dy[n:-n] == 0.5).all()
