@@ -362,8 +362,9 @@ int ob_cltk_step(ob_ctx *ctx, int64_t step, const void *grads, float *memory, in
  * type); padding and all other tensors and rows stay untouched.  With
  * accumulate != 0 they add to what the tensor's gradient holds (in fp32,
  * rounded once), otherwise they overwrite it.  Sums over tokens are fp32, in
- * an order that depends on the sizes alone: the same call gives the same
- * bits.  A call with no rows (tokens) reads nothing: its matrices and
+ * an order that the sizes, types, ids and, for dy, its row stride and alignment
+ * to 16 bytes settle: the same call gives the same bits, one with the same
+ * values in a dy of another stride or alignment may not.  A call with no rows (tokens) reads nothing: its matrices and
  * checkpoint may be NULL, and a gradient is written as 0 or left as it was.
  *
  * `work` is the caller's scratch of at least the bytes that the matching
@@ -399,7 +400,7 @@ int ob_act_layout(int64_t rows, int64_t cols, int64_t *pitch, int64_t *code_byte
 /* Writes x's checkpoint and, with fn != OB_FN_NONE, y = fn(x) in the same
  * pass.  x and y have type dtype; y may be x itself (with the same ld),
  * and is NULL with OB_FN_NONE.  In fp32 a value of fn is off by at most 2^-20
- * of itself (16 half steps; below 2^-126 it may be 0). */
+ * of itself (16 half steps), and where Phi or sigma is below 2^-126 it may be 0. */
 int ob_act_save(int32_t format, int32_t fn, int64_t rows, int64_t cols, int32_t dtype, const void *x, int64_t ldx,
                 void *y, int64_t ldy, uint8_t *codes, uint8_t *scales, void *stream);
 

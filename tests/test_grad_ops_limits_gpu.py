@@ -353,3 +353,34 @@ def test_save_of_more_tiles_than_one_launch_dimension():
     ck.act_backward("silu", dy, dy)
     small.act_backward("silu", torch.ones(n, 1, device=DEV), out)
     assert torch.equal(dy[-n:], out) and (dy[n:-n] == 0.5).all()
+
+
+# ---------------------------------------------------------------------------
+# the order of the sums
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dy_dtype", TYPES)
+@pytest.mark.parametrize("rows,out,inp", [(6000, 2056, 2050), (900, 264, 136)])
+def test_linear_grad_bits_by_layout(rows, out, inp, dy_dtype):
+    """Buffers of one row stride and alignment give the same bits, wherever they
+    lie; other strides and alignments may sum in another order, within the bound
+    of any order (n roundings, twice that for the matrix unit)."""
+    opt = OneBitAdam([out * inp, out], 1)
+    x = torch.randn(rows, inp, generator=base._gen(70))
+    ck = base._checkpoint(x.to(DEV), "e4m3")
+    dy = torch.randn(rows, out, generator=base._gen(71)).to(dy_dtype)
+
+    def run(extra, offset):
+        grads = torch.zeros(1, opt.N, device=DEV)
+        opt.linear_grad(0, 0, 1, ck, base._put(dy, dy_dtype, extra, offset)[0], grads)
+        return grads[0, : out * inp].view(out, inp).clone(), grads[0, opt.offsets[1]: opt.offsets[1] + out].clone()
+
+    xhat = torch.empty(rows, inp, device=DEV)
+    ck.load(xhat)
+    dy64 = dy.double().to(DEV)
+    mag = dy64.abs().t().contiguous() @ xhat.double().abs()
+    want = dy64.t().contiguous() @ xhat.double()
+    for extra, offset in ((0, 0), (8, 0), (0, 1), (3, 0)):
+        first, again = run(extra, offset), run(extra, offset + 64)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        assert ((first[0].double() - want).abs() <= 2 * (rows + 8) * ref.U32 * mag + 2.0 ** -126).all()
+        assert ((first[1].double() - dy64.sum(0)).abs() <= 2 * (rows + 8) * ref.U32 * dy64.abs().sum(0)).all()
