@@ -1,7 +1,6 @@
 """The gradient-making operators on the GPU at the ends of their ranges: the
 largest sizes, element counts past 2^31, and the choices by size that smaller
 tests do not reach.  Comparisons with torch run on the GPU, slice by slice."""
-import ctypes
 import threading
 
 import numpy as np
@@ -384,3 +383,141 @@ def test_linear_grad_bits_by_layout(rows, out, inp, dy_dtype):
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
         assert ((first[0].double() - want).abs() <= 2 * (rows + 8) * ref.U32 * mag + 2.0 ** -126).all()
         assert ((first[1].double() - dy64.sum(0)).abs() <= 2 * (rows + 8) * ref.U32 * dy64.abs().sum(0)).all()
+
+
+# ---------------------------------------------------------------------------
+# variants by size
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("grad", TYPES)
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("rows,out,inp,extra", [
+    (1500, 2056, 4100, 0),      # 256 x 256 tiles, rows of four columns each
+    (1500, 2056, 4101, 8),      # the same without
+    (6000, 2056, 2050, 0),      # and the rows in three slices
+    (16384, 2048, 2048, 0),     # four slices, whole tiles only
+])
+def test_linear_grad_of_large_tiles(rows, out, inp, extra, fmt, grad, bias):
+    """Whole numbers, sums of at most 16384 * 8 * 2 = 2^18 exact in fp32 and rounded once to the gradient's type."""
+    opt = OneBitAdam([5, out * inp, out, 9], 1, "bf16" if grad == torch.bfloat16 else "f32")
+    x = torch.randint(-8, 9, (rows, inp), generator=base._gen(80)).float().to(DEV)
+    dy, _ = base._put(torch.randint(-2, 3, (rows, out), generator=base._gen(81)).float(), torch.bfloat16, extra, 0)
+    ck = base._checkpoint(x, fmt)       # at most 8 = 2^3: exact in both formats
+    dw = dy.double().t().contiguous() @ x.double()
+    db = dy.double().sum(0)
+    a, b = opt.offsets[1], opt.offsets[2]
+    grads = torch.full((1, opt.N), 3.0, dtype=grad, device=DEV)
+    opt.linear_grad(0, 1, 2 if bias else None, ck, dy, grads)
+    weight, column = grads[0, a: a + out * inp].view(out, inp), grads[0, b: b + out]
+    assert torch.equal(weight, dw.to(grad))
+    assert torch.equal(column, db.to(grad) if bias else torch.full_like(column, 3.0))
+    old, old_b = weight.double(), column.double()
+    opt.linear_grad(0, 1, 2 if bias else None, ck, dy, grads, accumulate=True)
+    assert torch.equal(weight, (old + dw).to(grad))
+    assert torch.equal(column, (old_b + db).to(grad) if bias else old_b.to(grad))
+    base._others_untouched(opt, grads, 0, [1, 2] if bias else [1])
+
+
+@pytest.mark.parametrize("dy_dtype", TYPES)
+@pytest.mark.parametrize("tokens,dim", [(100, 66001), (40, 8 * 66000)])
+def test_embedding_grad_of_few_wide_tokens(tokens, dim, dy_dtype):
+    """More slices of columns than workgroups along them: each takes several,
+    with tokens of one row in several wavefronts.  Whole numbers, exact."""
+    vocab = 3
+    opt = OneBitAdam([70, vocab * dim, 4], 2)
+    ids = base._ids(tokens, vocab, 82)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(83)
+    dy = torch.randint(-4, 5, (tokens, dim), generator=gen, device=DEV).to(dy_dtype)
+    inside = ((ids >= 0) & (ids < vocab)).to(DEV)
+    want = torch.zeros(vocab, dim, device=DEV)
+    for v in range(vocab):
+        want[v] = dy[(ids == v).to(DEV)].float().sum(0)
+    dy[~inside] = float("nan")
+    grads = torch.full((2, opt.N), 3.0, device=DEV)
+    a = opt.offsets[1]
+    opt.embedding_grad(1, 1, dim, ids.to(DEV), dy, grads, scale=0.5)
+    got = grads[1, a: a + vocab * dim].view(vocab, dim)
+    assert torch.equal(got, 0.5 * want)
+    opt.embedding_grad(1, 1, dim, ids.to(DEV), dy, grads, scale=-1.0, accumulate=True)
+    assert torch.equal(got, -0.5 * want)
+    base._others_untouched(opt, grads, 1, [1])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,cols", [(5, 33), (100, 65), (97, 130), (40, 1)])
+def test_padding_bytes_reach_no_result(rows, cols, fmt):
+    """Columns past the last of a checkpoint hold what the buffer held: here the
+    scale of a NaN block and codes of NaN, 0 elsewhere for comparison."""
+    x = base._activations(rows, cols, 84).to(DEV)
+    dy = torch.randn(rows, 24, generator=base._gen(85)).to(DEV)
+    opt = OneBitAdam([24 * cols, 24], 1)
+    results = []
+    for code, scale in ((0xFF, 0xFF), (0x7F, 0xFF), (0, 0)):
+        ck = ActCheckpoint(rows, cols, fmt, device=DEV)
+        ck.codes.fill_(code)
+        ck.scales.fill_(scale)
+        ck.save(x)
+        out, dx = torch.empty_like(x), torch.empty_like(x)
+        grads = torch.zeros(1, opt.N, device=DEV)
+        ck.load(out)
+        ck.act_backward("gelu", out, dx)
+        opt.linear_grad(0, 0, 1, ck, dy, grads)
+        half = torch.zeros(1, opt.N, device=DEV)
+        opt.linear_grad(0, 0, 1, ck, dy.bfloat16(), half)
+        results.append((out, dx, grads, half))
+        assert all(torch.isfinite(t).all() for t in results[-1])
+    for r in results[:2]:
+        assert all(torch.equal(p, q) for p, q in zip(r, results[2]))
+
+
+# ---------------------------------------------------------------------------
+# past 2^31 elements
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_checkpoint_past_2_to_the_31_elements(fmt, dtype):
+    """2^19 + 39 rows of 4104 columns; the last blocks as those of a matrix of their own."""
+    rows, cols, n = (1 << 19) + 39, 4104, 32 * 40 + 7
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(86)
+    x = torch.zeros(rows, cols, dtype=dtype, device=DEV)
+    end = torch.randn(n, cols, generator=gen, device=DEV).to(dtype)
+    x[-n:] = end
+    ck, small = ActCheckpoint(rows, cols, fmt, device=DEV), ActCheckpoint(n, cols, fmt, device=DEV)
+    out = torch.empty(n, cols, dtype=dtype, device=DEV)
+    small.save(end, act="gelu", y=out)
+    ck.save(x, act="gelu", y=x)                        # in place
+    assert torch.equal(x[-n:], out) and int(torch.count_nonzero(x[:-n])) == 0
+    assert torch.equal(ck.codes[-n:, :cols], small.codes[:, :cols])
+    assert torch.equal(ck.scales[-small.scales.shape[0]:, :cols], small.scales[:, :cols])
+    ck.load(x)
+    small.load(out)
+    assert torch.equal(x[-n:], out) and int(torch.count_nonzero(x[:-n])) == 0
+    x.fill_(1.0)
+    ck.act_backward("silu", x, x)
+    small.act_backward("silu", torch.ones_like(out), out)
+    assert torch.equal(x[-n:], out) and int(torch.count_nonzero(x[:-n] != 0.5)) == 0
+
+
+@pytest.mark.parametrize("dy_dtype", TYPES)
+@pytest.mark.parametrize("wide", ["dy", "x"])
+def test_linear_grad_past_2_to_the_31_elements(wide, dy_dtype):
+    """2^20 + 5 rows of 2056 elements in dY (8 of them contracted) or in the
+    input; zero but for rows at both ends, whole numbers, exact in fp32."""
+    rows, n = (1 << 20) + 5, 700
+    out, inp = (8, 24) if wide == "dy" else (8, 2056)
+    opt = OneBitAdam([out * inp, out], 1)
+    x = torch.zeros(rows, inp, dtype=torch.bfloat16, device=DEV)
+    dy = torch.zeros(rows, 2056 if wide == "dy" else out, dtype=dy_dtype, device=DEV)[:, :out]
+    some = torch.cat([torch.arange(n), torch.arange(rows - n, rows)]).to(DEV)
+    xs = torch.randint(-8, 9, (2 * n, inp), generator=base._gen(87)).to(DEV)
+    ds = torch.randint(-4, 5, (2 * n, out), generator=base._gen(88)).to(DEV)
+    x[some], dy[some] = xs.bfloat16(), ds.to(dy_dtype)
+    ck = ActCheckpoint(rows, inp, "int8", device=DEV)
+    ck.save(x)
+    grads = torch.zeros(1, opt.N, device=DEV)
+    opt.linear_grad(0, 0, 1, ck, dy, grads)
+    assert torch.equal(grads[0, : out * inp].view(out, inp).double(), ds.double().t().contiguous() @ xs.double())
+    b = opt.offsets[1]
+    assert torch.equal(grads[0, b: b + out].double(), ds.double().sum(0))
