@@ -7,8 +7,8 @@
 // The contraction runs on the bf16 matrix units with fp32 accumulators.  X is
 // exact in bf16 (activation.h), so with bf16 dY the products are exact.  An
 // fp32 dY is cut into three bf16 parts of 8 significant bits each, which add
-// up to it exactly; three products per element keep fp32 accuracy at a third
-// of the bf16 rate.
+// up to it exactly but for bits below bf16's last, 2^-133; three products per
+// element keep fp32 accuracy at a third of the bf16 rate.
 //
 // Both operands lie with the contraction index t slowest ([t][o] and [t][i]),
 // and a matrix instruction wants 8 consecutive t per lane: the tiles go to LDS

@@ -419,7 +419,8 @@ int ob_act_backward(int32_t format, int32_t fn, int64_t rows, int64_t cols, cons
  *   dW[o][i] = sum over r of dy[r][o] * xhat[r][i],  db[o] = sum over r of dy[r][o]
  * tensor `weight` of the list is W [out_features][in_features], tensor `bias`
  * is b [out_features] (-1: none).  dy is [rows][out_features], fp32 or bf16;
- * products are exact and summed in fp32.  rows and in_features at most 2^24. */
+ * products are exact (of an fp32 dy, bits below 2^-133 are dropped) and summed
+ * in fp32.  rows and in_features at most 2^24. */
 int ob_linear_grad_work(int64_t rows, int64_t out_features, int64_t in_features, int32_t dy_dtype, int32_t bias,
                         int64_t *work_bytes);
 int ob_linear_grad(ob_ctx *ctx, int32_t worker, int32_t weight, int32_t bias, int64_t rows, int64_t out_features,

@@ -521,3 +521,31 @@ def test_linear_grad_past_2_to_the_31_elements(wide, dy_dtype):
     assert torch.equal(grads[0, : out * inp].view(out, inp).double(), ds.double().t().contiguous() @ xs.double())
     b = opt.offsets[1]
     assert torch.equal(grads[0, b: b + out].double(), ds.double().sum(0))
+
+
+# ---------------------------------------------------------------------------
+# tiny gradients
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows", [4, 64])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dy_dtype", TYPES)
+def test_linear_grad_of_tiny_values(rows, fmt, dy_dtype):
+    """One row of dY from 1e-28 down into the subnormals.  A bf16 dY and few
+    rows lose nothing but fp32's own rounding; of an fp32 dY, what its three
+    bf16 parts cannot hold, less than 2^-133 each, is lost."""
+    opt = OneBitAdam([16 * 8, 16], 1)
+    x = torch.zeros(rows, 8)
+    x[0] = torch.tensor([1.0, 2.0 ** 20, 2.0 ** -20, 1.5 * 2.0 ** -60, -1.0, 0.0, 3.0, 96.0])
+    dy = torch.zeros(rows, 16)
+    dy[0] = 1.2345678 * 10.0 ** -torch.arange(28.0, 44.0, dtype=torch.float64)
+    ck = base._checkpoint(x.to(DEV), fmt)
+    dyg = dy.to(dy_dtype).to(DEV)
+    grads = torch.zeros(1, opt.N, device=DEV)
+    opt.linear_grad(0, 0, 1, ck, dyg, grads)
+    dy64, x64 = base._f64(dyg)[0], x[0].double().numpy()
+    lost = 2.0 ** -133 if rows >= 8 and dy_dtype == torch.float32 else 0.0
+    want = np.outer(dy64, x64)
+    lim = lost * np.abs(x64) + np.abs(want) * ref.U32 + 2.0 ** -150       # the last: half of fp32's smallest step
+    assert (np.abs(base._f64(grads[0, :128].view(16, 8)) - want) <= lim).all()
+    b = opt.offsets[1]
+    assert (np.abs(base._f64(grads[0, b: b + 16]) - dy64) <= lost).all()
