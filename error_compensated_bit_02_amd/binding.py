@@ -138,16 +138,18 @@ def _device(t: torch.Tensor, name: str) -> torch.device:
 
 def _matrix(t: torch.Tensor, rows: int, cols: int, device, name: str):
     """(pointer, dtype code, row stride) of a [rows][cols] matrix with adjacent columns."""
-    if _device(t, name) != device:
-        raise OneBitError(f"{name} is on {t.device}, expected {device}")
+    if t.device != device:
+        raise OneBitError(f"{name} is on {_device(t, name)}, expected {device}")
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise OneBitError(f"{name} has dtype {t.dtype}, expected one of {tuple(_DTYPES)}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise OneBitError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
-    if cols > 1 and t.stride(1) != 1:
-        raise OneBitError(f"{name}'s columns must be adjacent (stride {t.stride(1)})")
-    ld = t.stride(0) if rows > 1 else cols
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise OneBitError(f"{name}'s columns must be adjacent (stride {step})")
+    if rows <= 1:
+        ld = cols
     if ld < cols:
         raise OneBitError(f"{name}'s rows overlap (row stride {ld}, {cols} columns)")
     return t.data_ptr(), code, ld
@@ -168,7 +170,7 @@ class _on:
         self.index = device.index
 
     def __enter__(self):
-        self.before = torch.cuda.current_device()
+        self.before = torch._C._cuda_getDevice()   # tensors of a device exist, so torch has begun to use it
         if self.before != self.index:
             torch.cuda.set_device(self.index)
 
@@ -254,40 +256,40 @@ class ActCheckpoint:
     def save(self, x, act: str = "none", y=None, stream=None) -> None:
         """Keep x; with an activation also y = act(x) in the same pass (y may be x)."""
         fn = self._fn(act)
-        xp, dtype, ldx = _matrix(x, self.rows, self.cols, self.device, "x")
-        yp, ldy = None, self.cols
+        xp, dtype, ldx = _matrix(x, self._rows, self._cols, self._device, "x")
+        yp, ldy = None, self._cols
         if (y is None) != (fn == 0):
             raise OneBitError("y is given with an activation, and only then")
         if y is not None:
-            yp, ydtype, ldy = _matrix(y, self.rows, self.cols, self.device, "y")
+            yp, ydtype, ldy = _matrix(y, self._rows, self._cols, self._device, "y")
             if ydtype != dtype:
                 raise OneBitError(f"y has dtype {y.dtype}, x {x.dtype}")
         codes, scales = self._pointers()
-        with _on(self.device):
-            st = self.lib.ob_act_save(self._format, fn, self.rows, self.cols, dtype, xp, ldx, yp, ldy,
-                                      codes, scales, _stream_on(stream, self.device))
+        with _on(self._device):
+            st = self.lib.ob_act_save(self._format, fn, self._rows, self._cols, dtype, xp, ldx, yp, ldy,
+                                      codes, scales, _stream_on(stream, self._device))
         _check(st, "ob_act_save")
 
     def load(self, out, stream=None) -> None:
         """Write the kept values (exact in float32 and in bfloat16)."""
-        op, dtype, ldo = _matrix(out, self.rows, self.cols, self.device, "out")
+        op, dtype, ldo = _matrix(out, self._rows, self._cols, self._device, "out")
         codes, scales = self._pointers()
-        with _on(self.device):
-            st = self.lib.ob_act_load(self._format, self.rows, self.cols, codes, scales, dtype, op, ldo,
-                                      _stream_on(stream, self.device))
+        with _on(self._device):
+            st = self.lib.ob_act_load(self._format, self._rows, self._cols, codes, scales, dtype, op, ldo,
+                                      _stream_on(stream, self._device))
         _check(st, "ob_act_load")
 
     def act_backward(self, act: str, dy, dx, stream=None) -> None:
         """dx = dy * act'(kept values); dx may be dy."""
         fn = self._fn(act)
-        gp, dtype, lddy = _matrix(dy, self.rows, self.cols, self.device, "dy")
-        xp, xdtype, lddx = _matrix(dx, self.rows, self.cols, self.device, "dx")
+        gp, dtype, lddy = _matrix(dy, self._rows, self._cols, self._device, "dy")
+        xp, xdtype, lddx = _matrix(dx, self._rows, self._cols, self._device, "dx")
         if xdtype != dtype:
             raise OneBitError(f"dx has dtype {dx.dtype}, dy {dy.dtype}")
         codes, scales = self._pointers()
-        with _on(self.device):
-            st = self.lib.ob_act_backward(self._format, fn, self.rows, self.cols, codes, scales, dtype,
-                                          gp, lddy, xp, lddx, _stream_on(stream, self.device))
+        with _on(self._device):
+            st = self.lib.ob_act_backward(self._format, fn, self._rows, self._cols, codes, scales, dtype,
+                                          gp, lddy, xp, lddx, _stream_on(stream, self._device))
         _check(st, "ob_act_backward")
 
 
@@ -519,11 +521,11 @@ class OneBitAdam:
                     stream=None) -> None:
         """Weight (tensor `weight`) and bias (tensor `bias`, or None) gradient of a
         linear layer from its input's checkpoint, into row `worker` of grads."""
-        rows, cols = checkpoint.rows, checkpoint.cols
+        rows, cols = checkpoint._rows, checkpoint._cols
         weight = self._tensor(weight, "weight")
         bias = -1 if bias is None else self._tensor(bias, "bias")
         out = self.numel[weight] // cols
-        self._on_device(checkpoint.codes, "checkpoint")
+        self._on_device(checkpoint._codes, "checkpoint")
         gp, gdt, lddy = _matrix(dy, rows, out, self.device, "dy")
         self._on_device(grads, "grads")
         codes, scales = checkpoint._pointers()

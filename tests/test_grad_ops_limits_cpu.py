@@ -50,8 +50,8 @@ class DeviceMatrix(DeviceBytes):
     def dim(self):
         return 2
 
-    def stride(self, d):
-        return (70, 1)[d]
+    def stride(self, *d):
+        return (70, 1)[d[0]] if d else (70, 1)
 
 
 def _checkpoint_of_stand_ins():
