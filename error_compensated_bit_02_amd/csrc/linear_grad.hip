@@ -21,14 +21,17 @@
 // Precision.  Sums are fp32 throughout, the parts of a split contraction too;
 // the only rounding to fewer bits is the one to the gradient's type at the end.
 //
-// Measured on MI355X (bias included).  8192 x 2048 over 16384 tokens, bf16 dY:
-// 402 us with e4m3 (1366 TFLOP/s; the library's bf16 product of that shape,
-// X in bf16 and no bias, 457 us), 480 us with int8, whose conversion takes
-// five vector instructions for two elements instead of one.  With constant
-// inputs it takes 336 us: the card lowers its clock under load.  Of the 390 us
-// of the contraction, copies cost 70 (left out: 320) and the reads of LDS 65.
-// 1024 x 1024 over 4096 tokens 30 us: 256 workgroups of 16 turns, whose start,
-// end and join are half of it.  1000 x 2048 over 777 in fp32 35 us.
+// Measured on MI355X (a call, bias included).  8192 x 2048 over 16384 tokens, bf16
+// dY: 400 us with e4m3 (396 to 430 as the card's clock goes, 1280-1390 TFLOP/s; the
+// library's bf16 product of that shape, X in bf16 and no bias, 457 us), 470 us with
+// int8, whose conversion takes five vector instructions for two elements instead
+// of one.  With constant inputs it takes 340 us: the card lowers its clock under
+// load.  1024 x 1024 over 4096 tokens 30 us, in fp32 50: 256 (512) workgroups of 16
+// turns.  A lone tile's turn takes 0.82 us where its products need 0.21: one
+// wavefront a SIMD has nobody to fill its waits (the matrix units are busy 12% of
+// the kernel's cycles, 64% in the large case); start, end, the split's parts and
+// the join are the rest.  1000 x 2048 over 777 in fp32 35 us, 4096 x 4096 over 8192
+// 807.
 #include "internal.h"
 #include "activation.h"
 
@@ -656,11 +659,17 @@ struct Plan {
 // dY): a 64-token turn of the large tile 1.55 us, of one small tile on a CU
 // 0.82, of two together 1.07; a workgroup's start and end 11 and 5 us; a slice
 // costs the writing and reading of its fp32 part at about 3 TB/s, and the
-// join.  16384 x 2048 x 2048: large tile in 4 slices 126 us, small in 2 146 us;
-// 4096 x 4096 x 1024: 52.3 against 51.9; 16384 x 8192 x 2048: large tile whole
-// 411 us (in 2 slices 465), small 549.  Where dY is not copied (or fp32) only
-// the small tile is built: the large one's registers would not hold a turn of
-// dY as well (it measured 236-277 us against 192 at 16384 x 2048 x 2048).
+// join.  Writing dW, which every plan does, is left out.  16384 x 2048 x 2048:
+// large tile in 4 slices 126 us, small in 2 146 us; 4096 x 4096 x 1024: 52.3
+// against 51.9; 16384 x 8192 x 2048: large tile whole 411 us (in 2 slices 465),
+// small 549.  Where dY is not copied (or fp32) only the small tile is built: the
+// large one's registers would not hold a turn of dY as well (it measured 236-277
+// us against 192 at 16384 x 2048 x 2048).
+// The constants are those of e4m3 with bf16 dY copied to LDS.  int8, fp32 dY and dY
+// through registers are planned with the same ones, which rank slices, but are
+// below their times: estimated and measured 408 and 470 us for int8 16384 x 8192 x
+// 2048, 155 and 192 for dY through registers at 16384 x 2048 x 2048, 553 and 807
+// for fp32 8192 x 4096 x 4096, 35 and 50 for fp32 4096 x 1024 x 1024.
 Plan plan_of(int64_t rows, int64_t out, int64_t in, bool dy_bf16, bool copies, bool bias) {
   Plan p{};
   if (rows < kFewRows) return p;

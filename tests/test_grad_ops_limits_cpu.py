@@ -1,9 +1,11 @@
 """Host side of the gradient-making operators at the ends of their ranges."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
+import grad_ops as ref
 from error_compensated_bit_02_amd import ActCheckpoint, OneBitError, binding
 
 INVALID = 1
@@ -103,3 +105,26 @@ def test_a_checkpoint_whose_memory_changed_is_refused(monkeypatch, which, change
         with pytest.raises(OneBitError, match="resized or moved"):
             call()
     assert len(calls) == 3
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_the_stated_error_of_a_checkpoint(fmt):
+    """e4m3: at most half a step of the element, 2^-4, or of the format's
+    smallest, 2^-10 times the scale.  int8: half the scale, which is at most
+    1/127 of the block's largest magnitude, or 2^-112 where the scale is the
+    smallest there is.  (The GPU's values equal ref.quantised bit for bit.)"""
+    g = torch.Generator()
+    g.manual_seed(1)
+    x = torch.randn(320, 40, generator=g).double().numpy()
+    x *= 2.0 ** np.linspace(-125, 100, 40)                     # blocks of every size, the last scale among them
+    x[::3] *= 2.0 ** -9
+    x[1, :] = 448.0 / 0.0009 * np.abs(x[0, :])                 # small elements of a large block
+    err = np.abs(ref.quantised(x, fmt) - x)
+    scale = np.repeat(2.0 ** (ref.scale_bytes(x, fmt).astype(np.float64) - 127), ref.BLOCK, axis=0)
+    top = np.repeat(np.abs(x).reshape(10, 32, 40).max(axis=1), ref.BLOCK, axis=0)
+    if fmt == "e4m3":
+        assert (err <= np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -10 * scale)).all()
+        assert (err > 2.0 ** -4 * np.abs(x)).any()             # the second part is needed
+    else:
+        assert (err <= np.maximum(top / 127, 2.0 ** -112)).all()
+        assert (err > top / 127).any()
