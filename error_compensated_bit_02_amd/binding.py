@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libob.so")
 OB_OK, OB_ERR_INVALID, OB_ERR_ALIGN, OB_ERR_NOMEM, OB_ERR_DEVICE, OB_ERR_SCRATCH = 0, 1, 2, 3, 4, 5
 OB_GRAD_F32, OB_GRAD_BF16 = 0, 1
 OB_ID_I32, OB_ID_I64 = 0, 1
+OB_MOMENTS_F32, OB_MOMENTS_8BIT = 0, 1
 ACT_FORMATS = {"e4m3": 0, "int8": 1}
 ACT_FNS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
 
@@ -40,6 +41,9 @@ SIGNATURES = {
     "ob_step_residual_noalloc": (ctypes.c_int, [_c_void_p, _i32] + [_c_void_p] * 10 + [_f64, _c_void_p]),
     "ob_materialize": (ctypes.c_int, [_c_void_p] * 9),
     "ob_warmup_step": (ctypes.c_int, [_c_void_p] * 5 + [_f64, _f64, _c_void_p]),
+    "ob_adamw_step": (ctypes.c_int, [_c_void_p, _i32] + [_c_void_p] * 8 + [_i64, _f64, _f64, _f64, _c_void_p,
+                                                                          ctypes.c_uint64, _c_void_p]),
+    "ob_adamw_load": (ctypes.c_int, [_c_void_p] * 5 + [_i32] + [_c_void_p] * 3),
     "ob_begin_compression": (ctypes.c_int, [_c_void_p] * 4),
     "ob_set_server_chunks": (ctypes.c_int, [_c_void_p, _i32]),
     "ob_server_scale_count": (_i32, [_c_void_p]),
@@ -457,6 +461,71 @@ class OneBitAdam:
             self._ctx, self._grad_ptr(grads), _ptr(m, f32, self.N, "m"), _ptr(v, f32, self.N, "v"),
             _ptr(params, f32, self.N, "params"), float(beta2), float(lr), _stream(stream))
         _check(st, "ob_warmup_step")
+
+    def adamw_state(self, moments: str = "f32", device=None) -> Dict[str, torch.Tensor]:
+        """Zero-filled moments for adamw_step: m, v [N] float32 ("f32"), or m, v [N] and
+        m_scale, v_scale [N/64] uint8 ("8bit")."""
+        if moments not in ("f32", "8bit"):
+            raise OneBitError(f"unknown moments {moments!r}, expected 'f32' or '8bit'")
+        d = self.device if device is None else torch.device(device)
+        if moments == "f32":
+            return {k: torch.zeros(self.N, dtype=torch.float32, device=d) for k in ("m", "v")}
+        return {k + end: torch.zeros(n, dtype=torch.uint8, device=d)
+                for k in ("m", "v") for end, n in (("", self.N), ("_scale", self.Nw))}
+
+    def _moments(self, state):
+        """(moments code, m, m_scale, v, v_scale) of a state dict."""
+        m, v = state["m"], state["v"]
+        self._on_device(m, "m")
+        self._on_device(v, "v")
+        if m.dtype == torch.float32:
+            if "m_scale" in state or "v_scale" in state:
+                raise OneBitError("float32 moments have no scales")
+            f32 = (torch.float32,)
+            return OB_MOMENTS_F32, _ptr(m, f32, self.N, "m"), None, _ptr(v, f32, self.N, "v"), None
+        u8 = (torch.uint8,)
+        self._on_device(state["m_scale"], "m_scale")
+        self._on_device(state["v_scale"], "v_scale")
+        return (OB_MOMENTS_8BIT, _ptr(m, u8, self.N, "m"), _ptr(state["m_scale"], u8, self.Nw, "m_scale"),
+                _ptr(v, u8, self.N, "v"), _ptr(state["v_scale"], u8, self.Nw, "v_scale"))
+
+    def adamw_step(self, grads, state, params, step, lr, beta2=0.999, weight_decay=0.0, decay=None, grad_scale=None,
+                   model=None, seed=0, stream=None) -> None:
+        """One AdamW step on the workers' average gradient (see include/ob.h).  state: adamw_state's dict;
+        decay: [T] float32 factors of the weight decay; grad_scale: one float32 on the device; model: [N]
+        bfloat16, the new parameters; seed: of the 8-bit moments' rounding, another one every step."""
+        kind, m, ms, v, vs = self._moments(state)
+        self._on_device(grads, "grads")
+        self._on_device(params, "params")
+        f32 = (torch.float32,)
+        for t, name in ((decay, "decay"), (grad_scale, "grad_scale"), (model, "model")):
+            if t is not None:
+                self._on_device(t, name)
+        if not 0 <= int(seed) < 1 << 64:
+            raise OneBitError(f"seed {seed} is not a 64-bit unsigned integer", OB_ERR_INVALID)
+        with _on(self.device):
+            st = self.lib.ob_adamw_step(
+                self._ctx, kind, self._grad_ptr(grads), None if grad_scale is None else _ptr(grad_scale, f32, 1, "grad_scale"),
+                m, ms, v, vs, _ptr(params, f32, self.N, "params"),
+                None if model is None else _ptr(model, (torch.bfloat16,), self.N, "model"), int(step), float(lr),
+                float(beta2), float(weight_decay), None if decay is None else _ptr(decay, f32, self.T, "decay"),
+                int(seed), _stream_on(stream, self.device))
+        _check(st, "ob_adamw_step")
+
+    def adamw_load(self, state, m, v, stream=None) -> None:
+        """The values of 8-bit moments into m, v [N], both float32 (exact) or both bfloat16."""
+        kind, mc, ms, vc, vs = self._moments(state)
+        if kind != OB_MOMENTS_8BIT:
+            raise OneBitError("float32 moments are their values")
+        self._on_device(m, "m")
+        self._on_device(v, "v")
+        if m.dtype != v.dtype:
+            raise OneBitError(f"m has dtype {m.dtype}, v {v.dtype}")
+        both = tuple(_DTYPES)
+        mp, vp = _ptr(m, both, self.N, "m"), _ptr(v, both, self.N, "v")
+        with _on(self.device):
+            st = self.lib.ob_adamw_load(self._ctx, mc, ms, vc, vs, _DTYPES[m.dtype], mp, vp, _stream_on(stream, self.device))
+        _check(st, "ob_adamw_load")
 
     def begin_compression(self, err_w, err_s, stream=None) -> None:
         """Zero the error buffers at the switch from warmup to compression."""

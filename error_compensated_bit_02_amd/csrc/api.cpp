@@ -28,6 +28,7 @@ struct ob_ctx {
   int32_t T = 0;
   int32_t W = 0;
   bool bf16 = false;
+  double beta1 = 0.0;
   float c1 = 0.0f;
   float c2 = 0.0f;
   float eps = 0.0f;
@@ -73,7 +74,8 @@ const char *const kKindNames[] = {
     "server_pass2", "server_pass2_update", "apply_update", "worker_residual",
     "server_residual", "update_residual", "materialize", "warmup", "zero_errors",
     "trust_norms", "trust_ratio", "cltk_select", "cltk_gather", "cltk_average",
-    "embedding_lookup", "embedding_order", "embedding_sum", "linear_grad", "linear_join"};
+    "embedding_lookup", "embedding_order", "embedding_sum", "linear_grad", "linear_join",
+    "adamw", "adamw_load"};
 static_assert(sizeof(kKindNames) / sizeof(kKindNames[0]) == ob::K_NUM_KINDS,
               "one name per kernel kind");
 
@@ -445,6 +447,7 @@ int ob_init(ob_ctx **out, int32_t num_tensors, const int64_t *numel, int32_t num
   c->T = num_tensors;
   c->W = num_workers;
   c->bf16 = grad_dtype == OB_GRAD_BF16;
+  c->beta1 = beta1;
   c->c1 = static_cast<float>(beta1);
   c->c2 = static_cast<float>(1.0 - beta1);
   c->eps = static_cast<float>(eps);
@@ -689,6 +692,60 @@ int ob_begin_compression(ob_ctx *c, float *err_w, float *err_s, void *stream) {
   if (st) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(c, ob::K_ZERO_ERRORS, s, [&] { ob::launch_zero_errors(c->geo, err_w, err_s, s); });
+}
+
+int ob_adamw_step(ob_ctx *c, int32_t moments, const void *grads, const float *grad_scale, void *m, uint8_t *m_scale,
+                  void *v, uint8_t *v_scale, float *params, uint16_t *model, int64_t step, double lr, double beta2,
+                  double weight_decay, const float *decay, uint64_t seed, void *stream) {
+  if (c == nullptr || (moments != OB_MOMENTS_F32 && moments != OB_MOMENTS_8BIT) || step < 1 ||
+      !std::isfinite(static_cast<float>(lr)) || !std::isfinite(beta2) || beta2 < 0.0 || beta2 >= 1.0 ||
+      !std::isfinite(weight_decay) || weight_decay < 0.0)
+    return OB_ERR_INVALID;
+  const bool eight = moments == OB_MOMENTS_8BIT;
+  if (!eight && (m_scale != nullptr || v_scale != nullptr)) return OB_ERR_INVALID;
+  ob::AdamwArgs a{};
+  a.grads = grads;
+  a.grad_scale = grad_scale;
+  a.m = m;
+  a.v = v;
+  a.m_scale = m_scale;
+  a.v_scale = v_scale;
+  a.params = params;
+  a.model = model;
+  a.decay = decay;
+  a.c1 = c->c1;
+  a.c2 = c->c2;
+  a.b2 = static_cast<float>(beta2);
+  a.cb2 = static_cast<float>(1.0 - beta2);
+  a.eps = c->eps;
+  a.fade = static_cast<float>(lr * weight_decay);
+  a.step = static_cast<float>(lr / (1.0 - std::pow(c->beta1, static_cast<double>(step))));
+  a.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
+  if (!std::isfinite(a.fade) || !std::isfinite(a.step) || !std::isfinite(a.root)) return OB_ERR_INVALID;
+  const uint32_t lo = static_cast<uint32_t>(seed), hi = static_cast<uint32_t>(seed >> 32);
+  a.key = ob::mix32(lo ^ ob::mix32(hi + 0x9E3779B9u));
+  int st = check_ptrs(grads, m, v, params);
+  if (st == OB_OK && eight) st = check_ptrs(m_scale, v_scale);
+  if (st == OB_OK && model != nullptr) st = check_ptr(model);
+  if (st == OB_OK && grad_scale != nullptr) st = check_elements(grad_scale, 4);
+  if (st == OB_OK && decay != nullptr) st = check_elements(decay, 4);
+  if (st) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(c, ob::K_ADAMW, s, [&] { ob::launch_adamw(c->geo, c->bf16, eight, a, s); });
+}
+
+int ob_adamw_load(ob_ctx *c, const uint8_t *m, const uint8_t *m_scale, const uint8_t *v, const uint8_t *v_scale,
+                  int32_t dtype, void *m_out, void *v_out, void *stream) {
+  if (c == nullptr || !dtype_ok(dtype)) return OB_ERR_INVALID;
+  const int st = check_ptrs(m, m_scale, v, v_scale, m_out, v_out);
+  if (st) return st;
+  ob::AdamwArgs a{};
+  a.m = const_cast<uint8_t *>(m);
+  a.v = const_cast<uint8_t *>(v);
+  a.m_scale = const_cast<uint8_t *>(m_scale);
+  a.v_scale = const_cast<uint8_t *>(v_scale);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(c, ob::K_ADAMW_LOAD, s, [&] { ob::launch_adamw_load(c->geo, a, dtype == OB_GRAD_BF16, m_out, v_out, s); });
 }
 
 int ob_set_server_chunks(ob_ctx *c, int32_t chunks) {

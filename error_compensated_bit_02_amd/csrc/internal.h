@@ -105,6 +105,8 @@ enum Kind {
   K_EMBED_SUM,
   K_LINEAR_GRAD,
   K_LINEAR_JOIN,
+  K_ADAMW,
+  K_ADAMW_LOAD,
   K_NUM_KINDS
 };
 
@@ -185,6 +187,35 @@ struct WarmupArgs {
   float *params;             // [N]
   float c1, c2, b2, cb2, lr, eps;
 };
+
+// AdamW over the list, its moments fp32 or 8-bit (adamw.hip).
+constexpr int kMomentBlock = 64;   // elements of the list that share a scale byte in 8-bit moments
+struct AdamwArgs {
+  const void *grads;         // [W][N] fp32 or bf16
+  const float *grad_scale;   // one factor for all gradients, or null
+  void *m;                   // [N] fp32, or codes
+  void *v;                   // [N] fp32, or codes of its root
+  uint8_t *m_scale;          // [N/64], 8-bit moments only
+  uint8_t *v_scale;
+  float *params;             // [N]
+  uint16_t *model;           // [N] the new parameters as bf16, or null
+  const float *decay;        // [T] factors of the weight decay, or null
+  float c1, c2, b2, cb2, eps;
+  float fade;                // lr * weight_decay
+  float step;                // lr / (1 - beta1^t)
+  float root;                // 1 / sqrt(1 - beta2^t)
+  uint32_t key;              // of the rounding's dither
+};
+// A bijection of 32 bits whose output bits each depend on all input bits (the
+// finalizer of MurmurHash3, public domain).
+__host__ __device__ inline uint32_t mix32(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x85EBCA6Bu;
+  x = (x ^ (x >> 13)) * 0xC2B2AE35u;
+  return x ^ (x >> 16);
+}
+void launch_adamw(const Geometry &g, bool bf16, bool eight, const AdamwArgs &a, hipStream_t s);
+// The 8-bit moments' values as fp32 or bf16.
+void launch_adamw_load(const Geometry &g, const AdamwArgs &a, bool bf16, void *m, void *v, hipStream_t s);
 
 // Cyclic local top-k codec (topk.hip).
 struct TopkArgs {

@@ -107,6 +107,11 @@ typedef enum {
   OB_FN_SILU = 3        /* x / (1 + exp(-x)) */
 } ob_act_fn;
 
+typedef enum {
+  OB_MOMENTS_F32 = 0,   /* Adam's moments as fp32 */
+  OB_MOMENTS_8BIT = 1   /* as 8-bit codes with a scale byte for every 64 elements */
+} ob_moments;
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char *ob_status_string(int status);
 
@@ -271,6 +276,52 @@ int ob_materialize(ob_ctx *ctx, const float *x_w, const float *scale_w, const fl
  * lr finite. */
 int ob_warmup_step(ob_ctx *ctx, const void *grads, float *m, float *v, float *params,
                    double beta2, double lr, void *stream);
+
+/* Source: the 1-bit Adam review, Proposed method, bullet 1 (the warmup is
+ * Adam at full precision).  AdamW's form of it (bias correction, decay beside
+ * the gradient) and the 8-bit moments are this library's.
+ *
+ * One AdamW step over the whole list, on the workers' average gradient:
+ *   g    = (sum over w = 0..W-1, ascending, from +0, of g_w[i]) / W, times *grad_scale if given
+ *   m[i] = c1*m[i] + c2*g;  v[i] = fp32(beta2)*v[i] + fp32(1 - beta2)*(g*g);  r = sqrt(v[i])
+ *   p[i] = (p[i] - p[i]*(fp32(lr*weight_decay)*decay[t])) - (m[i] / (r*root + eps))*rate
+ * with rate = fp32(lr / (1 - beta1^step)), root = fp32(1 / sqrt(1 - beta2^step)),
+ * step >= 1, every fp32 operation rounded once.  decay [T] (device; NULL: 1
+ * for every tensor) scales the decay by tensor, *grad_scale (device, one float;
+ * NULL: none) all gradients: a clipping factor that the device has computed.
+ * With model [N] bf16 not NULL the new parameters are also written there, rounded
+ * to nearest even: what ob_linear multiplies with.  grads [W][N] read; m, v
+ * [N] and params [N] read and overwritten; lr finite, weight_decay >= 0, beta2 in [0, 1);
+ * decay and *grad_scale need their element's alignment only.
+ * A captured call keeps its step, lr and seed at every replay.
+ *
+ * moments = OB_MOMENTS_F32: m, v [N] fp32; m_scale and v_scale are NULL.
+ * moments = OB_MOMENTS_8BIT: m, v [N] are codes, m_scale, v_scale [N/64] scale
+ * bytes: a block of 64 consecutive elements (no block spans two tensors, and
+ * padding is no part of one) stands for code * 2^(scale - 127), the scale the
+ * smallest, and at least 2^-111, for which the block's largest magnitude fits.  m:
+ * e4m3 codes; magnitudes past 1.875 * 2^127 count as that.  v: codes of its root,
+ * code 16k + f standing for f if k = 0 and (16 + f)*2^(k-1) otherwise (the
+ * largest is 31 * 2^14); v is the square, in fp32.  The step reads these values, computes
+ * as above and writes m and r back, rounded with a dither: of h = M(lo(i) ^ (key + hi(i)*0x9E3779B9)),
+ * i the element's place in the list, M(x) = x ^= x >> 16, x *= 0x85EBCA6B, x ^= x >> 13, x *=
+ * 0xC2B2AE35, x ^= x >> 16 and key = M(lo(seed) ^ M(hi(seed) + 0x9E3779B9)), all modulo 2^32 (lo,
+ * hi: the 32-bit halves), the low 16 bits are m's and the high 16 r's.  A magnitude
+ * between two codes takes the upper one if its remainder in steps plus the
+ * dither / 2^16 reaches 1 (below the smallest normal code the remainder is first rounded
+ * to nearest even at 2^-20 of a step, of r 2^-19), so rounding is unbiased over seeds: give
+ * every step another seed.  A root above 0 takes code 1 at least.  A block with a NaN or an
+ * infinity has scale 255 and codes 0 and stands for NaN throughout.  Zero-filled
+ * buffers stand for zeros: the state to start from.  m_scale and v_scale are
+ * aligned to 16 bytes as well. */
+int ob_adamw_step(ob_ctx *ctx, int32_t moments, const void *grads, const float *grad_scale, void *m, uint8_t *m_scale,
+                  void *v, uint8_t *v_scale, float *params, uint16_t *model, int64_t step, double lr, double beta2,
+                  double weight_decay, const float *decay, uint64_t seed, void *stream);
+
+/* The values of 8-bit moments: m_out, v_out [N] of type dtype, written (fp32:
+ * exact; what the compression phase starts from).  Padding stays untouched. */
+int ob_adamw_load(ob_ctx *ctx, const uint8_t *m, const uint8_t *m_scale, const uint8_t *v, const uint8_t *v_scale,
+                  int32_t dtype, void *m_out, void *v_out, void *stream);
 
 /* Source: the 1-bit Adam review, Proposed method, bullets 1 and 2 (the switch
  * to compressed momentum SGD, with the variance kept fixed from then on).

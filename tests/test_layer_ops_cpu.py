@@ -1,0 +1,50 @@
+"""Host side of the AdamW step and the linear layer's calls: refusals that come
+before any device work (the library is called with stand-in addresses that no
+refused call touches), and the tests' own reference of the 8-bit moments."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import layer_ops as ref
+from error_compensated_bit_02_amd import binding
+
+P = 1 << 20            # a stand-in device address, aligned to 16 bytes
+INVALID, ALIGN = 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.load_library()
+
+
+def test_adamw_without_a_context_is_refused(lib):
+    assert lib.ob_adamw_step(None, 0, P, None, P, None, P, None, P, None, 1, 1e-3, 0.999, 0.0, None, 0, None) == INVALID
+    assert lib.ob_adamw_load(None, P, P, P, P, 0, P, P, None) == INVALID
+
+
+def test_the_reference_rounds_both_ways_and_keeps_codes():
+    """Values on a code stay there whatever the dither; others take one of their two neighbours."""
+    rng = np.random.default_rng(0)
+    n = 64 * 50
+    m = (rng.normal(size=n) * 10.0 ** rng.uniform(-6, 3, n)).astype(ref.F)
+    r = np.abs(m)[::-1].copy()
+    places = np.arange(n, dtype=np.uint64)
+    mc, ms, rc, rs = ref.encode(m, r, places, 5)
+    m2, r2 = ref.decode_m(mc, ms), ref.decode_r(rc, rs)
+    again = ref.encode(m2, r2, places, 6)
+    assert np.array_equal(ref.decode_m(again[0], again[1]), m2) and np.array_equal(ref.decode_r(again[2], again[3]), r2)
+    top = np.repeat(np.abs(m).reshape(-1, 64).max(axis=1), 64)
+    assert (np.abs(m2 - m) <= np.maximum(np.abs(m) / 8, top * 2.0 ** -16)).all()
+    top = np.repeat(r.reshape(-1, 64).max(axis=1), 64)
+    assert (np.abs(r2 - r) <= np.maximum(r / 16, top * 2.0 ** -17)).all() and (r2[r > 0] > 0).all()
+
+
+def test_the_reference_dither_is_even():
+    """Each of the 16 bits of both halves is set for about half the places, and places past 2^32 differ."""
+    d = ref.dither(np.arange(1 << 16, dtype=np.uint64), 3)
+    for half in d:
+        for bit in range(16):
+            assert abs(int(((half >> np.uint64(bit)) & np.uint64(1)).sum()) - (1 << 15)) < 6 * 128
+    far = ref.dither(np.arange(1 << 16, dtype=np.uint64) + np.uint64(1 << 32), 3)
+    assert (far[0] != d[0]).mean() > 0.99
