@@ -60,6 +60,12 @@ SIGNATURES = {
     "ob_linear_grad_work": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_i64)]),
     "ob_linear_grad": (ctypes.c_int, [_c_void_p, _i32, _i32, _i32, _i64, _i64, _i64, _i32, _c_void_p, _c_void_p,
                                       _i32, _c_void_p, _i64, _i32, _c_void_p, _c_void_p, _i64, _c_void_p]),
+    "ob_linear_work": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32, _i32, _i32, ctypes.POINTER(_i64)]),
+    "ob_linear": (ctypes.c_int, [_c_void_p, _i32, _i32, _i64, _i64, _i64, _i32, _c_void_p, _i64, _i32, _c_void_p, _i32, _i32,
+                                 _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p]),
+    "ob_linear_input_grad": (ctypes.c_int, [_c_void_p, _i32, _i64, _i64, _i64, _i32, _c_void_p, _i64, _i32, _c_void_p, _i32,
+                                            _i32, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64,
+                                            _c_void_p]),
     "ob_embedding_lookup": (ctypes.c_int, [_c_void_p, _i32, _i64, _i64, _c_void_p, _i32, _c_void_p, _f64, _i32,
                                            _c_void_p, _i64, _c_void_p]),
     "ob_embedding_grad_work": (ctypes.c_int, [_i64, _i64, ctypes.POINTER(_i64)]),
@@ -611,6 +617,88 @@ class OneBitAdam:
         need = _i64()
         _check(self.lib.ob_linear_grad_work(int(rows), int(out_features), int(in_features), _DTYPES[dy_dtype],
                                             1 if bias else 0, ctypes.byref(need)), "ob_linear_grad_work")
+        return need.value
+
+    def _list(self, weights: torch.Tensor):
+        """(pointer, type code) of a list's parameters: params, or its bfloat16 copy."""
+        self._on_device(weights, "weights")
+        return _ptr(weights, tuple(_DTYPES), self.N, "weights"), _DTYPES[weights.dtype]
+
+    def linear(self, weight, bias, x, weights, y, act="none", residual=None, keep=None, work=None, stream=None) -> None:
+        """y = act(x W^T + b) + residual with W (tensor `weight`) and b (tensor `bias`, or None)
+        from weights, the list's parameters in float32 or bfloat16 [N]; keep: an ActCheckpoint
+        [rows][out] that takes the pre-activation; y may be residual."""
+        weight = self._tensor(weight, "weight")
+        bias = -1 if bias is None else self._tensor(bias, "bias")
+        fn = ActCheckpoint._fn(act)
+        if x.dim() != 2 or x.shape[1] == 0 or self.numel[weight] % x.shape[1]:
+            raise OneBitError(f"x has shape {tuple(x.shape)}, the weight {self.numel[weight]} elements")
+        rows, cols = x.shape
+        out = self.numel[weight] // cols
+        dev = self.device
+        xp, dt, ldx = _matrix(x, rows, cols, dev, "x")
+        yp, ydt, ldy = _matrix(y, rows, out, dev, "y")
+        lp, ldt = self._list(weights)
+        rp, rdt, ldr = (None, dt, out) if residual is None else _matrix(residual, rows, out, dev, "residual")
+        if ydt != dt or rdt != dt:
+            raise OneBitError(f"x has dtype {x.dtype}, y {y.dtype}" + ("" if residual is None else f", residual {residual.dtype}"))
+        codes = scales = None
+        if keep is not None:
+            if (keep._rows, keep._cols) != (rows, out):
+                raise OneBitError(f"keep is [{keep._rows}][{keep._cols}], expected [{rows}][{out}]")
+            self._on_device(keep._codes, "keep")
+            codes, scales = keep._pointers()
+        work, have = _work(work, self._linear_work(rows, out, cols, dt, ldt, xp, ldx, 0), stream, dev)
+        with _on(dev):
+            st = self.lib.ob_linear(
+                self._ctx, weight, bias, rows, out, cols, dt, xp, ldx, ldt, lp, fn, 0 if keep is None else keep._format, codes,
+                scales, rp, ldr, yp, ldy, None if work is None else work.data_ptr(), have, _stream_on(stream, dev))
+        _check(st, "ob_linear")
+
+    def linear_input_grad(self, weight, dy, weights, dx, act="none", kept=None, add=None, work=None, stream=None) -> None:
+        """dx = (dy W) * act'(kept) + add with W (tensor `weight`) from weights as in linear; kept: the
+        ActCheckpoint [rows][in] of what the activation was given, with an activation only; dx may be add."""
+        weight = self._tensor(weight, "weight")
+        fn = ActCheckpoint._fn(act)
+        if dy.dim() != 2 or dy.shape[1] == 0 or self.numel[weight] % dy.shape[1]:
+            raise OneBitError(f"dy has shape {tuple(dy.shape)}, the weight {self.numel[weight]} elements")
+        rows, out = dy.shape
+        cols = self.numel[weight] // out
+        dev = self.device
+        gp, dt, lddy = _matrix(dy, rows, out, dev, "dy")
+        xp, xdt, lddx = _matrix(dx, rows, cols, dev, "dx")
+        lp, ldt = self._list(weights)
+        ap, adt, lda = (None, dt, cols) if add is None else _matrix(add, rows, cols, dev, "add")
+        if xdt != dt or adt != dt:
+            raise OneBitError(f"dy has dtype {dy.dtype}, dx {dx.dtype}" + ("" if add is None else f", add {add.dtype}"))
+        if (kept is None) != (fn == 0):
+            raise OneBitError("kept is given with an activation, and only then")
+        codes = scales = None
+        if kept is not None:
+            if (kept._rows, kept._cols) != (rows, cols):
+                raise OneBitError(f"kept is [{kept._rows}][{kept._cols}], expected [{rows}][{cols}]")
+            self._on_device(kept._codes, "kept")
+            codes, scales = kept._pointers()
+        work, have = _work(work, self._linear_work(rows, out, cols, dt, ldt, gp, lddy, 1), stream, dev)
+        with _on(dev):
+            st = self.lib.ob_linear_input_grad(
+                self._ctx, weight, rows, out, cols, dt, gp, lddy, ldt, lp, fn, 0 if kept is None else kept._format, codes, scales,
+                ap, lda, xp, lddx, None if work is None else work.data_ptr(), have, _stream_on(stream, dev))
+        _check(st, "ob_linear_input_grad")
+
+    def _linear_work(self, rows, out, cols, dt, ldt, pointer, ld, input_grad) -> int:
+        aligned = pointer % 16 == 0 and (rows <= 1 or (ld * (4 if dt == OB_GRAD_F32 else 2) % 16 == 0 and ld <= 1 << 21))
+        need = _i64()
+        _check(self.lib.ob_linear_work(rows, out, cols, dt, ldt, 1 if aligned else 0, input_grad, ctypes.byref(need)),
+               "ob_linear_work")
+        return need.value
+
+    def linear_work(self, rows, out_features, in_features, dtype=torch.bfloat16, list_dtype=torch.bfloat16, aligned=True,
+                    input_grad=False) -> int:
+        """Bytes of scratch that linear (or linear_input_grad) needs; aligned: x's (dy's) rows start on 16 bytes."""
+        need = _i64()
+        _check(self.lib.ob_linear_work(int(rows), int(out_features), int(in_features), _DTYPES[dtype], _DTYPES[list_dtype],
+                                       1 if aligned else 0, 1 if input_grad else 0, ctypes.byref(need)), "ob_linear_work")
         return need.value
 
     # -- kernel timing -------------------------------------------------------

@@ -75,7 +75,7 @@ const char *const kKindNames[] = {
     "server_residual", "update_residual", "materialize", "warmup", "zero_errors",
     "trust_norms", "trust_ratio", "cltk_select", "cltk_gather", "cltk_average",
     "embedding_lookup", "embedding_order", "embedding_sum", "linear_grad", "linear_join",
-    "adamw", "adamw_load"};
+    "adamw", "adamw_load", "layer_pack", "layer_forward", "layer_input_grad", "layer_join"};
 static_assert(sizeof(kKindNames) / sizeof(kKindNames[0]) == ob::K_NUM_KINDS,
               "one name per kernel kind");
 
@@ -189,6 +189,52 @@ int check_work(int64_t need, const void *work, int64_t work_bytes) {
   if (need == 0) return OB_OK;
   if (work_bytes < need) return OB_ERR_INVALID;
   return check_ptr(work);
+}
+
+// Whether a matrix's rows all start on 16 bytes.
+bool rows_aligned(const void *p, int64_t rows, int64_t ld, int64_t size) {
+  return aligned16(p) && (rows <= 1 || ld * size % 16 == 0);
+}
+
+// Whether x or dy goes to the product as it is: bf16 rows that start on 16 bytes
+// and lie close enough for a tile's offsets.
+bool layer_aligned(const void *p, int64_t rows, int64_t ld, int32_t dtype) {
+  return rows_aligned(p, rows, ld, dtype_size(dtype)) && (rows <= 1 || ld <= (int64_t{1} << 21));
+}
+
+// Shape of a linear layer's call, checked; its workspace follows from it.
+bool layer_shape_ok(int64_t rows, int64_t out, int64_t in, int32_t dtype, int32_t list_dtype) {
+  return dtype_ok(dtype) && dtype_ok(list_dtype) && ob::layer_fits(rows, out, in) && act_shape_ok(rows, out) &&
+         act_shape_ok(rows, in);
+}
+
+int64_t layer_work(const ob::LayerPlan &p) { return static_cast<int64_t>(p.a_bytes + p.b_bytes + p.part_bytes); }
+
+// What the forward and the input gradient have in common behind their checks.
+int do_layer(ob_ctx *c, ob::LayerArgs &a, int32_t weight, int32_t bias, const void *list, void *work, int64_t work_bytes,
+             hipStream_t s) {
+  const ob::LayerShape &sh = a.shape;
+  const int64_t list_size = sh.weight_f32 ? 4 : 2;
+  const ob::LayerPlan p = ob::layer_plan(sh);
+  const int st = check_work(layer_work(p), work, work_bytes);
+  if (st) return st;
+  a.rows = sh.rows;
+  a.features = sh.back ? sh.in : sh.out;
+  a.f32 = sh.f32;
+  a.weight_f32 = sh.weight_f32;
+  a.weight = static_cast<const char *>(list) + c->off[weight] * list_size;
+  a.bias = bias >= 0 ? static_cast<const char *>(list) + c->off[bias] * list_size : nullptr;
+  a.pitch = ob::act_pitch(a.features);
+  const int64_t size = sh.f32 ? 4 : 2;
+  a.vec_y = rows_aligned(a.y, a.rows, a.ldy, size);
+  a.vec_add = a.add != nullptr && rows_aligned(a.add, a.rows, a.ldadd, size);
+  a.work = work;
+  int r = OB_OK;
+  if (p.pack_a || p.pack_b) r = timed_free(c, ob::K_LAYER_PACK, s, [&] { ob::launch_layer_pack(a, p, s); });
+  if (r == OB_OK)
+    r = timed_free(c, sh.back ? ob::K_LAYER_INPUT_GRAD : ob::K_LAYER_FORWARD, s, [&] { ob::launch_layer(a, p, s); });
+  if (r == OB_OK && p.splits > 1) r = timed_free(c, ob::K_LAYER_JOIN, s, [&] { ob::launch_layer_join(a, p, s); });
+  return r;
 }
 
 // Per-step scratch of one call: the context's own, or the static buffer of
@@ -985,6 +1031,87 @@ int ob_linear_grad(ob_ctx *c, int32_t worker, int32_t weight, int32_t bias, int6
   if (st == OB_OK && ob::linear_needs_join(a))
     st = timed_free(c, ob::K_LINEAR_JOIN, s, [&] { ob::launch_linear_join(a, s); });
   return st;
+}
+
+int ob_linear_work(int64_t rows, int64_t out_features, int64_t in_features, int32_t dtype, int32_t list_dtype,
+                   int32_t aligned, int32_t input_grad, int64_t *work_bytes) {
+  if (work_bytes == nullptr || !layer_shape_ok(rows, out_features, in_features, dtype, list_dtype)) return OB_ERR_INVALID;
+  *work_bytes = rows == 0 ? 0
+                          : layer_work(ob::layer_plan(ob::LayerShape{rows, out_features, in_features, dtype == OB_GRAD_F32,
+                                                                     list_dtype == OB_GRAD_F32, aligned != 0, input_grad != 0}));
+  return OB_OK;
+}
+
+int ob_linear(ob_ctx *c, int32_t weight, int32_t bias, int64_t rows, int64_t out_features, int64_t in_features,
+              int32_t dtype, const void *x, int64_t ldx, int32_t list_dtype, const void *list, int32_t fn, int32_t format,
+              uint8_t *codes, uint8_t *scales, const void *residual, int64_t ldr, void *y, int64_t ldy, void *work,
+              int64_t work_bytes, void *stream) {
+  if (c == nullptr || weight < 0 || weight >= c->T || bias < -1 || bias >= c->T || bias == weight || !act_fn_ok(fn) ||
+      !layer_shape_ok(rows, out_features, in_features, dtype, list_dtype))
+    return OB_ERR_INVALID;
+  if (c->numel[weight] / in_features != out_features || c->numel[weight] % in_features != 0) return OB_ERR_INVALID;
+  if (bias >= 0 && c->numel[bias] != out_features) return OB_ERR_INVALID;
+  if (!matrix_ok(rows, in_features, ldx) || !matrix_ok(rows, out_features, ldy)) return OB_ERR_INVALID;
+  if (residual != nullptr && !matrix_ok(rows, out_features, ldr)) return OB_ERR_INVALID;
+  if ((codes == nullptr) != (scales == nullptr) || (codes != nullptr && !act_format_ok(format))) return OB_ERR_INVALID;
+  if (rows == 0) return OB_OK;
+  if (x == y || (rows > 1 && y == residual && ldy != ldr)) return OB_ERR_INVALID;   // rows would overwrite others not yet read
+  int st = check_ptr(list);
+  if (st == OB_OK) st = check_elements(x, dtype_size(dtype));
+  if (st == OB_OK) st = check_elements(y, dtype_size(dtype));
+  if (st == OB_OK && residual != nullptr) st = check_elements(residual, dtype_size(dtype));
+  if (st == OB_OK && codes != nullptr) st = check_ptrs(codes, scales);
+  if (st) return st;
+  ob::LayerArgs a{};
+  a.shape = ob::LayerShape{rows, out_features, in_features, dtype == OB_GRAD_F32, list_dtype == OB_GRAD_F32,
+                           layer_aligned(x, rows, ldx, dtype), false};
+  a.x = x;
+  a.ldx = ldx;
+  a.fn = fn;
+  a.codes = codes;
+  a.scales = scales;
+  a.fmt = format;
+  a.add = residual;
+  a.ldadd = ldr;
+  a.y = y;
+  a.ldy = ldy;
+  return do_layer(c, a, weight, bias, list, work, work_bytes, static_cast<hipStream_t>(stream));
+}
+
+int ob_linear_input_grad(ob_ctx *c, int32_t weight, int64_t rows, int64_t out_features, int64_t in_features,
+                         int32_t dtype, const void *dy, int64_t lddy, int32_t list_dtype, const void *list, int32_t fn,
+                         int32_t format, const uint8_t *codes, const uint8_t *scales, const void *add, int64_t ldadd,
+                         void *dx, int64_t lddx, void *work, int64_t work_bytes, void *stream) {
+  if (c == nullptr || weight < 0 || weight >= c->T || !act_fn_ok(fn) ||
+      !layer_shape_ok(rows, out_features, in_features, dtype, list_dtype))
+    return OB_ERR_INVALID;
+  if (c->numel[weight] / in_features != out_features || c->numel[weight] % in_features != 0) return OB_ERR_INVALID;
+  if (!matrix_ok(rows, out_features, lddy) || !matrix_ok(rows, in_features, lddx)) return OB_ERR_INVALID;
+  if (add != nullptr && !matrix_ok(rows, in_features, ldadd)) return OB_ERR_INVALID;
+  if (fn != OB_FN_NONE && !act_format_ok(format)) return OB_ERR_INVALID;
+  if (rows == 0) return OB_OK;
+  if (fn == OB_FN_NONE && (codes != nullptr || scales != nullptr)) return OB_ERR_INVALID;
+  if (dx == dy || (rows > 1 && dx == add && lddx != ldadd)) return OB_ERR_INVALID;
+  int st = check_ptr(list);
+  if (st == OB_OK) st = check_elements(dy, dtype_size(dtype));
+  if (st == OB_OK) st = check_elements(dx, dtype_size(dtype));
+  if (st == OB_OK && add != nullptr) st = check_elements(add, dtype_size(dtype));
+  if (st == OB_OK && fn != OB_FN_NONE) st = check_ptrs(codes, scales);
+  if (st) return st;
+  ob::LayerArgs a{};
+  a.shape = ob::LayerShape{rows, out_features, in_features, dtype == OB_GRAD_F32, list_dtype == OB_GRAD_F32,
+                           layer_aligned(dy, rows, lddy, dtype), true};
+  a.x = dy;
+  a.ldx = lddy;
+  a.fn = fn;
+  a.codes = const_cast<uint8_t *>(codes);
+  a.scales = const_cast<uint8_t *>(scales);
+  a.fmt = format;
+  a.add = add;
+  a.ldadd = ldadd;
+  a.y = dx;
+  a.ldy = lddx;
+  return do_layer(c, a, weight, -1, list, work, work_bytes, static_cast<hipStream_t>(stream));
 }
 
 int ob_embedding_lookup(ob_ctx *c, int32_t tensor, int64_t dim, int64_t tokens, const void *ids, int32_t id_dtype,

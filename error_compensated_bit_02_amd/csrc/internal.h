@@ -107,6 +107,10 @@ enum Kind {
   K_LINEAR_JOIN,
   K_ADAMW,
   K_ADAMW_LOAD,
+  K_LAYER_PACK,
+  K_LAYER_FORWARD,
+  K_LAYER_INPUT_GRAD,
+  K_LAYER_JOIN,
   K_NUM_KINDS
 };
 
@@ -339,6 +343,49 @@ size_t linear_work_bytes(int64_t rows, int64_t out, int64_t in, bool dy_bf16, bo
 void launch_linear_grad(const LinearArgs &a, hipStream_t s);
 bool linear_needs_join(const LinearArgs &a);
 void launch_linear_join(const LinearArgs &a, hipStream_t s);
+
+// A linear layer's forward and input gradient (linear.hip).
+struct LayerShape {
+  int64_t rows, out, in;     // tokens, rows of the weight, columns of the weight
+  bool f32;                  // type of x (or dy), y (dx) and what is added
+  bool weight_f32;           // type of the list that holds weight and bias
+  bool aligned;              // x's (dy's) rows start on 16 bytes
+  bool back;                 // the input gradient
+};
+// How a call of this shape runs: operands packed into the workspace, tiles,
+// slices of the contraction.  The workspace holds A's parts, B's and the slices' sums.
+struct LayerPlan {
+  bool pack_a, pack_b;       // A: the weight, B: x or dy
+  int a_parts, b_parts;
+  int tile, m_tiles, n_tiles, splits;
+  int64_t turns_each;
+  size_t a_bytes, b_bytes, part_bytes;
+};
+struct LayerArgs {
+  LayerShape shape;
+  int64_t rows, features;    // of y or dx
+  const void *x;             // x or dy
+  int64_t ldx;
+  const void *weight;        // [out][in]
+  const void *bias;          // [out] or null
+  bool weight_f32, f32;
+  int fn;                    // forward: kActNone or the activation; backward: kActNone or the one whose input was kept
+  uint8_t *codes;            // forward: the pre-activation's checkpoint, written, or null; backward: read
+  uint8_t *scales;
+  int64_t pitch;
+  int fmt;
+  const void *add;           // residual, or a gradient to add, or null
+  int64_t ldadd;
+  void *y;                   // y or dx
+  int64_t ldy;
+  bool vec_y, vec_add;       // their rows start on 16 bytes
+  void *work;
+};
+bool layer_fits(int64_t rows, int64_t out, int64_t in);
+LayerPlan layer_plan(const LayerShape &s);
+void launch_layer_pack(const LayerArgs &a, const LayerPlan &p, hipStream_t s);   // if pack_a or pack_b
+void launch_layer(const LayerArgs &a, const LayerPlan &p, hipStream_t s);
+void launch_layer_join(const LayerArgs &a, const LayerPlan &p, hipStream_t s);   // if splits > 1
 
 // The no-allocation step's scratch: one static device array of this many
 // bytes per GPU (kernels.hip), which holds the step's partial sums and trust

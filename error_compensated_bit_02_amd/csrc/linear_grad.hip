@@ -34,6 +34,7 @@
 // 807.
 #include "internal.h"
 #include "activation.h"
+#include "tiles.h"
 
 #include <algorithm>
 
@@ -42,29 +43,10 @@
 namespace ob {
 namespace {
 
-#define OB_LDS __attribute__((address_space(3)))
-
-typedef __attribute__((ext_vector_type(4))) float f32x4;
-typedef __attribute__((ext_vector_type(4))) short s16x4;
-typedef __attribute__((ext_vector_type(2))) int i32x2;
-typedef __attribute__((ext_vector_type(4))) int i32x4;
-
-// Rows of a tile are spread over the LDS banks by an exclusive or on the
-// 32-byte (dY) or 16-byte (codes) unit within the row, so that the rows one
-// transposing read touches lie on different banks.
-__device__ __forceinline__ int swizzle_a(int r) { return (r & 3) | ((r >> 3) & 1) << 2; }
+// The codes' rows likewise, in units of 16 bytes.
 template <int BN>
 __device__ __forceinline__ int swizzle_b(int r) {
   return BN >= 256 ? ((r & 7) | ((r >> 3) & 1) << 3) : (r & 7);
-}
-
-// A buffer of `bytes` from `base` on: reads past its end give 0, which is what
-// missing tokens contribute.  Its end is rounded up to the 16 bytes that one
-// load takes (all loads start on 16 bytes, so such a load stays within memory
-// that the matrix's last element lies in; what it reads there belongs to
-// columns that are dropped).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *base, int bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (bytes + 15) & ~15, 0x00020000);
 }
 
 // An fp32 value as three bf16 parts (truncated, so no part overflows).
@@ -76,44 +58,6 @@ __device__ __forceinline__ void split3(float x, uint32_t &h, uint32_t &m, uint32
   m = b1 >> 16;
   const float r2 = r1 - __uint_as_float(b1 & 0xffff0000u);
   l = __float_as_uint(r2) >> 16;
-}
-
-// Start the copy of 16 or 4 bytes a lane, from its own offset, to LDS in lane
-// order.
-__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t from, OB_LDS unsigned char *to, int offset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (OB_LDS void *)to, 16, offset, 0, 0, 0);
-}
-
-__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t from, OB_LDS unsigned char *to, int offset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (OB_LDS void *)to, 4, offset, 0, 0, 0);
-}
-
-// A workgroup's place: consecutive workgroups go to the 8 XCDs in turn, so
-// the tiles are numbered such that each XCD (its own L2) gets a consecutive
-// range: one slice of the contraction where there are several, and within it
-// kGroup tiles along dY's columns times a run along X's, the shape that needs
-// the fewest bytes of both (dY has two bytes an element, X one).
-constexpr int kXcds = 8, kGroup = 4;
-struct Split {
-  int m_tiles, n_tiles;
-  int splits;                // slices of the contraction; more than one: joined from the workspace
-  int64_t turns_each;
-};
-struct Where {
-  int mt, nt, split;
-};
-__device__ __forceinline__ Where where(const Split &sp) {
-  const uint32_t m_tiles = sp.m_tiles, n_tiles = sp.n_tiles;
-  const uint32_t tiles = m_tiles * n_tiles, total = tiles * sp.splits;
-  const uint32_t id = blockIdx.x, xcd = id % kXcds, at = id / kXcds;
-  const uint32_t each = total / kXcds, more = total % kXcds;
-  const uint32_t lin = xcd * each + min(xcd, more) + at;
-  const uint32_t split = lin / tiles, t = lin - split * tiles;
-  const uint32_t band = t / (kGroup * n_tiles), in_band = t - band * kGroup * n_tiles;
-  const uint32_t high = min(uint32_t{kGroup}, m_tiles - band * kGroup);
-  // uniform over the workgroup: kept in scalar registers
-  return Where{__builtin_amdgcn_readfirstlane(static_cast<int>(band * kGroup + in_band % high)),
-               __builtin_amdgcn_readfirstlane(static_cast<int>(in_band / high)), __builtin_amdgcn_readfirstlane(static_cast<int>(split))};
 }
 
 // Writes a wavefront's results: to `part`, a matrix of its own, or rounded
@@ -196,13 +140,6 @@ __device__ __forceinline__ void store_columns(const LinearArgs &a, float (&sum)[
     const int64_t row = m0 + (wm * FO + wn * (FO / WN) + o) * 16 + lane;
     if (lane < 16 && row < a.out) part[row] = v;
   }
-}
-
-// Waits until at most N of this wavefront's loads are out and its LDS accesses
-// are done.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
 // Drops the first `s` (0..7) of eight elements, N 32-bit words of them; zeros move in.

@@ -479,6 +479,45 @@ int ob_linear_grad(ob_ctx *ctx, int32_t worker, int32_t weight, int32_t bias, in
                    const void *dy, int64_t lddy, int32_t accumulate, void *grads, void *work, int64_t work_bytes,
                    void *stream);
 
+/* A linear layer's forward, y = fn(x W^T + b) + residual, with W (tensor
+ * `weight`, [out_features][in_features]) and b (tensor `bias`, [out_features]; -1: none)
+ * read from a list in the padded layout of list_dtype: params itself, or the bf16 copy
+ * that ob_adamw_step writes.
+ *   h[t][o] = sum over i of x[t][i] * W[o][i] + b[o];  y[t][o] = fn(h[t][o]) + residual[t][o]
+ * x [rows][in_features], residual (NULL: none) and y [rows][out_features] have type dtype;
+ * y may be residual (with the same row stride), not x.  With codes and scales not NULL the
+ * checkpoint of h (its fp32 values, in the format and layout of ob_act_save) is
+ * written in the same pass: what ob_act_backward or ob_linear_input_grad take.
+ * Sums are fp32 in an order that the sizes, types and x's row stride and
+ * alignment settle.  Products of bf16 operands are exact; an fp32 operand is cut into three
+ * bf16 parts (bits below 2^-133 are dropped), and of two fp32 operands the
+ * products of parts below 2^-25 of the whole are left out.  An infinity in an fp32 operand may
+ * give NaN where plain arithmetic gives an infinity.  fn as in ob_act_save.
+ * rows up to 2^24, features up to 2^21.
+ *
+ * ob_linear_work (host only): the scratch of a call.  aligned != 0 promises that
+ * x (dy) starts on 16 bytes, its row stride is a multiple of 16 bytes and at most
+ * 2^21 elements: bf16 matrices that are not get a copy there. */
+int ob_linear_work(int64_t rows, int64_t out_features, int64_t in_features, int32_t dtype, int32_t list_dtype,
+                   int32_t aligned, int32_t input_grad, int64_t *work_bytes);
+int ob_linear(ob_ctx *ctx, int32_t weight, int32_t bias, int64_t rows, int64_t out_features, int64_t in_features,
+              int32_t dtype, const void *x, int64_t ldx, int32_t list_dtype, const void *list, int32_t fn, int32_t format,
+              uint8_t *codes, uint8_t *scales, const void *residual, int64_t ldr, void *y, int64_t ldy, void *work,
+              int64_t work_bytes, void *stream);
+
+/* The gradient to a linear layer's input,
+ *   dx[t][i] = (sum over o of dy[t][o] * W[o][i]) * fn'(kept[t][i]) + add[t][i]
+ * with kept the values of the checkpoint [rows][in_features] in codes and scales (fn =
+ * OB_FN_NONE: no such factor, codes and scales are NULL) and add a gradient that reached
+ * the same place another way (NULL: none).  dy [rows][out_features], add and dx
+ * [rows][in_features] have type dtype; dx may be add (with the same row stride), not dy.
+ * W, sums, products, limits and scratch as for ob_linear (ob_linear_work with
+ * input_grad != 0); fn' as in ob_act_backward. */
+int ob_linear_input_grad(ob_ctx *ctx, int32_t weight, int64_t rows, int64_t out_features, int64_t in_features,
+                         int32_t dtype, const void *dy, int64_t lddy, int32_t list_dtype, const void *list, int32_t fn,
+                         int32_t format, const uint8_t *codes, const uint8_t *scales, const void *add, int64_t ldadd,
+                         void *dx, int64_t lddx, void *work, int64_t work_bytes, void *stream);
+
 /* Embedding lookup: out[t] = fp32(scale) * E[ids[t]], with tensor `tensor` of
  * params [N] as the table E [numel/dim][dim], and at most 16,777,215 tokens;
  * fp32(scale) is finite.  A negative id is padding and gives a row of zeros;

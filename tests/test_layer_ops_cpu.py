@@ -23,6 +23,32 @@ def test_adamw_without_a_context_is_refused(lib):
     assert lib.ob_adamw_load(None, P, P, P, P, 0, P, P, None) == INVALID
 
 
+def test_linear_without_a_context_is_refused(lib):
+    assert lib.ob_linear(None, 0, -1, 1, 8, 8, 1, P, 8, 1, P, 0, 0, None, None, None, 0, 2 * P, 8, P, 1 << 20, None) == INVALID
+    assert lib.ob_linear_input_grad(None, 0, 1, 8, 8, 1, P, 8, 1, P, 0, 0, None, None, None, 0, 2 * P, 8, P, 1 << 20, None) == INVALID
+
+
+def test_linear_work_sizes(lib):
+    n = ctypes.c_int64()
+
+    def work(rows, out, inp, dt=1, lt=1, aligned=1, back=0):
+        st = lib.ob_linear_work(rows, out, inp, dt, lt, aligned, back, ctypes.byref(n))
+        return n.value if st == 0 else -st
+
+    for back in (0, 1):
+        assert work(0, 8, 8, back=back) == 0
+        assert work(4096, 4096, 4096, back=back) == 0                        # bf16 as it lies, no slices
+        assert work(4096, 4096, 4096, aligned=0, back=back) == 4096 * 4096 * 2
+        assert work(4096, 4096, 4096, dt=0, lt=0, back=back) == 2 * 3 * 4096 * 4096 * 2
+        assert work(1 << 24, 1 << 10, 1 << 10, back=back) >= 0 and work(1, 1 << 21, 1 << 21, back=back) >= 0
+        for bad in [(-1, 8, 8), ((1 << 24) + 1, 8, 8), (8, 0, 8), (8, 8, 0), (8, (1 << 21) + 1, 8), (8, 8, (1 << 21) + 1),
+                    (1 << 24, 1 << 21, 8)]:
+            assert work(*bad, back=back) == -INVALID, bad
+        assert work(8, 8, 8, dt=2, back=back) == -INVALID and work(8, 8, 8, lt=-1, back=back) == -INVALID
+    assert work(64, 64, 7) >= 2 * 64 * 64 * 2                                # rows of 7 elements: both operands are copied
+    assert lib.ob_linear_work(1, 1, 1, 0, 0, 1, 0, None) == INVALID
+
+
 def test_the_reference_rounds_both_ways_and_keeps_codes():
     """Values on a code stay there whatever the dither; others take one of their two neighbours."""
     rng = np.random.default_rng(0)

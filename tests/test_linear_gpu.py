@@ -1,0 +1,453 @@
+"""A linear layer's forward and input gradient on the GPU against plain 64-bit
+definitions.  Whole numbers, whose sums fp32 holds exactly, must match bit for
+bit; the rest is held to bounds counted from the roundings made."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import grad_ops as ref
+from error_compensated_bit_02_amd import ActCheckpoint, OneBitAdam, OneBitError
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+FNS = ["none", "gelu", "gelu_tanh", "silu"]
+F32, BF16 = torch.float32, torch.bfloat16
+TYPES = [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)]      # x, list
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+
+
+def _gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _put(t, dtype, extra=0, offset=0, fill=7.0):
+    """t on the GPU as a view with row stride cols + extra, starting `offset` elements into its buffer."""
+    rows, cols = t.shape
+    flat = torch.full((offset + max(rows, 1) * (cols + extra),), fill, dtype=dtype, device=DEV)
+    view = flat[offset:].view(max(rows, 1), cols + extra)[:rows, :cols]
+    view.copy_(t.to(dtype))
+    return view, flat
+
+
+class Layer:
+    """A list whose tensors 1 and 2 are a layer's weight and bias, between others that hold NaN, as does the padding."""
+
+    def __init__(self, out, inp, dtype, seed=0, whole=False, scale=1.0):
+        self.out, self.inp = out, inp
+        g = _gen(seed)
+        if whole:
+            w, b = torch.randint(-2, 3, (out, inp), generator=g).float(), torch.randint(-9, 10, (out,), generator=g).float()
+        else:
+            w, b = torch.randn(out, inp, generator=g) * scale, torch.randn(out, generator=g)
+        self.opt = OneBitAdam([70, out * inp, out, 5], 1)
+        self.list = torch.full((self.opt.N,), float("nan"), dtype=dtype, device=DEV)
+        o = self.opt.offsets
+        self.list[o[1]: o[1] + out * inp] = w.reshape(-1).to(DEV).to(dtype)
+        self.list[o[2]: o[2] + out] = b.to(DEV).to(dtype)
+        self.w = _f64(w.to(dtype))
+        self.b = _f64(b.to(dtype))
+
+
+def _values(rows, cols, seed, whole, lim=3):
+    g = _gen(seed)
+    return torch.randint(-lim, lim + 1, (rows, cols), generator=g).float() if whole else torch.randn(rows, cols, generator=g)
+
+
+def _round(x, dtype):
+    """float64 values, exact in fp32, rounded to dtype as the kernels do."""
+    t = torch.from_numpy(np.asarray(x))
+    assert torch.equal(t.float().double(), t)
+    return t.float().to(dtype).double().numpy()
+
+
+SHAPES = [  # rows, out, in, x's extra columns and offset in elements
+    (1, 1, 1, 0, 0), (1, 5, 8, 0, 0), (1, 129, 64, 0, 0), (2, 64, 65, 1, 1), (7, 40, 72, 8, 8), (16, 300, 136, 0, 0),
+    (31, 33, 31, 0, 4), (33, 256, 200, 24, 0), (64, 72, 1000, 0, 0), (129, 130, 264, 7, 0), (300, 257, 96, 0, 0),
+    (513, 520, 328, 16, 8), (1, 4096, 1024, 0, 0), (5, 1000, 4104, 0, 0)]
+
+
+@pytest.mark.parametrize("rows,out,inp,extra,offset", SHAPES)
+@pytest.mark.parametrize("xt,lt", TYPES)
+def test_forward_of_whole_numbers(rows, out, inp, extra, offset, xt, lt):
+    """Sums of at most 4104 * 3 * 2 + 9: exact in fp32; y rounds once.  With residual, without bias, in place over the
+    residual, and the checkpoint of the sums beside it."""
+    ly = Layer(out, inp, lt, seed=rows, whole=True)
+    x, _ = _put(_values(rows, inp, 1, True), xt, extra, offset)
+    res, _ = _put(_values(rows, out, 2, True), xt, 3, 1)
+    h = _f64(x) @ ly.w.T
+    y, flat = _put(torch.zeros(rows, out), xt, 5, 2)
+    ly.opt.linear(1, 2, x, ly.list, y)
+    assert np.array_equal(_f64(y), _round(h + ly.b, xt))
+    ly.opt.linear(1, None, x, ly.list, y, residual=res)
+    assert np.array_equal(_f64(y), _round(h + _f64(res), xt))
+    want = _round(h + ly.b + _f64(res), xt)
+    ly.opt.linear(1, 2, x, ly.list, res, residual=res)
+    assert np.array_equal(_f64(res), want)
+    # nothing beside y's columns is written
+    pad = flat[2:].view(rows, out + 5)[:, out:]
+    assert (pad == 7.0).all() and (flat[:2] == 7.0).all()
+    for fmt in ("e4m3", "int8"):
+        ck = ActCheckpoint(rows, out, fmt, device=DEV)
+        ck.codes.fill_(0x55)
+        ck.scales.fill_(0x55)
+        ly.opt.linear(1, 2, x, ly.list, y, keep=ck)
+        assert np.array_equal(_f64(y), _round(h + ly.b, xt))
+        codes, scales = ck.codes.cpu().numpy(), ck.scales.cpu().numpy()
+        assert np.array_equal(scales[:, :out], ref.scale_bytes(h + ly.b, fmt))
+        assert np.array_equal(ref.decoded(codes, scales, out, fmt), ref.quantised(h + ly.b, fmt))
+        assert (scales[:, out:] == 0x55).all() and (codes[:, out:] == 0x55).all()
+
+
+@pytest.mark.parametrize("rows,out,inp,extra,offset", SHAPES)
+@pytest.mark.parametrize("dt,lt", TYPES)
+def test_input_grad_of_whole_numbers(rows, out, inp, extra, offset, dt, lt):
+    ly = Layer(out, inp, lt, seed=rows, whole=True)
+    dy, _ = _put(_values(rows, out, 1, True), dt, extra, offset)
+    add, _ = _put(_values(rows, inp, 2, True), dt, 3, 1)
+    want = _f64(dy) @ ly.w
+    dx, flat = _put(torch.zeros(rows, inp), dt, 5, 2)
+    ly.opt.linear_input_grad(1, dy, ly.list, dx)
+    assert np.array_equal(_f64(dx), _round(want, dt))
+    total = _round(want + _f64(add), dt)
+    ly.opt.linear_input_grad(1, dy, ly.list, dx, add=add)
+    assert np.array_equal(_f64(dx), total)
+    ly.opt.linear_input_grad(1, dy, ly.list, add, add=add)
+    assert np.array_equal(_f64(add), total)
+    assert (flat[2:].view(rows, inp + 5)[:, inp:] == 7.0).all() and (flat[:2] == 7.0).all()
+
+
+@pytest.mark.parametrize("rows,out,inp,extra", [(2100, 2056, 520, 0), (1111, 1032, 2048, 8), (4500, 777, 640, 0), (700, 4100, 264, 1)])
+@pytest.mark.parametrize("xt,lt", [(BF16, BF16), (F32, F32)])
+def test_many_tiles(rows, out, inp, extra, xt, lt):
+    """Sizes that take large tiles and several slices, rows off 16 bytes among them; whole numbers, bit for bit."""
+    ly = Layer(out, inp, lt, seed=3, whole=True)
+    x, _ = _put(_values(rows, inp, 1, True), xt, extra)
+    dy, _ = _put(_values(rows, out, 2, True), xt, extra)
+    y, dx = torch.empty(rows, out, dtype=xt, device=DEV), torch.empty(rows, inp, dtype=xt, device=DEV)
+    ck = ActCheckpoint(rows, out, "e4m3", device=DEV)
+    ly.opt.linear(1, 2, x, ly.list, y, keep=ck)
+    h = _f64(x) @ ly.w.T + ly.b
+    assert np.array_equal(_f64(y), _round(h, xt))
+    got = torch.empty(rows, out, device=DEV)
+    ck.load(got)
+    other = ActCheckpoint(rows, out, "e4m3", device=DEV)      # the checkpoint's own kernel is tested bit for bit
+    other.save(torch.from_numpy(h).float().to(DEV))
+    assert torch.equal(ck.scales[:, :out], other.scales[:, :out]) and torch.equal(ck.codes[:, :out], other.codes[:, :out])
+    ly.opt.linear_input_grad(1, dy, ly.list, dx)
+    assert np.array_equal(_f64(dx), _round(_f64(dy) @ ly.w, xt))
+
+
+def _sum_error(n, mag, xt, lt):
+    """n additions in any order are off by n * 2^-24 of the sum of magnitudes, twice that for the matrix unit, whose
+    inner sums may truncate; each fp32 operand has three parts, two of them six products, whose leading ones alone
+    are not small: 2^-7 of the others.  Left-out products: below 2^-25 each of three."""
+    parts = 1 + 2.0 ** -5 if F32 in (xt, lt) else 1.0
+    return (2 * (n + 8) * parts + 2) * ref.U32 * mag
+
+
+def _near(got, want, err, dtype):
+    got = _f64(got)
+    slack = err + ref.HALF[dtype] * (np.abs(want) + err)
+    assert (np.abs(got - want) <= slack).all(), np.max(np.abs(got - want) / np.maximum(slack, 1e-300))
+
+
+@pytest.mark.parametrize("rows,out,inp,extra,offset", [(3, 40, 64, 0, 0), (50, 129, 200, 1, 1), (300, 256, 520, 8, 8)])
+@pytest.mark.parametrize("xt,lt", TYPES)
+@pytest.mark.parametrize("fn", FNS)
+@pytest.mark.parametrize("res", [False, True])
+def test_forward(rows, out, inp, extra, offset, xt, lt, fn, res):
+    """The activation's error beside that of its argument, whose slope is at most 1.13."""
+    ly = Layer(out, inp, lt, seed=rows, scale=inp ** -0.5)
+    x, _ = _put(_values(rows, inp, 1, False) * 2, xt, extra, offset)
+    r, _ = _put(_values(rows, out, 2, False), xt, 3, 1)
+    y = torch.empty(rows, out, dtype=xt, device=DEV)
+    ly.opt.linear(1, 2, x, ly.list, y, act=fn, residual=r if res else None)
+    h = _f64(x) @ ly.w.T + ly.b
+    e = _sum_error(inp, np.abs(_f64(x)) @ np.abs(ly.w).T + np.abs(ly.b), xt, lt)
+    want = h
+    if fn != "none":
+        want = ref.act(h, fn)
+        e = 1.13 * e + ref.act_error(h, fn) * np.abs(want) + np.abs(h) * 2.0 ** -126      # Phi or sigma below that may be 0
+    if res:
+        want = want + _f64(r)
+        e = e + ref.U32 * (np.abs(want) + e)
+    _near(y, want, e, xt)
+
+
+def _slope_error(x, fn):
+    """Error of act'(x) = F + x F': its two terms carry act_error each, and lose what a factor flushed below 2^-126 is
+    multiplied by, at most 2|x|(1 + 3*0.044715 x^2)."""
+    s = ref.act_slope(x, fn)
+    second = np.abs(s - (ref._phi(x) if fn == "gelu" else ref._sigmoid(ref.C * (x + ref.K * x ** 3) if fn == "gelu_tanh" else x)))
+    return (np.abs(s) + 2 * second) * ref.act_error(x, fn) + 2.0 ** -126 * (1 + 2 * np.abs(x) * (1 + 3 * ref.K * x * x))
+
+
+@pytest.mark.parametrize("rows,out,inp,extra,offset", [(3, 40, 64, 0, 0), (50, 129, 200, 1, 1), (300, 256, 520, 8, 8)])
+@pytest.mark.parametrize("dt,lt", TYPES)
+@pytest.mark.parametrize("fn", FNS[1:])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("add", [False, True])
+def test_input_grad(rows, out, inp, extra, offset, dt, lt, fn, fmt, add):
+    ly = Layer(out, inp, lt, seed=rows, scale=out ** -0.5)
+    dy, _ = _put(_values(rows, out, 1, False), dt, extra, offset)
+    a, _ = _put(_values(rows, inp, 2, False), dt, 3, 1)
+    x = _values(rows, inp, 3, False) * 3
+    x[:, inp // 2] *= 20.0
+    ck = ActCheckpoint(rows, inp, fmt, device=DEV)
+    ck.save(x.to(DEV))
+    dx = torch.empty(rows, inp, dtype=dt, device=DEV)
+    ly.opt.linear_input_grad(1, dy, ly.list, dx, act=fn, kept=ck, add=a if add else None)
+    held = ref.decoded(ck.codes.cpu().numpy(), ck.scales.cpu().numpy(), inp, fmt)
+    s = ref.act_slope(held, fn)
+    g = _f64(dy) @ ly.w
+    e = _sum_error(out, np.abs(_f64(dy)) @ np.abs(ly.w), dt, lt)
+    es = _slope_error(held, fn)
+    want = g * s
+    e = e * (np.abs(s) + es) + np.abs(g) * es + ref.U32 * np.abs(want)
+    if add:
+        want = want + _f64(a)
+        e = e + ref.U32 * (np.abs(want) + e)
+    _near(dx, want, e, dt)
+
+
+def test_gradients_against_differences():
+    """The layer is linear in x: with whole numbers the change of sum(dy * y) along a direction equals the gradient
+    along it exactly; and through the activation, central differences of its 64-bit form."""
+    rows, out, inp = 40, 56, 72
+    ly = Layer(out, inp, BF16, seed=5, whole=True)
+    x, d = _values(rows, inp, 1, True), _values(rows, inp, 2, True)
+    dy = _values(rows, out, 3, True)
+    y = [torch.empty(rows, out, device=DEV) for _ in range(2)]
+    ly.opt.linear(1, 2, x.to(DEV), ly.list, y[0])
+    ly.opt.linear(1, 2, (x + d).to(DEV), ly.list, y[1])
+    dx = torch.empty(rows, inp, device=DEV)
+    ly.opt.linear_input_grad(1, dy.to(DEV), ly.list, dx)
+    assert float(((y[1] - y[0]).cpu().double() * dy.double()).sum()) == float((dx.cpu().double() * d.double()).sum())
+    # z -> act(z) -> layer: dz = (dy W) act'(z) at the kept values of z
+    z = _values(rows, inp, 4, False)
+    ck = ActCheckpoint(rows, inp, "e4m3", device=DEV)
+    ck.save(z.to(DEV))
+    held = ref.decoded(ck.codes.cpu().numpy(), ck.scales.cpu().numpy(), inp, "e4m3")
+    for fn in FNS[1:]:
+        ly.opt.linear_input_grad(1, dy.to(DEV), ly.list, dx, act=fn, kept=ck)
+        loss = lambda q: float(((ref.act(q, fn) @ ly.w.T) * dy.double().numpy()).sum())   # noqa: E731
+        step, dirn = 1e-4, _f64(d)
+        diff = (loss(held + step * dirn) - loss(held - step * dirn)) / (2 * step)
+        # third derivatives are below 3 and steps below 3e-4: 3 * (3e-4)^2 / 6 of each term; fp32's own error beside it
+        g = np.abs(dy.double().numpy() @ ly.w)
+        terms = (g * np.abs(dirn)).sum()
+        assert abs(float((_f64(dx) * dirn).sum()) - diff) <= terms * (3 * 9e-8 / 6 + 64 * ref.U32) + 1e-6
+
+
+def test_layer_trains():
+    """One whole step of a layer as a program runs it: forward with its pre-activation kept, the gradients of input, weight
+    and bias, AdamW with the bf16 copy, and the next forward from that copy."""
+    rows, out, inp = 200, 96, 160
+    opt = OneBitAdam([out * inp, out], 1)
+    g = _gen(1)
+    params = torch.zeros(opt.N)
+    params[: out * inp] = torch.randn(out * inp, generator=g) * inp ** -0.5
+    params = params.to(DEV)
+    model = params.to(BF16)
+    x = torch.randn(rows, inp, generator=g).to(DEV).to(BF16)
+    xk, hk = ActCheckpoint(rows, inp, "e4m3", device=DEV), ActCheckpoint(rows, out, "e4m3", device=DEV)
+    y, dh = (torch.empty(rows, out, dtype=BF16, device=DEV) for _ in range(2))
+    dx = torch.empty(rows, inp, dtype=BF16, device=DEV)
+    grads = torch.zeros(1, opt.N, device=DEV)
+    state = opt.adamw_state("8bit")
+    dy = torch.randn(rows, out, generator=g).to(DEV).to(BF16)
+    for step in (1, 2):
+        xk.save(x)
+        opt.linear(0, 1, x, model, y, act="gelu", residual=dy, keep=hk)
+        hk.act_backward("gelu", dy, dh)
+        opt.linear_grad(0, 0, 1, xk, dh, grads)
+        opt.linear_input_grad(0, dh, model, dx, add=x)
+        w = _f64(model[: out * inp].view(out, inp))
+        h = _f64(x) @ w.T + _f64(model[opt.offsets[1]: opt.offsets[1] + out])
+        e = _sum_error(inp, np.abs(_f64(x)) @ np.abs(w).T, BF16, BF16)
+        _near(y, ref.act(h, "gelu") + _f64(dy), 1.13 * e + ref.act_error(h, "gelu") * np.abs(h) + ref.U32 * np.abs(_f64(dy)) * 2 + ref.U32 * np.abs(h), BF16)
+        _near(dx, _f64(dh) @ w + _f64(x), _sum_error(out, np.abs(_f64(dh)) @ np.abs(w), BF16, BF16) + 2 * ref.U32 * np.abs(_f64(x)), BF16)
+        before = params.clone()
+        opt.adamw_step(grads, state, params, step, 1e-2, weight_decay=0.1, model=model, seed=step)
+        assert torch.equal(model, params.to(BF16)) and not torch.equal(before, params)
+
+
+@pytest.mark.parametrize("dt,lt", TYPES)
+def test_non_finite_values_stay_in_their_row_and_column(dt, lt):
+    """A NaN token gives a NaN row, a NaN weight its column; the rest does not change.  In the checkpoint a NaN row makes
+    its blocks NaN."""
+    rows, out, inp = 70, 80, 100
+    ly = Layer(out, inp, lt, seed=1, whole=True)
+    x, _ = _put(_values(rows, inp, 1, True), dt)
+    y = [torch.empty(rows, out, dtype=dt, device=DEV) for _ in range(2)]
+    ly.opt.linear(1, 2, x, ly.list, y[0])
+    x[37, 5] = float("nan")
+    ly.list[ly.opt.offsets[1] + 9 * inp + 3] = float("nan")
+    ck = ActCheckpoint(rows, out, "e4m3", device=DEV)
+    ly.opt.linear(1, 2, x, ly.list, y[1], keep=ck)
+    bad = torch.zeros(rows, out, dtype=torch.bool, device=DEV)
+    bad[37] = True
+    bad[:, 9] = True
+    assert torch.isnan(y[1][bad]).all() and torch.equal(y[1][~bad], y[0][~bad])
+    v = torch.empty(rows, out, device=DEV)
+    ck.load(v)
+    block = torch.zeros_like(bad)
+    block[32:64] = True
+    block[:, 9] = True
+    assert torch.equal(torch.isnan(v), block)
+    dy, _ = _put(_values(rows, out, 2, True), dt)
+    dy[:, 9] = 0.0
+    dy[11, 4] = float("nan")
+    dx = torch.empty(rows, inp, dtype=dt, device=DEV)
+    ly.opt.linear_input_grad(1, dy, ly.list, dx)
+    bad = torch.zeros(rows, inp, dtype=torch.bool, device=DEV)
+    bad[11] = True
+    bad[:, 3] = True          # 0 * NaN
+    assert torch.equal(torch.isnan(dx), bad)
+
+
+def test_fp32_keeps_small_parts():
+    """Operands whose low bits carry the answer, and values near both ends of the range."""
+    ly = Layer(4, 8, F32, seed=0)
+    o = ly.opt.offsets
+    w = torch.zeros(4, 8)
+    w[0, 0], w[0, 1] = 1.0 + 2.0 ** -20, -1.0
+    w[1, 0] = 1.2345678e38
+    w[2, 0] = 2.3456789e-30
+    w[3, 0] = 3.4028234663852886e38
+    ly.list[o[1]: o[1] + 32] = w.reshape(-1).to(DEV)
+    x = torch.zeros(1, 8)
+    x[0, :2] = 1.0
+    y = torch.empty(1, 4, device=DEV)
+    ly.opt.linear(1, None, x.to(DEV), ly.list, y)
+    assert torch.equal(y.cpu()[0], torch.tensor([2.0 ** -20, float(w[1, 0]), float(w[2, 0]), float(w[3, 0])]))
+    x[0, 0] = 1.0 + 2.0 ** -23          # the square of 1 + 2^-23 less 1: 2^-22, its 2^-46 left out
+    w[0, 0] = 1.0 + 2.0 ** -23
+    ly.list[o[1]] = w[0, 0]
+    ly.opt.linear(1, None, x.to(DEV), ly.list, y)
+    assert float(y[0, 0]) == 2.0 ** -22
+
+
+def test_no_rows():
+    ly = Layer(10, 20, BF16)
+    x, y = torch.empty(0, 20, dtype=BF16, device=DEV), torch.empty(0, 10, dtype=BF16, device=DEV)
+    ly.opt.linear(1, 2, x, ly.list, y, act="gelu", residual=torch.empty_like(y), keep=ActCheckpoint(0, 10, device=DEV))
+    ly.opt.linear_input_grad(1, y, ly.list, x)
+
+
+def test_work_streams_and_repeats():
+    """A caller's own scratch, full of NaN, another stream, two calls at once on two streams: the same bits."""
+    rows, out, inp = 65, 300, 1000
+    ly = Layer(out, inp, F32, seed=2)
+    x = _values(rows, inp, 1, False).to(DEV)
+    y = [torch.empty(rows, out, device=DEV) for _ in range(4)]
+    ly.opt.linear(1, 2, x, ly.list, y[0], act="silu")
+    need = ly.opt.linear_work(rows, out, inp, F32, F32)
+    assert need > 0
+    works = [torch.full((need // 4 + 1,), float("nan"), device=DEV) for _ in range(2)]
+    ly.opt.linear(1, 2, x, ly.list, y[1], act="silu", work=works[0])
+    torch.cuda.synchronize()
+    for w in works:
+        w.fill_(float("nan"))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for k, s in enumerate(streams):
+        ly.opt.linear(1, 2, x, ly.list, y[2 + k], act="silu", work=works[k], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y[0], t) for t in y[1:])
+    with pytest.raises(OneBitError, match="bytes"):
+        ly.opt.linear(1, 2, x, ly.list, y[0], work=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("rows,out,inp,dt", [(3, 512, 512, BF16), (200, 256, 512, F32), (1000, 520, 264, BF16)])
+def test_graphs(rows, out, inp, dt):
+    """Forward and input gradient captured together, replayed with other inputs and work between."""
+    ly = Layer(out, inp, dt, seed=2, scale=inp ** -0.5)
+    x, dy = _values(rows, inp, 1, False).to(DEV).to(dt), _values(rows, out, 2, False).to(DEV).to(dt)
+    y, dx = torch.empty(rows, out, dtype=dt, device=DEV), torch.empty(rows, inp, dtype=dt, device=DEV)
+    ck = ActCheckpoint(rows, inp, device=DEV)
+    work = [torch.empty(max(16, ly.opt.linear_work(rows, out, inp, dt, dt, input_grad=b)), dtype=torch.uint8, device=DEV)
+            for b in (False, True)]
+
+    def both():
+        ck.save(x)
+        ly.opt.linear(1, 2, x, ly.list, y, act="gelu", work=work[0])
+        ly.opt.linear_input_grad(1, dy, ly.list, dx, act="gelu", kept=ck, work=work[1])
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for k in range(3):
+        x.copy_(_values(rows, inp, 10 + k, False))
+        dy.copy_(_values(rows, out, 20 + k, False))
+        both()
+        torch.cuda.synchronize()
+        want = y.clone(), dx.clone()
+        y.fill_(0.0)
+        dx.fill_(0.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(dx, want[1])
+
+
+def test_refusals():
+    ly = Layer(24, 40, BF16, seed=1)
+    opt = ly.opt
+    x, y = torch.zeros(6, 40, dtype=BF16, device=DEV), torch.full((6, 24), 7.0, dtype=BF16, device=DEV)
+    dx = torch.full((6, 40), 7.0, dtype=BF16, device=DEV)
+    ck, ik = ActCheckpoint(6, 24, device=DEV), ActCheckpoint(6, 40, device=DEV)
+
+    def fwd(match, **k):
+        a = dict(weight=1, bias=2, x=x, weights=ly.list, y=y) | k
+        with pytest.raises(OneBitError, match=match):
+            opt.linear(**a)
+        assert (y == 7.0).all()
+
+    def back(match, **k):
+        a = dict(weight=1, dy=y, weights=ly.list, dx=dx) | k
+        with pytest.raises(OneBitError, match=match):
+            opt.linear_input_grad(**a)
+        assert (dx == 7.0).all()
+
+    for call in (fwd, back):
+        call("one of the list", weight=4)
+        call("weights", weights=ly.list[:64])
+        call("weights has dtype", weights=ly.list.half())
+        call("activation", act="relu")
+    fwd("one of the list", bias=-1)
+    fwd("status 1", bias=1)
+    fwd("status 1", bias=3)
+    fwd("x has shape", x=torch.zeros(6, 41, dtype=BF16, device=DEV))
+    fwd("x has shape", x=torch.zeros(6, 0, dtype=BF16, device=DEV))
+    fwd("adjacent", x=torch.zeros(40, 6, dtype=BF16, device=DEV).t())
+    fwd("y has shape", y=torch.full((6, 25), 7.0, dtype=BF16, device=DEV))
+    fwd("dtype", y=torch.zeros(6, 24, device=DEV))
+    fwd("dtype", residual=torch.zeros(6, 24, device=DEV))
+    fwd("keep is", keep=ik)
+    fwd("device tensor", x=torch.zeros(6, 40, dtype=BF16))
+    back("kept is given", act="gelu")
+    back("kept is given", kept=ik)
+    back("kept is", act="gelu", kept=ck)
+    back("dtype", add=torch.zeros(6, 40, device=DEV))
+    # the output over its own input, and over what is added at another stride
+    sq = Layer(40, 40, BF16)
+    z = torch.zeros(6, 40, dtype=BF16, device=DEV)
+    with pytest.raises(OneBitError, match="status 1"):
+        sq.opt.linear(1, None, z, sq.list, z)
+    with pytest.raises(OneBitError, match="status 1"):
+        sq.opt.linear_input_grad(1, z, sq.list, z)
