@@ -208,6 +208,9 @@ def _work(work, need: int, stream, device: torch.device):
         return torch.empty(need, dtype=torch.uint8, device=device), need
 
 
+_linear_needs: Dict[tuple, int] = {}     # scratch of a linear layer's calls by shape
+
+
 def act_layout(rows: int, cols: int):
     """(pitch, bytes of codes, bytes of scales) of a rows x cols checkpoint (host only)."""
     out = [_i64() for _ in range(3)]
@@ -688,10 +691,15 @@ class OneBitAdam:
 
     def _linear_work(self, rows, out, cols, dt, ldt, pointer, ld, input_grad) -> int:
         aligned = pointer % 16 == 0 and (rows <= 1 or (ld * (4 if dt == OB_GRAD_F32 else 2) % 16 == 0 and ld <= 1 << 21))
-        need = _i64()
-        _check(self.lib.ob_linear_work(rows, out, cols, dt, ldt, 1 if aligned else 0, input_grad, ctypes.byref(need)),
-               "ob_linear_work")
-        return need.value
+        key = rows, out, cols, dt, ldt, aligned, input_grad
+        need = _linear_needs.get(key)
+        if need is None:    # asked once a shape: the call costs a fifth of a small layer's
+            if len(_linear_needs) >= 4096:
+                _linear_needs.clear()
+            got = _i64()
+            _check(self.lib.ob_linear_work(*key[:5], 1 if aligned else 0, input_grad, ctypes.byref(got)), "ob_linear_work")
+            need = _linear_needs[key] = got.value
+        return need
 
     def linear_work(self, rows, out_features, in_features, dtype=torch.bfloat16, list_dtype=torch.bfloat16, aligned=True,
                     input_grad=False) -> int:

@@ -10,6 +10,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,7 +24,7 @@ SOURCES = [os.path.join(CSRC, "kernels.hip"), os.path.join(CSRC, "topk.hip"),
 
 FLAGS = [
     "--offload-arch=gfx950",
-    "-O3", "-fPIC", "-shared", "-std=c++17",
+    "-O3", "-fPIC", "-std=c++17",
     "-ffp-contract=off",
     "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -39,17 +41,24 @@ def hipcc() -> str:
 
 def build(verbose: bool = False) -> str:
     """Compile libob.so next to this file; returns its path.  Always recompiles."""
+    def run(args):
+        cmd = [hipcc(), *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC, *args]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        proc = subprocess.run(cmd, capture_output=True, text=True)
+        noise = "is not a recognized feature for this target"
+        err = "\n".join(l for l in proc.stderr.splitlines() if noise not in l)
+        if proc.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({proc.returncode}):\n{err}")
+        if verbose and err.strip():
+            print(err, file=sys.stderr)
+
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", tmp, *SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    proc = subprocess.run(cmd, capture_output=True, text=True)
-    noise = "is not a recognized feature for this target"
-    err = "\n".join(l for l in proc.stderr.splitlines() if noise not in l)
-    if proc.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({proc.returncode}):\n{err}")
-    if verbose and err.strip():
-        print(err, file=sys.stderr)
+    with tempfile.TemporaryDirectory() as objects:   # one compiler a source, in parallel
+        names = [os.path.join(objects, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(min(len(SOURCES), os.cpu_count() or 1, 16)) as pool:
+            list(pool.map(lambda so: run(["-c", "-o", so[1], so[0]]), zip(SOURCES, names)))
+        run(["-shared", "-o", tmp, *names])
     os.replace(tmp, LIB)
     return LIB
 

@@ -10,7 +10,7 @@
 // the forward and along f in the backward.  The weight is the instruction's first
 // operand, so a lane's four results are four consecutive f of one token.
 //
-// fp32 operands are cut into three bf16 parts each (pack_kernel), rounded to
+// fp32 operands are cut into three bf16 parts each (pack_units), rounded to
 // nearest, so that each part is at most 2^-8 of the one before and they add up to
 // the value exactly (but for bits below bf16's last, 2^-133).  Of two fp32 operands
 // the products of parts whose order sums to at most 2 are taken, six of nine; the
@@ -22,13 +22,14 @@
 #include "tiles.h"
 
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #pragma clang fp contract(off)
 
 namespace ob {
 namespace {
 
-constexpr int kTurn = 64;            // contraction steps of a turn
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 // What multiplies: matrices of bf16 parts whose rows start on 16 bytes.
@@ -37,8 +38,6 @@ struct Product {
   int64_t a_rows;                    // backward: A's rows, the true length
   const uint16_t *a, *b;
   int64_t lda, ldb, a_part, b_part;  // row strides and distances of the parts, in elements
-  int pairs;                         // products of parts
-  uint32_t a_sel, b_sel;             // two bits a pair: the parts of each operand
 };
 
 // ---------------------------------------------------------------------------
@@ -105,48 +104,48 @@ __device__ __forceinline__ void write_bytes(uint8_t *p, int n, u32x2 w) {
     if (k < n) p[k] = static_cast<uint8_t>(w[k >> 2] >> (8 * (k & 3)));
 }
 
-template <bool FINE>
-__device__ __forceinline__ void act8(int fn, float (&v)[8]) {
-  if (fn == kActGelu) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = act_value<kActGelu, FINE>(v[k]);
-  } else if (fn == kActGeluTanh) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = act_value<kActGeluTanh, FINE>(v[k]);
-  } else if (fn == kActSilu) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = act_value<kActSilu, FINE>(v[k]);
-  }
-}
-
-template <bool FINE>
-__device__ __forceinline__ void slope8(int fn, const float (&x)[8], float (&v)[8]) {
-  if (fn == kActGelu) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = v[k] * act_slope<kActGelu, FINE>(x[k]);
-  } else if (fn == kActGeluTanh) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = v[k] * act_slope<kActGeluTanh, FINE>(x[k]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = v[k] * act_slope<kActSilu, FINE>(x[k]);
-  }
-}
-
 // Row stride of the sums in LDS, in floats: 16 bytes more than a row.
 template <int FW>
 constexpr int kSlabRow = FW + 4;
 
+// What a wavefront's epilogue reads of 32 tokens beside the sums, as bf16 vectors
+// and codes: loaded before the sums of the block in front are worked on, for a
+// load's latency has nothing else to hide behind in a workgroup that ends.
+template <int FW>
+struct Beside {
+  static constexpr int kLanes = FW / 8, kStep = 64 / kLanes, kRows = 32 / kStep;   // lanes of a token, tokens apart, tokens of a lane
+  u32x4 add[kRows];
+  u32x2 codes[kRows], scales;
+};
+
+template <int FW, bool BACK, int FN>
+__device__ __forceinline__ void load_beside(const LayerArgs &a, int64_t t0, int64_t f0, Beside<FW> &b) {
+  using B = Beside<FW>;
+  const int lane = threadIdx.x & 63, r0 = lane / B::kLanes;
+  const int64_t f = f0 + lane % B::kLanes * 8;
+  const bool add = a.add && a.vec_add && !a.f32 && f + 8 <= a.features;
+  b.scales = u32x2{0, 0};
+  if (BACK && FN != kActNone && f < a.features && t0 < a.rows)    // whole groups of eight are in bounds, the pitch being a multiple of 64
+    b.scales = *reinterpret_cast<const u32x2 *>(a.scales + t0 / kActBlock * a.pitch + f);
+#pragma unroll
+  for (int j = 0; j < B::kRows; ++j) {
+    const int64_t t = t0 + r0 + B::kStep * j;
+    if (t >= a.rows) continue;
+    if (add) b.add[j] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.add) + t * a.ldadd + f);
+    if (BACK && FN != kActNone && f < a.features) b.codes[j] = *reinterpret_cast<const u32x2 *>(a.codes + t * a.pitch + f);
+  }
+}
+
 // A wavefront turns the sums of tokens t0 .. t0 + 31 and features f0 .. f0 + FW - 1
-// into results.  A lane has eight features of every RPI-th token.
-template <int FW, bool BACK>
-__device__ __forceinline__ void finish(const LayerArgs &a, OB_LDS const float *slab, int64_t t0, int64_t f0) {
-  constexpr int LPR = FW / 8, RPI = 64 / LPR, NR = 32 / RPI;
-  const int lane = threadIdx.x & 63, c = lane % LPR, r0 = lane / LPR;
+// into results.  A lane has eight features of every kStep-th token.
+template <int FW, bool BACK, int FN>
+__device__ __forceinline__ void finish(const LayerArgs &a, OB_LDS const float *slab, int64_t t0, int64_t f0, const Beside<FW> &b) {
+  using B = Beside<FW>;
+  const int lane = threadIdx.x & 63, c = lane % B::kLanes, r0 = lane / B::kLanes;
   const int64_t f = f0 + c * 8;
   const int n = static_cast<int>(max(int64_t{0}, min(int64_t{8}, a.features - f)));
   const auto sums = [&](int j, float (&v)[8]) __attribute__((always_inline)) {
-    OB_LDS const float *p = slab + (r0 + RPI * j) * kSlabRow<FW> + c * 8;
+    OB_LDS const float *p = slab + (r0 + B::kStep * j) * kSlabRow<FW> + c * 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const f32x4 w = *(OB_LDS const f32x4 *)(p + 4 * h);
@@ -164,8 +163,8 @@ __device__ __forceinline__ void finish(const LayerArgs &a, OB_LDS const float *s
 #pragma unroll
       for (int k = 0; k < 8; ++k) top[k] = 0;
 #pragma unroll
-      for (int j = 0; j < NR; ++j) {
-        if (t0 + r0 + RPI * j < a.rows) {
+      for (int j = 0; j < B::kRows; ++j) {
+        if (t0 + r0 + B::kStep * j < a.rows) {
           float v[8];
           sums(j, v);
 #pragma unroll
@@ -173,7 +172,7 @@ __device__ __forceinline__ void finish(const LayerArgs &a, OB_LDS const float *s
         }
       }
 #pragma unroll
-      for (int d = LPR; d < 64; d <<= 1) {
+      for (int d = B::kLanes; d < 64; d <<= 1) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) top[k] = max(top[k], static_cast<uint32_t>(__shfl_xor(static_cast<int>(top[k]), d)));
       }
@@ -186,38 +185,54 @@ __device__ __forceinline__ void finish(const LayerArgs &a, OB_LDS const float *s
       }
       if (r0 == 0 && t0 < a.rows) write_bytes(a.scales + t0 / kActBlock * a.pitch + f, n, w);
     }
-  } else {
-    if (a.fn != kActNone && n > 0 && t0 < a.rows) {    // whole groups of eight are in bounds, the pitch being a multiple of 64
-      const u32x2 w = *reinterpret_cast<const u32x2 *>(a.scales + t0 / kActBlock * a.pitch + f);
+  } else if constexpr (FN != kActNone) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) scale[k] = act_scale_or_nan((w[k >> 2] >> (8 * (k & 3))) & 0xffu);
-    }
+    for (int k = 0; k < 8; ++k) scale[k] = act_scale_or_nan((b.scales[k >> 2] >> (8 * (k & 3))) & 0xffu);
   }
   if (n <= 0) return;
   const int es = a.f32 ? 4 : 2;
-#pragma unroll 1
-  for (int j = 0; j < NR; ++j) {
-    const int64_t t = t0 + r0 + RPI * j;
-    if (t >= a.rows) break;
+#pragma unroll
+  for (int j = 0; j < B::kRows; ++j) {
+    const int64_t t = t0 + r0 + B::kStep * j;
+    if (t >= a.rows) continue;
     float v[8];
     sums(j, v);
     if constexpr (!BACK) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = v[k] + bias[k];
       if (a.codes) write_bytes(a.codes + t * a.pitch + f, n, a.fmt == kE4M3 ? encode8<kE4M3>(v, scale) : encode8<kInt8>(v, scale));
-      if (a.f32) act8<true>(a.fn, v);
-      else act8<false>(a.fn, v);
-    } else if (a.fn != kActNone) {
-      const u32x2 w = *reinterpret_cast<const u32x2 *>(a.codes + t * a.pitch + f);
+      if constexpr (FN != kActNone) {
+        if (a.f32) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = act_value<FN, true>(v[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = act_value<FN, false>(v[k]);
+        }
+      }
+    } else if constexpr (FN != kActNone) {
       float x[8];
-      if (a.fmt == kE4M3) decode8<kE4M3>(w, scale, x);
-      else decode8<kInt8>(w, scale, x);
-      if (a.f32) slope8<true>(a.fn, x, v);
-      else slope8<false>(a.fn, x, v);
+      if (a.fmt == kE4M3) decode8<kE4M3>(b.codes[j], scale, x);
+      else decode8<kInt8>(b.codes[j], scale, x);
+      if (a.f32) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = v[k] * act_slope<FN, true>(x[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = v[k] * act_slope<FN, false>(x[k]);
+      }
     }
     if (a.add) {
       float r[8];
-      read8(static_cast<const char *>(a.add) + (t * a.ldadd + f) * es, a.f32, a.vec_add, n, r);
+      if (a.vec_add && !a.f32 && n >= 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          r[2 * k] = __uint_as_float(b.add[j][k] << 16);
+          r[2 * k + 1] = __uint_as_float(b.add[j][k] & 0xffff0000u);
+        }
+      } else {
+        read8(static_cast<const char *>(a.add) + (t * a.ldadd + f) * es, a.f32, a.vec_add, n, r);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = v[k] + r[k];
     }
@@ -228,25 +243,40 @@ __device__ __forceinline__ void finish(const LayerArgs &a, OB_LDS const float *s
 // ---------------------------------------------------------------------------
 // the product
 // ---------------------------------------------------------------------------
-// 16-byte unit u of row r of a tile whose rows are 128 bytes along k lies at unit
-// u ^ swizzle_k(r): the 16 rows that one read touches at one k lie on all banks.
-__device__ __forceinline__ int swizzle_k(int r) { return (r >> 1) & 7; }
+// 16-byte unit u of row r of a tile whose rows lie along k, KT steps each, lies at
+// unit u ^ swizzle_k(r): the 16 rows that one read touches at one k lie on all banks.
+template <int KT>
+__device__ __forceinline__ int swizzle_k(int r) { return KT == 64 ? (r >> 1) & 7 : (r >> 2) & 3; }
+
+// f(0), f(1), ... f(N - 1) with constants.
+template <typename F, int... I>
+__device__ __forceinline__ void each(F &&f, std::integer_sequence<int, I...>) { (f(std::integral_constant<int, I>{}), ...); }
+template <int N, typename F>
+__device__ __forceinline__ void each(F &&f) { each(f, std::make_integer_sequence<int, N>{}); }
+
+// The products of two operands' parts that are taken, the small ones first.
+constexpr int kPartA[] = {2, 0, 1, 1, 0, 0}, kPartB[] = {0, 2, 1, 0, 1, 0};
 
 // One workgroup's tile of C over one slice of the contraction: BF features, BT
-// tokens, WF x WT wavefronts.  BACK: A lies along f.
+// tokens, WF x WT wavefronts, PA and PB parts of the operands.  BACK: A lies along f.
 //
-// Stages.  A turn's two steps of 32 read their operands from LDS one step ahead of
-// their products.  The barrier stands between them: behind it the next turn's tile
-// is in LDS and nobody reads the present one any more, so the copies of the turn
-// STAGES ahead go into its place.
-template <int BF, int BT, int WF, int WT, int STAGES, bool BACK>
-__global__ __launch_bounds__(64 * WF * WT, 2) void layer_kernel(const LayerArgs a, const Product q, const Split sp, float *part) {
-  constexpr int NW = WF * WT, FI = BF / WF / 16, FO = BT / WT / 16, FW = FI * 16;
-  constexpr int A_BYTES = BF * kTurn * 2, B_BYTES = BT * kTurn * 2, STAGE = A_BYTES + B_BYTES;
-  constexpr int JA = A_BYTES / 1024 / NW, JB = B_BYTES / 1024 / NW, RA = 512 / BF;
-  static_assert(JA * NW * 1024 == A_BYTES && JB * NW * 1024 == B_BYTES && FO % 2 == 0, "tile shape");
+// Stages.  The operands of a step of 32 are read from LDS one step ahead of their
+// products.  A turn's barrier stands where its last operands have been read: behind
+// it the next turn's tile is in LDS and nobody reads the present one any more, so the
+// copies of the turn STAGES ahead go into its place.
+// Parts: all products of a step run
+// on the same reads, so a part is loaded once a tile and not once a product (fp32
+// 777 x 2048 -> 1000: 27 us for the products one after the other).
+template <int BF, int BT, int WF, int WT, int KT, int PA, int PB, int STAGES, int WGS, bool BACK, int FN>
+__global__ __launch_bounds__(64 * WF * WT, WGS * WF * WT / 4) void layer_kernel(const LayerArgs a, const Product q, const Split sp, float *part) {
+  constexpr int NW = WF * WT, FI = BF / WF / 16, FO = BT / WT / 16, FW = FI * 16;      // fragments of a wavefront
+  constexpr int UNITS = KT / 8, ROWS = 64 / UNITS;       // units of a row, rows of one copy
+  constexpr int A_PART = BF * KT * 2, B_PART = BT * KT * 2, A_BYTES = PA * A_PART, STAGE = A_BYTES + PB * B_PART;
+  constexpr int JA = A_PART / 1024 / NW, JB = B_PART / 1024 / NW, RA = 512 / BF;
+  static_assert(JA * NW * 1024 == A_PART && JB * NW * 1024 == B_PART && FO % 2 == 0, "tile shape");
   static_assert(!BACK || BF >= 128, "the transposing read's swizzle spans eight units");
   static_assert(NW * 32 * kSlabRow<FW> * 4 <= STAGES * STAGE, "the epilogue's sums fit the stages");
+  static_assert(WGS * STAGES * STAGE <= 160 * 1024, "LDS of a CU");
   __shared__ __attribute__((aligned(1024))) unsigned char shared[STAGES * STAGE];
   OB_LDS unsigned char *const lds = (OB_LDS unsigned char *)shared;
 
@@ -254,18 +284,19 @@ __global__ __launch_bounds__(64 * WF * WT, 2) void layer_kernel(const LayerArgs 
   const int wf = wave / WT, wt = wave % WT, g = lane >> 4, li = lane & 15;
   const Where at = where(sp);
   const int64_t f0 = static_cast<int64_t>(at.mt) * BF, t0 = static_cast<int64_t>(at.nt) * BT;
-  const int turns_of_pair = static_cast<int>((q.depth + kTurn - 1) / kTurn);
   const int64_t first = at.split * sp.turns_each;
-  const int turns = static_cast<int>(min(sp.turns_each, static_cast<int64_t>(turns_of_pair) * q.pairs - first));
+  const int turns = static_cast<int>(min(sp.turns_each, (q.depth + KT - 1) / KT - first));
 
   f32x4 acc[FI][FO];
 #pragma unroll
   for (int i = 0; i < FI; ++i)
 #pragma unroll
-    for (int o = 0; o < FO; ++o) acc[i][o] = f32x4{0, 0, 0, 0};
+    for (int o = 0; o < FO; ++o) acc[i][o] = f32x4{};
 
   // Where this lane's 16 bytes of each copy come from: the copies write LDS in
   // lane order, so the swizzle is applied to the source.
+  const auto row_of = [&](int copy) __attribute__((always_inline)) { return copy * ROWS + lane / UNITS; };
+  const auto unit_of = [&](int copy) __attribute__((always_inline)) { return (lane % UNITS) ^ swizzle_k<KT>(row_of(copy)); };
   int from_a[JA], from_b[JB];
 #pragma unroll
   for (int j = 0; j < JA; ++j) {
@@ -273,126 +304,153 @@ __global__ __launch_bounds__(64 * WF * WT, 2) void layer_kernel(const LayerArgs 
       const int r = (wave * JA + j) * RA + lane / (BF / 8), c = lane % (BF / 8);
       from_a[j] = r * static_cast<int>(q.lda) * 2 + (((c >> 1) ^ swizzle_a(r)) << 5) + (c & 1) * 16;
     } else {
-      const int r = (wave * JA + j) * 8 + (lane >> 3);
-      from_a[j] = r * static_cast<int>(q.lda) * 2 + (((lane & 7) ^ swizzle_k(r)) << 4);
+      from_a[j] = row_of(wave * JA + j) * static_cast<int>(q.lda) * 2 + unit_of(wave * JA + j) * 16;
     }
   }
 #pragma unroll
-  for (int j = 0; j < JB; ++j) {
-    const int r = (wave * JB + j) * 8 + (lane >> 3);
-    from_b[j] = r * static_cast<int>(q.ldb) * 2 + (((lane & 7) ^ swizzle_k(r)) << 4);
-  }
+  for (int j = 0; j < JB; ++j) from_b[j] = row_of(wave * JB + j) * static_cast<int>(q.ldb) * 2 + unit_of(wave * JB + j) * 16;
   const int features = static_cast<int>(min(int64_t{BF}, q.features - f0)), tokens = static_cast<int>(min(int64_t{BT}, q.rows - t0));
   const int lda = static_cast<int>(q.lda), ldb = static_cast<int>(q.ldb);
-  // the next turn to be copied: its pair, its place in the pair, how many are left
-  int pair = static_cast<int>(first / turns_of_pair), kt = static_cast<int>(first % turns_of_pair), left = turns;
-
-  const auto start = [&](OB_LDS unsigned char *dst) __attribute__((always_inline)) {
-    const int64_t k0 = static_cast<int64_t>(kt) * kTurn;
-    const int depth = static_cast<int>(min(int64_t{kTurn}, q.depth - k0)), any = -left >> 31;    // all ones or zeros by whether there is a turn
-    const uint16_t *pa = q.a + ((q.a_sel >> (2 * pair)) & 3) * q.a_part, *pb = q.b + ((q.b_sel >> (2 * pair)) & 3) * q.b_part;
-    pa += BACK ? k0 * q.lda + f0 : f0 * q.lda + k0;
-    pb += t0 * q.ldb + k0;
-    const auto ra = buffer(pa, (BACK ? ((static_cast<int>(min(int64_t{kTurn}, q.a_rows - k0)) - 1) * lda + static_cast<int>(q.features - f0)) * 2 : ((features - 1) * lda + depth) * 2) & any);
-    const auto rb = buffer(pb, (((tokens - 1) * ldb + depth) * 2) & any);
-    const bool cut = depth < kTurn;      // units past the contraction's end are read as past the buffer's
+  // The next turn to be copied: where it reads, how much of the contraction is left,
+  // and how many turns.
+  const int64_t k0 = first * KT;
+  const char *at_a = reinterpret_cast<const char *>(q.a + (BACK ? k0 * q.lda + f0 : f0 * q.lda + k0));
+  const char *at_b = reinterpret_cast<const char *>(q.b + t0 * q.ldb + k0);
+  int left = turns, depth = static_cast<int>(q.depth - k0), a_rows = static_cast<int>(q.a_rows - k0);
+  // The copies of a turn: their buffers and offsets, then the copies one by one.
+  // Units past the contraction's end are read as past the buffer's.
+  struct Turn {
+    __amdgpu_buffer_rsrc_t a[PA], b[PB];
+    int from_a[JA], from_b[JB];
+  };
+  const auto aim = [&](Turn &n) __attribute__((always_inline)) {
+    const int any = -left >> 31;     // all ones or zeros by whether there is a turn
+    const int steps = min(depth, KT), rows = min(a_rows, KT);
+    const int size_a = (BACK ? (rows - 1) * lda + static_cast<int>(q.features - f0) : (features - 1) * lda + steps) * 2;
+    const int size_b = ((tokens - 1) * ldb + steps) * 2;
 #pragma unroll
-    for (int j = 0; j < JA; ++j) {
-      int from = from_a[j];
-      if constexpr (!BACK) {
-        const int r = (wave * JA + j) * 8 + (lane >> 3);
-        if (cut && ((lane & 7) ^ swizzle_k(r)) * 8 >= depth) from = 0x7ffffff0;
-      }
-      copy16(ra, dst + (wave * JA + j) * 1024, from);
-    }
+    for (int s = 0; s < PA; ++s) n.a[s] = buffer(at_a + s * q.a_part * 2, size_a & any);
 #pragma unroll
-    for (int j = 0; j < JB; ++j) {
-      int from = from_b[j];
-      const int r = (wave * JB + j) * 8 + (lane >> 3);
-      if (cut && ((lane & 7) ^ swizzle_k(r)) * 8 >= depth) from = 0x7ffffff0;
-      copy16(rb, dst + A_BYTES + (wave * JB + j) * 1024, from);
-    }
+    for (int s = 0; s < PB; ++s) n.b[s] = buffer(at_b + s * q.b_part * 2, size_b & any);
+    const auto inside = [&](int copy, int from) __attribute__((always_inline)) { return unit_of(copy) * 8 < steps ? from : 0x7ffffff0; };
+#pragma unroll
+    for (int j = 0; j < JA; ++j) n.from_a[j] = BACK ? from_a[j] : inside(wave * JA + j, from_a[j]);
+#pragma unroll
+    for (int j = 0; j < JB; ++j) n.from_b[j] = inside(wave * JB + j, from_b[j]);
     --left;
-    if (++kt == turns_of_pair) {
-      kt = 0;
-      if (left > 0) ++pair;
-    }
+    depth -= KT;
+    a_rows -= KT;
+    at_a += BACK ? static_cast<int64_t>(lda) * (KT * 2) : KT * 2;
+    at_b += KT * 2;
   };
-  constexpr int kLoads = JA + JB;
+  constexpr int kLoads = PA * JA + PB * JB;
+  const auto copy = [&](const Turn &n, int c, OB_LDS unsigned char *dst) __attribute__((always_inline)) {
+    if (c < PA * JA) copy16(n.a[c / JA], dst + c / JA * A_PART + (wave * JA + c % JA) * 1024, n.from_a[c % JA]);
+    else copy16(n.b[(c - PA * JA) / JB], dst + A_BYTES + (c - PA * JA) / JB * B_PART + (wave * JB + (c - PA * JA) % JB) * 1024, n.from_b[(c - PA * JA) % JB]);
+  };
 
-  struct Operands {
-    bf16x8 a[FI], b[FO];
+  struct Operands {                // of a step of 32
+    bf16x8 a[PA][FI], b[PB][FO];
   };
-  const int row_a = 8 * g + (li >> 2), sw_a = (li >> 2) | (g & 1) << 2;     // of the transposing read
-  const auto fetch = [&](OB_LDS const unsigned char *T, int kk, Operands &f) __attribute__((always_inline)) {
-    const int unit = ((kk * 4 + g) ^ swizzle_k(li)) << 4;
-#pragma unroll
-    for (int i = 0; i < FI; ++i) {
+  const int row_a = 8 * g + (li >> 2), piece_a = (li & 3) * 8;       // of the transposing read: four k of a lane's feature
+  constexpr int kReads = PA * FI + PB * FO;                          // reads of a step
+  const auto read = [&](OB_LDS const unsigned char *T, int kk, int r, Operands &f) __attribute__((always_inline)) {
+    const int unit = ((kk * 4 + g) ^ swizzle_k<KT>(li)) << 4;
+    if (r < PA * FI) {
+      const int s = r / FI, i = r % FI;
       if constexpr (BACK) {
-        OB_LDS const unsigned char *p = T + (kk * 32 + row_a) * (BF * 2) + (((wf * FI + i) ^ sw_a) << 5) + (li & 3) * 8;
+        OB_LDS const unsigned char *p = T + s * A_PART + (kk * 32 + row_a) * (BF * 2) + (((wf * FI + i) ^ swizzle_a(row_a)) << 5) + piece_a;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p));
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p + 4 * BF * 2));
-        f.a[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        f.a[s][i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
       } else {
-        f.a[i] = *(OB_LDS const bf16x8 *)(T + ((wf * FI + i) * 16 + li) * (kTurn * 2) + unit);
+        f.a[s][i] = *(OB_LDS const bf16x8 *)(T + s * A_PART + ((wf * FI + i) * 16 + li) * (KT * 2) + unit);
       }
-    }
-#pragma unroll
-    for (int o = 0; o < FO; ++o) f.b[o] = *(OB_LDS const bf16x8 *)(T + A_BYTES + ((wt * FO + o) * 16 + li) * (kTurn * 2) + unit);
-  };
-  const auto multiply = [&](const Operands &f) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < FI; ++i)
-#pragma unroll
-      for (int o = 0; o < FO; ++o) acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.a[i], f.b[o], acc[i][o], 0, 0, 0);
-  };
-  // Spreads the reads between the products: the wavefronts of a SIMD come out of
-  // the barrier together, and a run of reads would fill the LDS queue while the
-  // matrix unit stands still.
-  const auto interleave = [&]() __attribute__((always_inline)) {
-    constexpr int kReads = (BACK ? 2 : 1) * FI + FO;
-#pragma unroll
-    for (int k = 0; k < kReads; ++k) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one product
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one read
+    } else {
+      const int s = (r - PA * FI) / FO, o = (r - PA * FI) % FO;
+      f.b[s][o] = *(OB_LDS const bf16x8 *)(T + A_BYTES + s * B_PART + ((wt * FO + o) * 16 + li) * (KT * 2) + unit);
     }
   };
-  // One turn: x holds its first step's operands, and the next turn's afterwards.
-  // The two stages differ, which __restrict says: the compiler would otherwise
-  // hold every read back until all copies have landed.
-  const auto turn = [&](Operands &x, Operands &y, OB_LDS unsigned char *__restrict cur, OB_LDS unsigned char *__restrict next)
-                        __attribute__((always_inline)) {
-    fetch(cur, 1, y);
-    multiply(x);
-    interleave();
-    __builtin_amdgcn_sched_barrier(0);
+  // One step: its products, with the reads of the next
+  // step's operands and the copies spread between them: a run of either would fill its
+  // queue, and a wavefront that waits there issues no products.  The fences keep the
+  // compiler from gathering them again.
+  constexpr int kProducts = PA == 3 && PB == 3 ? 6 : PA * PB, kOne = FI * FO, kMul = kProducts * kOne;
+  constexpr int kSpan = (kMul + 1) / 2;          // reads and copies come with the first half of the products: the next barrier waits for both
+  const auto step = [&](const Operands &x, OB_LDS const unsigned char *from, int kk, Operands &y, auto copies, const Turn &n,
+                        OB_LDS unsigned char *dst) __attribute__((always_inline)) {
+    each<kMul>([&](auto at) __attribute__((always_inline)) {
+      constexpr int m = at, p = m / kOne, i = m % kOne / FO, o = m % FO;
+      constexpr int s = kProducts == 6 ? kPartA[p] : PA == 3 ? 2 - p : 0, u = kProducts == 6 ? kPartB[p] : PB == 3 ? 2 - p : 0;
+      acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.a[s][i], x.b[u][o], acc[i][o], 0, 0, 0);
+      constexpr int r0 = m < kSpan ? m * kReads / kSpan : kReads, r1 = m < kSpan ? (m + 1) * kReads / kSpan : kReads;
+      each<r1 - r0>([&](auto r) __attribute__((always_inline)) { read(from, kk, r0 + r, y); });
+      if constexpr (decltype(copies)::value) {
+        constexpr int c0 = m < kSpan ? m * kLoads / kSpan : kLoads, c1 = m < kSpan ? (m + 1) * kLoads / kSpan : kLoads;
+        each<c1 - c0>([&](auto c) __attribute__((always_inline)) { copy(n, c0 + c, dst); });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  const auto arrived = [&]() __attribute__((always_inline)) {
     wait_loads<(STAGES - 2) * kLoads>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    start(cur);
-    fetch(next, 0, x);
-    multiply(y);
-    interleave();
-    __builtin_amdgcn_sched_barrier(0);
+  };
+  // One turn.  The two stages differ, which __restrict says: the compiler would
+  // otherwise hold every read back until all copies have landed.
+  // Two steps: x holds the first one's operands, and the next turn's afterwards.
+  const auto turn_of_two = [&](Operands &x, Operands &y, OB_LDS unsigned char *__restrict cur, OB_LDS unsigned char *__restrict next)
+                               __attribute__((always_inline)) {
+    Turn n;
+    step(x, cur, 1, y, std::false_type{}, n, cur);
+    aim(n);
+    arrived();
+    step(y, next, 0, x, std::true_type{}, n, cur);
+  };
+  // One step: x holds its operands, y the next turn's afterwards.
+  const auto turn_of_one = [&](Operands &x, Operands &y, OB_LDS unsigned char *__restrict cur, OB_LDS unsigned char *__restrict next)
+                               __attribute__((always_inline)) {
+    Turn n;
+    aim(n);
+    arrived();
+    step(x, next, 0, y, std::true_type{}, n, cur);
   };
 
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) start(lds + s * STAGE);
+  for (int s = 0; s < STAGES; ++s) {
+    Turn n;
+    aim(n);
+#pragma unroll
+    for (int c = 0; c < kLoads; ++c) copy(n, c, lds + s * STAGE);
+  }
   wait_loads<(STAGES - 1) * kLoads>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   {
     Operands x, y;
-    fetch(lds, 0, x);
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(lds, 0, r, x);
     int stage = 0;
-    for (int t = 0; t < turns; ++t) {
+    const auto stages = [&](auto &&turn, Operands &x, Operands &y) __attribute__((always_inline)) {
       const int next = stage + 1 == STAGES ? 0 : stage + 1;
       turn(x, y, lds + stage * STAGE, lds + next * STAGE);
       stage = next;
+    };
+    if constexpr (KT == 64) {
+      for (int t = 0; t < turns; ++t) stages(turn_of_two, x, y);
+    } else {
+      // in pairs without a way out between them, past which the compiler would move the reads
+      for (int t = turns / 2; t > 0; --t) {
+        stages(turn_of_one, x, y);
+        stages(turn_of_one, y, x);
+      }
+      if (turns % 2) stages(turn_of_one, x, y);
     }
   }
   wait_loads<0>();                 // no copy may land after the workgroup has ended, or in the epilogue's sums
 
+  // A lane's sums: four features of one token of a fragment.
   if (part) {
     const int64_t ldp = (q.features + 3) / 4 * 4;
     float *out = part + at.split * q.rows * ldp;
@@ -408,6 +466,9 @@ __global__ __launch_bounds__(64 * WF * WT, 2) void layer_kernel(const LayerArgs 
     }
     return;
   }
+  const int64_t mine = t0 + wt * FO * 16, at_f = f0 + wf * FW;
+  Beside<FW> beside[2];
+  load_beside<FW, BACK, FN>(a, mine, at_f, beside[0]);
   __builtin_amdgcn_s_barrier();    // nobody reads the tiles any more
   asm volatile("" ::: "memory");
   OB_LDS float *slab = (OB_LDS float *)lds + wave * 32 * kSlabRow<FW>;
@@ -417,40 +478,307 @@ __global__ __launch_bounds__(64 * WF * WT, 2) void layer_kernel(const LayerArgs 
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < FI; ++i) *(OB_LDS f32x4 *)(slab + (h * 16 + li) * kSlabRow<FW> + i * 16 + g * 4) = acc[i][o + h];
+    if (o + 2 < FO) load_beside<FW, BACK, FN>(a, mine + (o + 2) * 16, at_f, beside[(o / 2 + 1) & 1]);
     __builtin_amdgcn_wave_barrier();
-    finish<FW, BACK>(a, slab, t0 + (wt * FO + o) * 16, f0 + wf * FW);
+    finish<FW, BACK, FN>(a, slab, mine + o * 16, at_f, beside[(o / 2) & 1]);
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-// The slices' sums in order, and the epilogue: a wavefront takes 32 tokens of 64
-// features.
-constexpr int kJoinWidth = 64;
-template <bool BACK>
-__global__ __launch_bounds__(kBlock) void layer_join_kernel(const LayerArgs a, const float *part, int splits) {
-  __shared__ __attribute__((aligned(16))) float shared[kWaves * 32 * kSlabRow<kJoinWidth>];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+// The slices' sums and the epilogue: a workgroup takes 32 tokens of 32 features, in
+// GROUPS groups of 256 work-items that add up every GROUPS-th slice (few tokens in
+// many slices would otherwise wait for one load after the other: 32 tokens of 1024
+// features in 32 slices took 20 us with a wavefront a block).
+constexpr int kJoinWidth = 32;
+template <int GROUPS, bool BACK, int FN>
+__global__ __launch_bounds__(kBlock * GROUPS) void layer_join_kernel(const LayerArgs a, const float *part, int splits) {
+  constexpr int SLAB = 32 * kSlabRow<kJoinWidth>;
+  __shared__ __attribute__((aligned(16))) float shared[GROUPS * SLAB];
+  OB_LDS float *slabs = (OB_LDS float *)shared;
   const uint32_t across = static_cast<uint32_t>((a.features + kJoinWidth - 1) / kJoinWidth);
-  const uint32_t id = blockIdx.x * kWaves + wave, band = id / across;
-  const int64_t t0 = static_cast<int64_t>(band) * 32, f0 = static_cast<int64_t>(id - band * across) * kJoinWidth;
-  if (t0 >= a.rows) return;
+  const uint32_t band = blockIdx.x / across;
+  const int64_t t0 = static_cast<int64_t>(band) * 32, f0 = static_cast<int64_t>(blockIdx.x - band * across) * kJoinWidth;
   const int64_t ldp = (a.features + 3) / 4 * 4, each = a.rows * ldp;
-  OB_LDS float *slab = (OB_LDS float *)shared + wave * 32 * kSlabRow<kJoinWidth>;
-  const int c = lane % 16, r0 = lane / 16;
-  const int64_t f = f0 + c * 4;
-#pragma unroll 2
-  for (int j = 0; j < 8; ++j) {
-    const int64_t t = t0 + r0 + 4 * j;
-    f32x4 v = {0, 0, 0, 0};
-    if (t < a.rows && f < a.features) {
-      const float *p = part + t * ldp + f;
+  const int group = threadIdx.x / kBlock, id = threadIdx.x % kBlock, r = id / 8, c = id % 8 * 4;
+  Beside<kJoinWidth> beside;
+  if (threadIdx.x < 64) load_beside<kJoinWidth, BACK, FN>(a, t0, f0, beside);
+  f32x4 v = {0, 0, 0, 0};
+  if (t0 + r < a.rows && f0 + c < a.features) {
+    const float *p = part + (t0 + r) * ldp + f0 + c;
 #pragma unroll 4
-      for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * each);
-    }
-    *(OB_LDS f32x4 *)(slab + (r0 + 4 * j) * kSlabRow<kJoinWidth> + c * 4) = v;
+    for (int s = group; s < splits; s += GROUPS) v += *reinterpret_cast<const f32x4 *>(p + s * each);
   }
-  __builtin_amdgcn_wave_barrier();
-  finish<kJoinWidth, BACK>(a, slab, t0, f0);
+  OB_LDS f32x4 *mine = (OB_LDS f32x4 *)(slabs + group * SLAB + r * kSlabRow<kJoinWidth> + c);
+  *mine = v;
+  __syncthreads();
+  if constexpr (GROUPS > 1) {
+    if (group == 0) {
+#pragma unroll
+      for (int s = 1; s < GROUPS; ++s) v += *(OB_LDS f32x4 *)(slabs + s * SLAB + r * kSlabRow<kJoinWidth> + c);
+      *mine = v;
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x < 64) finish<kJoinWidth, BACK, FN>(a, slabs, t0, f0, beside);
+}
+
+// ---------------------------------------------------------------------------
+// a few tokens: bound by reading the weight
+// ---------------------------------------------------------------------------
+// Up to kFewTokens tokens are multiplied on the vector units in fp32, straight from
+// the weight as it lies in the list, whatever its type or alignment.
+constexpr int kFewTokens = 8;
+constexpr int kFewRows = 4;           // forward: features of a wavefront
+constexpr int kFewLanes = 4;          // backward: lanes, of eight features each, of a workgroup
+constexpr int kFewBlock = 512, kFewGroups = kFewBlock / kFewLanes;
+constexpr int kFewEach = 8, kFewChunk = kFewEach * kFewGroups;        // backward: rows of a group, of a workgroup, under way together
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
+// Eight elements of a row as they lie, from anywhere; the last of a row one by one.
+template <typename T>
+struct Eight {
+  T v[8];
+  __device__ __forceinline__ void load(const T *p) { __builtin_memcpy(v, p, sizeof(v)); }
+  __device__ __forceinline__ void load_some(const T *p, int64_t n) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < n ? p[k] : T{0};
+  }
+  __device__ __forceinline__ float operator[](int k) const { return to_f32(v[k]); }
+};
+
+// Sums v over the lanes whose numbers differ in the bits D down to LAST, each lane
+// keeping a part of the N sums (one at least), from the returned one on.
+template <int N, int D, int LAST, int SIZE>
+__device__ __forceinline__ int scatter_sums(float (&v)[SIZE]) {
+  if constexpr (D < LAST) {
+    return 0;
+  } else if constexpr (N == 1) {
+    v[0] += __shfl_xor(v[0], D);
+    return scatter_sums<1, D / 2, LAST>(v);
+  } else {
+    const bool up = threadIdx.x & D;
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+      const float send = up ? v[k] : v[k + N / 2], keep = up ? v[k + N / 2] : v[k];
+      v[k] = keep + __shfl_xor(send, D);
+    }
+    return (up ? N / 2 : 0) + scatter_sums<N / 2, D / 2, LAST>(v);
+  }
+}
+
+// The epilogue for one feature of R tokens.
+template <int R, bool BACK, int FN>
+__device__ __forceinline__ void finish_few(const LayerArgs &a, int64_t f, float (&h)[8]) {
+  const int rows = static_cast<int>(a.rows);
+  if constexpr (!BACK) {
+    if (a.bias) {
+      const float b = a.weight_f32 ? static_cast<const float *>(a.bias)[f] : to_f32(static_cast<const uint16_t *>(a.bias)[f]);
+#pragma unroll
+      for (int t = 0; t < R; ++t) h[t] = h[t] + b;
+    }
+    if (a.codes) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int t = 0; t < R; ++t)
+        if (t < rows) top = max(top, __float_as_uint(h[t]) & 0x7fffffffu);
+      const uint32_t s = a.fmt == kE4M3 ? act_scale<kE4M3>(top) : act_scale<kInt8>(top);
+      float inv[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) inv[t] = a.fmt == kE4M3 ? act_inverse<kE4M3>(s) : act_inverse<kInt8>(s);
+      const u32x2 w = a.fmt == kE4M3 ? encode8<kE4M3>(h, inv) : encode8<kInt8>(h, inv);
+      a.scales[f] = static_cast<uint8_t>(s);
+#pragma unroll
+      for (int t = 0; t < R; ++t)
+        if (t < rows) a.codes[t * a.pitch + f] = static_cast<uint8_t>(w[t >> 2] >> (8 * (t & 3)));
+    }
+    if constexpr (FN != kActNone) {
+#pragma unroll
+      for (int t = 0; t < R; ++t) h[t] = a.f32 ? act_value<FN, true>(h[t]) : act_value<FN, false>(h[t]);
+    }
+  } else if constexpr (FN != kActNone) {
+    u32x2 w = {0, 0};
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+      if (t < rows) w[t >> 2] |= static_cast<uint32_t>(a.codes[t * a.pitch + f]) << (8 * (t & 3));
+    float scale[8], x[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) scale[t] = act_scale_or_nan(a.scales[f]);
+    if (a.fmt == kE4M3) decode8<kE4M3>(w, scale, x);
+    else decode8<kInt8>(w, scale, x);
+#pragma unroll
+    for (int t = 0; t < R; ++t) h[t] = h[t] * (a.f32 ? act_slope<FN, true>(x[t]) : act_slope<FN, false>(x[t]));
+  }
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    if (t < rows) {
+      if (a.f32) {
+        if (a.add) h[t] = h[t] + static_cast<const float *>(a.add)[t * a.ldadd + f];
+        static_cast<float *>(a.y)[t * a.ldy + f] = h[t];
+      } else {
+        if (a.add) h[t] = h[t] + to_f32(static_cast<const uint16_t *>(a.add)[t * a.ldadd + f]);
+        static_cast<uint16_t *>(a.y)[t * a.ldy + f] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(h[t]));
+      }
+    }
+  }
+}
+
+// The activation as a constant: finish_few is small, the kernels in front of it are many.
+template <int R, bool BACK>
+__device__ __forceinline__ void finish_few(const LayerArgs &a, int64_t f, float (&h)[8]) {
+  if (a.fn == kActGelu) finish_few<R, BACK, kActGelu>(a, f, h);
+  else if (a.fn == kActGeluTanh) finish_few<R, BACK, kActGeluTanh>(a, f, h);
+  else if (a.fn == kActSilu) finish_few<R, BACK, kActSilu>(a, f, h);
+  else finish_few<R, BACK, kActNone>(a, f, h);
+}
+
+// Forward: a wavefront multiplies kFewRows rows of the weight with all tokens, 512
+// steps of the contraction at a time.  SLICED: the four wavefronts of a workgroup
+// share the rows and divide the contraction; otherwise each has rows of its own.
+template <int R, typename TW, typename TX, bool SLICED>
+__global__ __launch_bounds__(kBlock) void layer_few_kernel(const LayerArgs a) {
+  constexpr int FEATURES = SLICED ? kFewRows : kFewRows * kWaves;      // of a workgroup
+  __shared__ float sums[kWaves][kFewRows * R];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t g0 = static_cast<int64_t>(blockIdx.x) * FEATURES, f0 = SLICED ? g0 : g0 + wave * kFewRows;
+  const int64_t depth = a.shape.in;
+  float acc[kFewRows * R];
+#pragma unroll
+  for (int k = 0; k < kFewRows * R; ++k) acc[k] = 0.0f;
+  const TW *w0[kFewRows];
+  const TX *x0[R];
+#pragma unroll
+  for (int o = 0; o < kFewRows; ++o) w0[o] = static_cast<const TW *>(a.weight) + min(f0 + o, a.features - 1) * depth + lane * 8;
+#pragma unroll
+  for (int t = 0; t < R; ++t) x0[t] = static_cast<const TX *>(a.x) + min(static_cast<int64_t>(t), a.rows - 1) * a.ldx + lane * 8;
+  const auto add = [&](const Eight<TW> (&w)[kFewRows], const Eight<TX> (&x)[R]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int o = 0; o < kFewRows; ++o)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[o * R + t] = __builtin_fmaf(w[o][k], x[t][k], acc[o * R + t]);
+  };
+  constexpr int STEP = SLICED ? 512 * kWaves : 512;
+  int64_t k0 = SLICED ? wave * 512 : 0;
+#pragma unroll 2
+  for (; k0 + 512 <= depth; k0 += STEP) {
+    Eight<TW> w[kFewRows];
+    Eight<TX> x[R];
+#pragma unroll
+    for (int o = 0; o < kFewRows; ++o) w[o].load(w0[o] + k0);
+#pragma unroll
+    for (int t = 0; t < R; ++t) x[t].load(x0[t] + k0);
+    add(w, x);
+  }
+  if (k0 < depth) {
+    const int64_t n = depth - k0 - lane * 8;
+    Eight<TW> w[kFewRows];
+    Eight<TX> x[R];
+#pragma unroll
+    for (int o = 0; o < kFewRows; ++o) w[o].load_some(w0[o] + k0, n);
+#pragma unroll
+    for (int t = 0; t < R; ++t) x[t].load_some(x0[t] + k0, n);
+    add(w, x);
+  }
+  const int at = scatter_sums<kFewRows * R, 32, 1>(acc);
+  if constexpr (kFewRows * R == 32) {
+    if ((lane & 1) == 0) sums[wave][at] = acc[0];
+  } else {
+    if ((lane & (64 / (kFewRows * R) - 1)) == 0) sums[wave][at] = acc[0];
+  }
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c >= FEATURES || g0 + c >= a.features) return;
+  float h[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    h[t] = 0.0f;
+    if (t < R) {
+      if constexpr (SLICED) {
+#pragma unroll
+        for (int s = 0; s < kWaves; ++s) h[t] += sums[s][c * R + t];
+      } else {
+        h[t] = sums[c / kFewRows][c % kFewRows * R + t];
+      }
+    }
+  }
+  finish_few<R, false>(a, g0 + c, h);
+}
+
+// Backward: kFewLanes lanes take eight features each of one row of the weight, the
+// workgroup's 128 groups of them kFewEach rows each, all under way together: a slice
+// of the contraction, whose sums go to `part` where there are several.  Neighbouring
+// workgroups' features share cache lines, so they are given to one XCD.
+template <int R, typename TW, typename TX>
+__global__ __launch_bounds__(kFewBlock) void layer_few_back_kernel(const LayerArgs a, float *part) {
+  constexpr int FEATURES = kFewLanes * 8, WAVES = kFewBlock / 64;
+  __shared__ __attribute__((aligned(16))) float dys[kFewChunk][R];
+  __shared__ float sums[WAVES][R][FEATURES];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = threadIdx.x / kFewLanes, l = threadIdx.x % kFewLanes;
+  const uint32_t xcd = blockIdx.x % kXcds, place = xcd * (gridDim.x / kXcds) + min(xcd, gridDim.x % kXcds) + blockIdx.x / kXcds;
+  const int64_t g0 = static_cast<int64_t>(place) * FEATURES, f = g0 + l * 8, c0 = static_cast<int64_t>(blockIdx.y) * kFewChunk;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(kFewChunk), a.shape.out - c0));
+  const int64_t n = a.features - f;
+  Eight<TW> w[kFewEach];
+#pragma unroll
+  for (int e = 0; e < kFewEach; ++e) {
+    const TW *p = static_cast<const TW *>(a.weight) + (c0 + min(group + e * kFewGroups, rows - 1)) * a.features + f;
+    if (n >= 8) w[e].load(p);
+    else w[e].load_some(p, n);
+  }
+#pragma unroll
+  for (int t = 0; t < R; ++t)
+    for (int o = threadIdx.x; o < rows; o += kFewBlock)
+      dys[o][t] = t < a.rows ? to_f32(static_cast<const TX *>(a.x)[t * a.ldx + c0 + o]) : 0.0f;
+  __syncthreads();
+  float acc[R * 8];
+#pragma unroll
+  for (int k = 0; k < R * 8; ++k) acc[k] = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kFewEach; ++e) {
+    const int o = group + e * kFewGroups;
+    if (o < rows) {
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        const float y = dys[o][t];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[t * 8 + k] = __builtin_fmaf(y, w[e][k], acc[t * 8 + k]);
+      }
+    }
+  }
+  constexpr int KEPT = R * 8 * kFewLanes / 64 > 0 ? R * 8 * kFewLanes / 64 : 1;      // sums that a lane is left with
+  const int at = scatter_sums<R * 8, 32, kFewLanes>(acc);
+  // with fewer sums than lanes the last of the lanes' bits hold copies
+  if (R * 8 * kFewLanes >= 64 || (lane & kFewLanes) == 0) {
+#pragma unroll
+    for (int k = 0; k < KEPT; ++k) sums[wave][(at + k) / 8][l * 8 + (at + k) % 8] = acc[k];
+  }
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c >= FEATURES || g0 + c >= a.features) return;
+  float h[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    h[t] = 0.0f;
+    if (t < R) {
+#pragma unroll
+      for (int s = 0; s < WAVES; ++s) h[t] += sums[s][t][c];
+    }
+  }
+  if (part) {
+    const int64_t ldp = (a.features + 3) / 4 * 4;
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+      if (t < a.rows) part[(blockIdx.y * a.rows + t) * ldp + g0 + c] = h[t];
+    return;
+  }
+  finish_few<R, true>(a, g0 + c, h);
 }
 
 // ---------------------------------------------------------------------------
@@ -461,6 +789,7 @@ __global__ __launch_bounds__(kBlock) void layer_join_kernel(const LayerArgs a, c
 // as one.
 struct PackArgs {
   const void *from;
+  bool f32;
   int64_t ld;
   uint16_t *to;
   int64_t rows, cols, pitch;
@@ -484,27 +813,23 @@ __device__ __forceinline__ void parts3(float x, uint16_t (&h)[3]) {
 }
 
 template <typename T>
-__global__ __launch_bounds__(kBlock) void pack_kernel(const PackArgs a) {
-  const int64_t units = a.pitch / 8, total = a.rows * units, step = static_cast<int64_t>(gridDim.x) * kBlock;
-  for (int64_t id = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; id < total; id += step) {
+__device__ __forceinline__ void pack_units(const PackArgs &a, int64_t first, int64_t step) {
+  const int64_t units = a.pitch / 8, total = a.rows * units;
+  for (int64_t id = first; id < total; id += step) {
     const int64_t r = id / units, c = (id - r * units) * 8;
+    Eight<T> v;
     const T *p = static_cast<const T *>(a.from) + r * a.ld + c;
-    T v[8];
-    if (c + 8 <= a.cols) {
-      __builtin_memcpy(v, p, sizeof(v));       // rows start anywhere
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = c + k < a.cols ? p[k] : T{0};
-    }
+    if (c + 8 <= a.cols) v.load(p);
+    else v.load_some(p, a.cols - c);
     uint16_t *out = a.to + r * a.pitch + c;
     if constexpr (sizeof(T) == 2) {
-      __builtin_memcpy(__builtin_assume_aligned(out, 16), v, 16);
+      __builtin_memcpy(__builtin_assume_aligned(out, 16), v.v, 16);
     } else {
       uint16_t w[3][8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         uint16_t h[3];
-        parts3(v[k], h);
+        parts3(v.v[k], h);
 #pragma unroll
         for (int s = 0; s < 3; ++s) w[s][k] = h[s];
       }
@@ -514,32 +839,70 @@ __global__ __launch_bounds__(kBlock) void pack_kernel(const PackArgs a) {
   }
 }
 
+// The weight by the first `blocks` workgroups, x or dy by the others.
+__global__ __launch_bounds__(kBlock) void pack_kernel(const PackArgs a, const PackArgs b, uint32_t blocks) {
+  const bool first = blockIdx.x < blocks;
+  const PackArgs &p = first ? a : b;
+  const int64_t at = static_cast<int64_t>(first ? blockIdx.x : blockIdx.x - blocks) * kBlock + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(first ? blocks : gridDim.x - blocks) * kBlock;
+  if (p.f32) pack_units<float>(p, at, step);
+  else pack_units<uint16_t>(p, at, step);
+}
+
 // ---------------------------------------------------------------------------
 // plans
 // ---------------------------------------------------------------------------
+// Tiles that are built, and their times in microseconds: of a workgroup's start and
+// end, of a turn on a CU of its own and with as many workgroups as a CU holds.
 struct Tiles {
-  int features, tokens;
+  int features, tokens, depth, per_cu;
+  double start, alone, full;
 };
-constexpr Tiles kTiles[] = {{256, 256}, {128, 128}, {128, 32}};
+constexpr Tiles kPlainTiles[] = {{256, 256, 64, 1, 9.0, 1.40, 1.40}, {128, 128, 64, 2, 4.5, 0.60, 1.0}, {128, 32, 64, 2, 4.0, 0.40, 0.55}};
+constexpr Tiles kPartTiles[] = {{128, 128, 32, 1, 5.0, 1.25, 1.25}, {128, 64, 32, 1, 4.0, 0.62, 0.62}};      // six products
+constexpr Tiles kThreeTiles[] = {{128, 128, 32, 2, 5.0, 0.50, 0.85}, {128, 64, 32, 2, 4.0, 0.40, 0.60}};      // three
 
 int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t features_of(const LayerShape &s) { return s.back ? s.in : s.out; }
 int64_t depth_of(const LayerShape &s) { return s.back ? s.out : s.in; }
 
-template <int BF, int BT, int WF, int WT, int STAGES>
+// Calls f with the direction and the activation as constants.
+template <typename F>
+void by_kind(const LayerArgs &a, F &&f) {
+  const auto by_fn = [&](auto back) {
+    if (a.fn == kActGelu) f(back, std::integral_constant<int, kActGelu>{});
+    else if (a.fn == kActGeluTanh) f(back, std::integral_constant<int, kActGeluTanh>{});
+    else if (a.fn == kActSilu) f(back, std::integral_constant<int, kActSilu>{});
+    else f(back, std::integral_constant<int, kActNone>{});
+  };
+  if (a.shape.back) by_fn(std::true_type{});
+  else by_fn(std::false_type{});
+}
+
+template <int BF, int BT, int WF, int WT, int KT, int PA, int PB, int STAGES, int WGS>
 void layer_one(const LayerArgs &a, const LayerPlan &p, const Product &q, float *part, hipStream_t s) {
   const Split sp{p.m_tiles, p.n_tiles, p.splits, p.turns_each};
   const dim3 grid(static_cast<unsigned>(p.m_tiles) * p.n_tiles * p.splits);
-  if (a.shape.back) layer_kernel<BF, BT, WF, WT, STAGES, true><<<grid, 64 * WF * WT, 0, s>>>(a, q, sp, part);
-  else layer_kernel<BF, BT, WF, WT, STAGES, false><<<grid, 64 * WF * WT, 0, s>>>(a, q, sp, part);
+  by_kind(a, [&](auto back, auto fn) {
+    layer_kernel<BF, BT, WF, WT, KT, PA, PB, STAGES, WGS, decltype(back)::value, decltype(fn)::value>
+        <<<grid, 64 * WF * WT, 0, s>>>(a, q, sp, part);
+  });
 }
 
-void pack(const void *from, bool f32, int64_t ld, int64_t rows, int64_t cols, void *to, hipStream_t s) {
-  const PackArgs a{from, ld, static_cast<uint16_t *>(to), rows, cols, up64(cols)};
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((rows * (a.pitch / 8) + kBlock - 1) / kBlock, 1 << 16)));
-  if (f32) pack_kernel<float><<<grid, kBlock, 0, s>>>(a);
-  else pack_kernel<uint16_t><<<grid, kBlock, 0, s>>>(a);
+template <int R, typename TW, typename TX>
+void layer_few(const LayerArgs &a, int slices, float *part, hipStream_t s) {
+  const auto groups = [&](int64_t each) { return static_cast<unsigned>((a.features + each - 1) / each); };
+  if (a.shape.back) layer_few_back_kernel<R, TW, TX><<<dim3(groups(kFewLanes * 8), slices), kFewBlock, 0, s>>>(a, part);
+  else if (a.features >= 4096) layer_few_kernel<R, TW, TX, false><<<groups(kFewRows * kWaves), kBlock, 0, s>>>(a);
+  else layer_few_kernel<R, TW, TX, true><<<groups(kFewRows), kBlock, 0, s>>>(a);
+}
+
+template <typename TW, typename TX>
+void layer_few_by_rows(const LayerArgs &a, int slices, float *part, hipStream_t s) {
+  if (a.rows == 1) layer_few<1, TW, TX>(a, slices, part, s);
+  else if (a.rows <= 4) layer_few<4, TW, TX>(a, slices, part, s);
+  else layer_few<8, TW, TX>(a, slices, part, s);
 }
 
 char *work_at(const LayerArgs &a, size_t bytes) { return static_cast<char *>(a.work) + bytes; }
@@ -556,35 +919,40 @@ bool layer_fits(int64_t rows, int64_t out, int64_t in) {
 LayerPlan layer_plan(const LayerShape &s) {
   LayerPlan p{};
   const int64_t features = features_of(s), depth = depth_of(s);
-  p.a_parts = s.weight_f32 ? 3 : 1;
-  p.b_parts = s.f32 ? 3 : 1;
-  p.pack_a = s.weight_f32 || s.in % 8 != 0;
-  p.pack_b = s.f32 || depth % 8 != 0 || !s.aligned;
-  const int pairs = p.a_parts == 3 && p.b_parts == 3 ? 6 : std::max(p.a_parts, p.b_parts);
-  const int64_t turns = (depth + kTurn - 1) / kTurn * pairs;
-  if (p.pack_a) p.a_bytes = up256(static_cast<size_t>(p.a_parts) * s.out * up64(s.in) * 2);
-  if (p.pack_b) p.b_bytes = up256(static_cast<size_t>(p.b_parts) * s.rows * up64(depth) * 2);
-  const double part = static_cast<double>(s.rows) * features * 4 / 3e6;
-  constexpr double kStart[] = {11.0, 5.0, 4.0}, kAlone[] = {1.6, 0.8, 0.45}, kFull[] = {1.6, 1.1, 0.6};
-  constexpr int kPerCu[] = {1, 2, 2};
-  double best = 0.0;
-  p.tile = -1;
-  for (int k = 0; k < 3; ++k) {
-    const int64_t m = (features + kTiles[k].features - 1) / kTiles[k].features, n = (s.rows + kTiles[k].tokens - 1) / kTiles[k].tokens;
-    const int64_t most = m * n >= 512 ? 1 : std::min<int64_t>(turns, 64);      // no slices where the tiles fill the card
-    for (int64_t want = 1; want <= most; ++want) {
-      const int64_t each = (turns + want - 1) / want, splits = (turns + each - 1) / each, groups = m * n * splits;
-      if (splits != want || groups > kMaxGrid / 2) continue;
-      double t = kStart[k] + (splits > 1 ? 4.0 + splits * part : 0.0);
-      if (groups <= 256) t += each * kAlone[k];
-      else t += static_cast<double>((groups + 256 * kPerCu[k] - 1) / (256 * kPerCu[k])) * each * kFull[k];
-      if (p.tile < 0 || t < best) {
-        best = t;
-        p.tile = k;
-        p.m_tiles = static_cast<int>(m);
-        p.n_tiles = static_cast<int>(n);
-        p.splits = static_cast<int>(splits);
-        p.turns_each = each;
+  p.splits = 1;
+  if (s.rows <= kFewTokens) {
+    p.tile = -1;
+    if (s.back) p.splits = static_cast<int>((depth + kFewChunk - 1) / kFewChunk);
+  } else {
+    p.a_parts = s.weight_f32 ? 3 : 1;
+    p.b_parts = s.f32 ? 3 : 1;
+    p.pack_a = s.weight_f32 || s.in % 8 != 0;
+    p.pack_b = s.f32 || depth % 8 != 0 || !s.aligned;
+    if (p.pack_a) p.a_bytes = up256(static_cast<size_t>(p.a_parts) * s.out * up64(s.in) * 2);
+    if (p.pack_b) p.b_bytes = up256(static_cast<size_t>(p.b_parts) * s.rows * up64(depth) * 2);
+    const int products = p.a_parts * p.b_parts;
+    const Tiles *tiles = products == 1 ? kPlainTiles : products == 9 ? kPartTiles : kThreeTiles;
+    const double part = static_cast<double>(s.rows) * features * 4 / 3e6;
+    double best = 0.0;
+    p.tile = -1;
+    for (int k = 0; k < (products == 1 ? 3 : 2); ++k) {
+      const int64_t m = (features + tiles[k].features - 1) / tiles[k].features, n = (s.rows + tiles[k].tokens - 1) / tiles[k].tokens;
+      const int64_t turns = (depth + tiles[k].depth - 1) / tiles[k].depth, most = m * n >= 512 ? 1 : std::min<int64_t>(turns, 64);      // no slices where the tiles fill the card
+      for (int64_t want = 1; want <= most; ++want) {
+        const int64_t each = (turns + want - 1) / want, splits = (turns + each - 1) / each, groups = m * n * splits;
+        if (splits != want || groups > kMaxGrid / 2) continue;
+        double t = tiles[k].start + (splits > 1 ? 4.0 + splits * part : 0.0);
+        const int64_t held = 256 * tiles[k].per_cu;
+        if (groups <= 256) t += each * tiles[k].alone;
+        else t += static_cast<double>((groups + held - 1) / held) * each * tiles[k].full;
+        if (p.tile < 0 || t < best) {
+          best = t;
+          p.tile = k;
+          p.m_tiles = static_cast<int>(m);
+          p.n_tiles = static_cast<int>(n);
+          p.splits = static_cast<int>(splits);
+          p.turns_each = each;
+        }
       }
     }
   }
@@ -593,11 +961,28 @@ LayerPlan layer_plan(const LayerShape &s) {
 }
 
 void launch_layer_pack(const LayerArgs &a, const LayerPlan &p, hipStream_t s) {
-  if (p.pack_a) pack(a.weight, a.weight_f32, a.shape.in, a.shape.out, a.shape.in, work_at(a, 0), s);
-  if (p.pack_b) pack(a.x, a.f32, a.ldx, a.rows, depth_of(a.shape), work_at(a, p.a_bytes), s);
+  const int64_t depth = depth_of(a.shape);
+  const PackArgs w{a.weight, a.weight_f32, a.shape.in, static_cast<uint16_t *>(a.work), a.shape.out, a.shape.in, up64(a.shape.in)};
+  const PackArgs x{a.x, a.f32, a.ldx, reinterpret_cast<uint16_t *>(work_at(a, p.a_bytes)), a.rows, depth, up64(depth)};
+  const auto blocks = [](const PackArgs &q) {
+    return static_cast<uint32_t>(std::min<int64_t>((q.rows * (q.pitch / 8) + kBlock - 1) / kBlock, 1 << 15));
+  };
+  const uint32_t first = p.pack_a ? blocks(w) : 0, others = p.pack_b ? blocks(x) : 0;
+  pack_kernel<<<first + others, kBlock, 0, s>>>(w, x, first);
 }
 
 void launch_layer(const LayerArgs &a, const LayerPlan &p, hipStream_t s) {
+  float *part = p.splits > 1 ? reinterpret_cast<float *>(work_at(a, p.a_bytes + p.b_bytes)) : nullptr;
+  if (p.tile < 0) {
+    if (a.weight_f32) {
+      if (a.f32) layer_few_by_rows<float, float>(a, p.splits, part, s);
+      else layer_few_by_rows<float, uint16_t>(a, p.splits, part, s);
+    } else {
+      if (a.f32) layer_few_by_rows<uint16_t, float>(a, p.splits, part, s);
+      else layer_few_by_rows<uint16_t, uint16_t>(a, p.splits, part, s);
+    }
+    return;
+  }
   const int64_t depth = depth_of(a.shape);
   Product q{};
   q.rows = a.rows;
@@ -610,32 +995,29 @@ void launch_layer(const LayerArgs &a, const LayerPlan &p, hipStream_t s) {
   q.b = static_cast<const uint16_t *>(p.pack_b ? work_at(a, p.a_bytes) : a.x);
   q.ldb = p.pack_b ? up64(depth) : a.ldx;
   q.b_part = a.rows * q.ldb;
-  if (p.a_parts == 3 && p.b_parts == 3) {      // small products first
-    constexpr uint32_t kA[] = {2, 0, 1, 1, 0, 0}, kB[] = {0, 2, 1, 0, 1, 0};
-    q.pairs = 6;
-    for (int k = 0; k < 6; ++k) {
-      q.a_sel |= kA[k] << (2 * k);
-      q.b_sel |= kB[k] << (2 * k);
-    }
+  if (p.a_parts * p.b_parts == 1) {
+    if (p.tile == 0) layer_one<256, 256, 4, 2, 64, 1, 1, 2, 1>(a, p, q, part, s);
+    else if (p.tile == 1) layer_one<128, 128, 4, 2, 64, 1, 1, 2, 2>(a, p, q, part, s);
+    else layer_one<128, 32, 4, 1, 64, 1, 1, 4, 2>(a, p, q, part, s);
+  } else if (p.a_parts == 3 && p.b_parts == 3) {
+    if (p.tile == 0) layer_one<128, 128, 2, 2, 32, 3, 3, 3, 1>(a, p, q, part, s);
+    else layer_one<128, 64, 4, 1, 32, 3, 3, 4, 1>(a, p, q, part, s);
+  } else if (p.a_parts == 3) {
+    if (p.tile == 0) layer_one<128, 128, 2, 2, 32, 3, 1, 2, 2>(a, p, q, part, s);
+    else layer_one<128, 64, 4, 1, 32, 3, 1, 2, 2>(a, p, q, part, s);
   } else {
-    q.pairs = std::max(p.a_parts, p.b_parts);
-    for (int k = 0; k < q.pairs; ++k) {
-      if (p.a_parts == 3) q.a_sel |= static_cast<uint32_t>(2 - k) << (2 * k);
-      if (p.b_parts == 3) q.b_sel |= static_cast<uint32_t>(2 - k) << (2 * k);
-    }
+    if (p.tile == 0) layer_one<128, 128, 2, 2, 32, 1, 3, 2, 2>(a, p, q, part, s);
+    else layer_one<128, 64, 4, 1, 32, 1, 3, 2, 2>(a, p, q, part, s);
   }
-  float *part = p.splits > 1 ? reinterpret_cast<float *>(work_at(a, p.a_bytes + p.b_bytes)) : nullptr;
-  if (p.tile == 0) layer_one<256, 256, 4, 2, 2>(a, p, q, part, s);
-  else if (p.tile == 1) layer_one<128, 128, 2, 2, 2>(a, p, q, part, s);
-  else layer_one<128, 32, 4, 1, 4>(a, p, q, part, s);
 }
 
 void launch_layer_join(const LayerArgs &a, const LayerPlan &p, hipStream_t s) {
   const float *part = reinterpret_cast<const float *>(work_at(a, p.a_bytes + p.b_bytes));
-  const int64_t waves = (a.rows + 31) / 32 * ((a.features + kJoinWidth - 1) / kJoinWidth);
-  const dim3 grid(static_cast<unsigned>((waves + kWaves - 1) / kWaves));
-  if (a.shape.back) layer_join_kernel<true><<<grid, kBlock, 0, s>>>(a, part, p.splits);
-  else layer_join_kernel<false><<<grid, kBlock, 0, s>>>(a, part, p.splits);
+  const dim3 grid(static_cast<unsigned>((a.rows + 31) / 32 * ((a.features + kJoinWidth - 1) / kJoinWidth)));
+  by_kind(a, [&](auto back, auto fn) {
+    if (p.splits >= 4 && grid.x < 256) layer_join_kernel<4, decltype(back)::value, decltype(fn)::value><<<grid, kBlock * 4, 0, s>>>(a, part, p.splits);
+    else layer_join_kernel<1, decltype(back)::value, decltype(fn)::value><<<grid, kBlock, 0, s>>>(a, part, p.splits);
+  });
 }
 
 }  // namespace ob
