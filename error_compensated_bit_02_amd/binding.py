@@ -165,12 +165,31 @@ def _matrix(t: torch.Tensor, rows: int, cols: int, device, name: str):
     return t.data_ptr(), code, ld
 
 
+def _rows(t: torch.Tensor, rows: int, cols: int, device, name: str):
+    """As _matrix, the usual case in fewer calls into torch."""
+    if t.get_device() == device.index and t.shape == (rows, cols):
+        code, (ld, step) = _DTYPES.get(t.dtype), t.stride()
+        if rows == 1:
+            ld = cols
+        if code is not None and step == 1 and ld >= cols:
+            return t.data_ptr(), code, ld
+    return _matrix(t, rows, cols, device, name)
+
+
 def _stream_on(stream, device: torch.device) -> int:
     if stream is None:   # its handle alone: building a stream object costs a fifth of a small call
         return torch._C._cuda_getCurrentRawStream(device.index)
     if stream.device != device:
         raise OneBitError(f"the stream is on {stream.device}, the tensors on {device}")
     return stream.cuda_stream
+
+
+def _call(fn, device: torch.device, *args) -> int:
+    """fn(*args) with `device` current."""
+    if torch._C._cuda_getDevice() == device.index:      # tensors of a device exist, so torch has begun to use it
+        return fn(*args)
+    with _on(device):
+        return fn(*args)
 
 
 class _on:
@@ -326,6 +345,7 @@ class OneBitAdam:
         self.T = len(self.numel)
         self.W = int(workers)
         self.grad_dtype = grad_dtype
+        self._grad_type = torch.bfloat16 if grad_dtype == "bf16" else torch.float32
         self.beta1, self.eps = float(beta1), float(eps)
         self.offsets = layout(self.numel)
         self.N = self.offsets[-1]
@@ -485,56 +505,45 @@ class OneBitAdam:
     def _moments(self, state):
         """(moments code, m, m_scale, v, v_scale) of a state dict."""
         m, v = state["m"], state["v"]
-        self._on_device(m, "m")
-        self._on_device(v, "v")
-        if m.dtype == torch.float32:
+        if m.dtype is torch.float32:
             if "m_scale" in state or "v_scale" in state:
                 raise OneBitError("float32 moments have no scales")
-            f32 = (torch.float32,)
-            return OB_MOMENTS_F32, _ptr(m, f32, self.N, "m"), None, _ptr(v, f32, self.N, "v"), None
-        u8 = (torch.uint8,)
-        self._on_device(state["m_scale"], "m_scale")
-        self._on_device(state["v_scale"], "v_scale")
-        return (OB_MOMENTS_8BIT, _ptr(m, u8, self.N, "m"), _ptr(state["m_scale"], u8, self.Nw, "m_scale"),
-                _ptr(v, u8, self.N, "v"), _ptr(state["v_scale"], u8, self.Nw, "v_scale"))
+            return (OB_MOMENTS_F32, self._flat(m, torch.float32, self.N, "m"), None,
+                    self._flat(v, torch.float32, self.N, "v"), None)
+        u8 = torch.uint8
+        return (OB_MOMENTS_8BIT, self._flat(m, u8, self.N, "m"), self._flat(state["m_scale"], u8, self.Nw, "m_scale"),
+                self._flat(v, u8, self.N, "v"), self._flat(state["v_scale"], u8, self.Nw, "v_scale"))
 
     def adamw_step(self, grads, state, params, step, lr, beta2=0.999, weight_decay=0.0, decay=None, grad_scale=None,
                    model=None, seed=0, stream=None) -> None:
         """One AdamW step on the workers' average gradient (see include/ob.h).  state: adamw_state's dict;
         decay: [T] float32 factors of the weight decay; grad_scale: one float32 on the device; model: [N]
         bfloat16, the new parameters; seed: of the 8-bit moments' rounding, another one every step."""
+        f32 = torch.float32
         kind, m, ms, v, vs = self._moments(state)
-        self._on_device(grads, "grads")
-        self._on_device(params, "params")
-        f32 = (torch.float32,)
-        for t, name in ((decay, "decay"), (grad_scale, "grad_scale"), (model, "model")):
-            if t is not None:
-                self._on_device(t, name)
-        if not 0 <= int(seed) < 1 << 64:
+        seed = int(seed)
+        if not 0 <= seed < 1 << 64:
             raise OneBitError(f"seed {seed} is not a 64-bit unsigned integer", OB_ERR_INVALID)
-        with _on(self.device):
-            st = self.lib.ob_adamw_step(
-                self._ctx, kind, self._grad_ptr(grads), None if grad_scale is None else _ptr(grad_scale, f32, 1, "grad_scale"),
-                m, ms, v, vs, _ptr(params, f32, self.N, "params"),
-                None if model is None else _ptr(model, (torch.bfloat16,), self.N, "model"), int(step), float(lr),
-                float(beta2), float(weight_decay), None if decay is None else _ptr(decay, f32, self.T, "decay"),
-                int(seed), _stream_on(stream, self.device))
-        _check(st, "ob_adamw_step")
+        _check(_call(
+            self.lib.ob_adamw_step, self.device, self._ctx, kind, self._flat(grads, self._grad_type, self.W * self.N, "grads"),
+            None if grad_scale is None else self._flat(grad_scale, f32, 1, "grad_scale"), m, ms, v, vs,
+            self._flat(params, f32, self.N, "params"),
+            None if model is None else self._flat(model, torch.bfloat16, self.N, "model"), step, lr, beta2, weight_decay,
+            None if decay is None else self._flat(decay, f32, self.T, "decay"), seed, _stream_on(stream, self.device)),
+            "ob_adamw_step")
 
     def adamw_load(self, state, m, v, stream=None) -> None:
         """The values of 8-bit moments into m, v [N], both float32 (exact) or both bfloat16."""
         kind, mc, ms, vc, vs = self._moments(state)
         if kind != OB_MOMENTS_8BIT:
             raise OneBitError("float32 moments are their values")
-        self._on_device(m, "m")
-        self._on_device(v, "v")
-        if m.dtype != v.dtype:
+        if m.dtype is not v.dtype:
             raise OneBitError(f"m has dtype {m.dtype}, v {v.dtype}")
-        both = tuple(_DTYPES)
-        mp, vp = _ptr(m, both, self.N, "m"), _ptr(v, both, self.N, "v")
-        with _on(self.device):
-            st = self.lib.ob_adamw_load(self._ctx, mc, ms, vc, vs, _DTYPES[m.dtype], mp, vp, _stream_on(stream, self.device))
-        _check(st, "ob_adamw_load")
+        code = _DTYPES.get(m.dtype)
+        if code is None:
+            raise OneBitError(f"m has dtype {m.dtype}, expected one of {tuple(_DTYPES)}")
+        _check(_call(self.lib.ob_adamw_load, self.device, self._ctx, mc, ms, vc, vs, code, self._flat(m, m.dtype, self.N, "m"),
+                     self._flat(v, v.dtype, self.N, "v"), _stream_on(stream, self.device)), "ob_adamw_load")
 
     def begin_compression(self, err_w, err_s, stream=None) -> None:
         """Zero the error buffers at the switch from warmup to compression."""
@@ -545,6 +554,13 @@ class OneBitAdam:
         _check(st, "ob_begin_compression")
 
     # -- what fills a gradient row -------------------------------------------
+    def _flat(self, t: torch.Tensor, dtype: torch.dtype, numel: int, name: str) -> int:
+        """Pointer of a flat buffer on the context's device."""
+        if t.get_device() == self.device.index and t.dtype is dtype and t.numel() == numel and t.is_contiguous():
+            return t.data_ptr()
+        self._on_device(t, name)
+        return _ptr(t, (dtype,), numel, name)
+
     def _on_device(self, t: torch.Tensor, name: str) -> None:
         if _device(t, name) != self.device:
             raise OneBitError(f"{name} is on {t.device}, the context on {self.device}")
@@ -624,8 +640,10 @@ class OneBitAdam:
 
     def _list(self, weights: torch.Tensor):
         """(pointer, type code) of a list's parameters: params, or its bfloat16 copy."""
-        self._on_device(weights, "weights")
-        return _ptr(weights, tuple(_DTYPES), self.N, "weights"), _DTYPES[weights.dtype]
+        code = _DTYPES.get(weights.dtype)
+        if code is None:
+            raise OneBitError(f"weights has dtype {weights.dtype}, expected one of {tuple(_DTYPES)}")
+        return self._flat(weights, weights.dtype, self.N, "weights"), code
 
     def linear(self, weight, bias, x, weights, y, act="none", residual=None, keep=None, work=None, stream=None) -> None:
         """y = act(x W^T + b) + residual with W (tensor `weight`) and b (tensor `bias`, or None)
@@ -633,16 +651,19 @@ class OneBitAdam:
         [rows][out] that takes the pre-activation; y may be residual."""
         weight = self._tensor(weight, "weight")
         bias = -1 if bias is None else self._tensor(bias, "bias")
-        fn = ActCheckpoint._fn(act)
-        if x.dim() != 2 or x.shape[1] == 0 or self.numel[weight] % x.shape[1]:
-            raise OneBitError(f"x has shape {tuple(x.shape)}, the weight {self.numel[weight]} elements")
-        rows, cols = x.shape
-        out = self.numel[weight] // cols
+        fn = ACT_FNS.get(act)
+        if fn is None:
+            ActCheckpoint._fn(act)
+        shape, size = tuple(x.shape), self.numel[weight]
+        if len(shape) != 2 or shape[1] == 0 or size % shape[1]:
+            raise OneBitError(f"x has shape {shape}, the weight {size} elements")
+        rows, cols = shape
+        out = size // cols
         dev = self.device
-        xp, dt, ldx = _matrix(x, rows, cols, dev, "x")
-        yp, ydt, ldy = _matrix(y, rows, out, dev, "y")
+        xp, dt, ldx = _rows(x, rows, cols, dev, "x")
+        yp, ydt, ldy = _rows(y, rows, out, dev, "y")
         lp, ldt = self._list(weights)
-        rp, rdt, ldr = (None, dt, out) if residual is None else _matrix(residual, rows, out, dev, "residual")
+        rp, rdt, ldr = (None, dt, out) if residual is None else _rows(residual, rows, out, dev, "residual")
         if ydt != dt or rdt != dt:
             raise OneBitError(f"x has dtype {x.dtype}, y {y.dtype}" + ("" if residual is None else f", residual {residual.dtype}"))
         codes = scales = None
@@ -651,27 +672,30 @@ class OneBitAdam:
                 raise OneBitError(f"keep is [{keep._rows}][{keep._cols}], expected [{rows}][{out}]")
             self._on_device(keep._codes, "keep")
             codes, scales = keep._pointers()
-        work, have = _work(work, self._linear_work(rows, out, cols, dt, ldt, xp, ldx, 0), stream, dev)
-        with _on(dev):
-            st = self.lib.ob_linear(
-                self._ctx, weight, bias, rows, out, cols, dt, xp, ldx, ldt, lp, fn, 0 if keep is None else keep._format, codes,
-                scales, rp, ldr, yp, ldy, None if work is None else work.data_ptr(), have, _stream_on(stream, dev))
-        _check(st, "ob_linear")
+        need = self._linear_work(rows, out, cols, dt, ldt, xp, ldx, 0)
+        work, have = (None, 0) if need == 0 and work is None else _work(work, need, stream, dev)
+        _check(_call(
+            self.lib.ob_linear, dev, self._ctx, weight, bias, rows, out, cols, dt, xp, ldx, ldt, lp, fn,
+            0 if keep is None else keep._format, codes, scales, rp, ldr, yp, ldy,
+            None if work is None else work.data_ptr(), have, _stream_on(stream, dev)), "ob_linear")
 
     def linear_input_grad(self, weight, dy, weights, dx, act="none", kept=None, add=None, work=None, stream=None) -> None:
         """dx = (dy W) * act'(kept) + add with W (tensor `weight`) from weights as in linear; kept: the
         ActCheckpoint [rows][in] of what the activation was given, with an activation only; dx may be add."""
         weight = self._tensor(weight, "weight")
-        fn = ActCheckpoint._fn(act)
-        if dy.dim() != 2 or dy.shape[1] == 0 or self.numel[weight] % dy.shape[1]:
-            raise OneBitError(f"dy has shape {tuple(dy.shape)}, the weight {self.numel[weight]} elements")
-        rows, out = dy.shape
-        cols = self.numel[weight] // out
+        fn = ACT_FNS.get(act)
+        if fn is None:
+            ActCheckpoint._fn(act)
+        shape, size = tuple(dy.shape), self.numel[weight]
+        if len(shape) != 2 or shape[1] == 0 or size % shape[1]:
+            raise OneBitError(f"dy has shape {shape}, the weight {size} elements")
+        rows, out = shape
+        cols = size // out
         dev = self.device
-        gp, dt, lddy = _matrix(dy, rows, out, dev, "dy")
-        xp, xdt, lddx = _matrix(dx, rows, cols, dev, "dx")
+        gp, dt, lddy = _rows(dy, rows, out, dev, "dy")
+        xp, xdt, lddx = _rows(dx, rows, cols, dev, "dx")
         lp, ldt = self._list(weights)
-        ap, adt, lda = (None, dt, cols) if add is None else _matrix(add, rows, cols, dev, "add")
+        ap, adt, lda = (None, dt, cols) if add is None else _rows(add, rows, cols, dev, "add")
         if xdt != dt or adt != dt:
             raise OneBitError(f"dy has dtype {dy.dtype}, dx {dx.dtype}" + ("" if add is None else f", add {add.dtype}"))
         if (kept is None) != (fn == 0):
@@ -682,12 +706,12 @@ class OneBitAdam:
                 raise OneBitError(f"kept is [{kept._rows}][{kept._cols}], expected [{rows}][{cols}]")
             self._on_device(kept._codes, "kept")
             codes, scales = kept._pointers()
-        work, have = _work(work, self._linear_work(rows, out, cols, dt, ldt, gp, lddy, 1), stream, dev)
-        with _on(dev):
-            st = self.lib.ob_linear_input_grad(
-                self._ctx, weight, rows, out, cols, dt, gp, lddy, ldt, lp, fn, 0 if kept is None else kept._format, codes, scales,
-                ap, lda, xp, lddx, None if work is None else work.data_ptr(), have, _stream_on(stream, dev))
-        _check(st, "ob_linear_input_grad")
+        need = self._linear_work(rows, out, cols, dt, ldt, gp, lddy, 1)
+        work, have = (None, 0) if need == 0 and work is None else _work(work, need, stream, dev)
+        _check(_call(
+            self.lib.ob_linear_input_grad, dev, self._ctx, weight, rows, out, cols, dt, gp, lddy, ldt, lp, fn,
+            0 if kept is None else kept._format, codes, scales, ap, lda, xp, lddx,
+            None if work is None else work.data_ptr(), have, _stream_on(stream, dev)), "ob_linear_input_grad")
 
     def _linear_work(self, rows, out, cols, dt, ldt, pointer, ld, input_grad) -> int:
         aligned = pointer % 16 == 0 and (rows <= 1 or (ld * (4 if dt == OB_GRAD_F32 else 2) % 16 == 0 and ld <= 1 << 21))
