@@ -108,6 +108,17 @@ __device__ __forceinline__ void write_bytes(uint8_t *p, int n, u32x2 w) {
 template <int FW>
 constexpr int kSlabRow = FW + 4;
 
+// The largest of the lanes whose numbers differ in the bits from LANES on.
+template <int LANES>
+__device__ __forceinline__ uint32_t max_of_rows(uint32_t v) {
+  if constexpr (LANES <= 4) v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x124, 0xf, 0xf, true)));   // rotations
+  if constexpr (LANES <= 8) v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x128, 0xf, 0xf, true)));   // of 16 lanes
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
+}
+
 // What a wavefront's epilogue reads of 32 tokens beside the sums, as bf16 vectors
 // and codes: loaded before the sums of the block in front are worked on, for a
 // load's latency has nothing else to hide behind in a workgroup that ends.
@@ -164,18 +175,14 @@ __device__ __forceinline__ void finish(const LayerArgs &a, OB_LDS const float *s
       for (int k = 0; k < 8; ++k) top[k] = 0;
 #pragma unroll
       for (int j = 0; j < B::kRows; ++j) {
-        if (t0 + r0 + B::kStep * j < a.rows) {
-          float v[8];
-          sums(j, v);
+        float v[8];
+        sums(j, v);
+        const bool in = t0 + r0 + B::kStep * j < a.rows;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) top[k] = max(top[k], __float_as_uint(v[k] + bias[k]) & 0x7fffffffu);
-        }
+        for (int k = 0; k < 8; ++k) top[k] = max(top[k], in ? __float_as_uint(v[k] + bias[k]) & 0x7fffffffu : 0u);
       }
 #pragma unroll
-      for (int d = B::kLanes; d < 64; d <<= 1) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top[k] = max(top[k], static_cast<uint32_t>(__shfl_xor(static_cast<int>(top[k]), d)));
-      }
+      for (int k = 0; k < 8; ++k) top[k] = max_of_rows<B::kLanes>(top[k]);
       u32x2 w = {0, 0};
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -352,14 +359,16 @@ __global__ __launch_bounds__(64 * WF * WT, WGS * WF * WT / 4) void layer_kernel(
   struct Operands {                // of a step of 32
     bf16x8 a[PA][FI], b[PB][FO];
   };
-  const int row_a = 8 * g + (li >> 2), piece_a = (li & 3) * 8;       // of the transposing read: four k of a lane's feature
+  // Of the transposing read, which gives a lane four k of its feature: where it starts for the wavefront's first
+  // fragment; the others' units differ in the bits that the swizzle exchanges.
+  const int row_a = 8 * g + (li >> 2), off_a = row_a * (BF * 2) + (((wf * FI) ^ swizzle_a(row_a)) << 5) + (li & 3) * 8;
   constexpr int kReads = PA * FI + PB * FO;                          // reads of a step
   const auto read = [&](OB_LDS const unsigned char *T, int kk, int r, Operands &f) __attribute__((always_inline)) {
     const int unit = ((kk * 4 + g) ^ swizzle_k<KT>(li)) << 4;
     if (r < PA * FI) {
       const int s = r / FI, i = r % FI;
       if constexpr (BACK) {
-        OB_LDS const unsigned char *p = T + s * A_PART + (kk * 32 + row_a) * (BF * 2) + (((wf * FI + i) ^ swizzle_a(row_a)) << 5) + piece_a;
+        OB_LDS const unsigned char *p = T + (off_a ^ (i << 5)) + s * A_PART + kk * 32 * (BF * 2);
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p));
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((OB_LDS s16x4 *)(p + 4 * BF * 2));
         f.a[s][i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
