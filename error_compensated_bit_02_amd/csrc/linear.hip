@@ -35,7 +35,7 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 // What multiplies: matrices of bf16 parts whose rows start on 16 bytes.
 struct Product {
   int64_t rows, features, depth;     // of C, and the contraction's length: a multiple of 8, past its true end B is zero
-  int64_t a_rows;                    // backward: A's rows, the true length
+  int64_t true_depth;
   const uint16_t *a, *b;
   int64_t lda, ldb, a_part, b_part;  // row strides and distances of the parts, in elements
 };
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(64 * WF * WT, WGS * WF * WT / 4) void layer_kernel(
   const Where at = where(sp);
   const int64_t f0 = static_cast<int64_t>(at.mt) * BF, t0 = static_cast<int64_t>(at.nt) * BT;
   const int64_t first = at.split * sp.turns_each;
-  const int turns = static_cast<int>(min(sp.turns_each, (q.depth + KT - 1) / KT - first));
+  const int turns = static_cast<int>(min(sp.turns_each, (q.true_depth + KT - 1) / KT - first));
 
   f32x4 acc[FI][FO];
 #pragma unroll
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(64 * WF * WT, WGS * WF * WT / 4) void layer_kernel(
   const int64_t k0 = first * KT;
   const char *at_a = reinterpret_cast<const char *>(q.a + (BACK ? k0 * q.lda + f0 : f0 * q.lda + k0));
   const char *at_b = reinterpret_cast<const char *>(q.b + t0 * q.ldb + k0);
-  int left = turns, depth = static_cast<int>(q.depth - k0), a_rows = static_cast<int>(q.a_rows - k0);
+  int left = turns, depth = static_cast<int>(q.depth - k0), a_rows = static_cast<int>(q.true_depth - k0);
   // The copies of a turn: their buffers and offsets, then the copies one by one.
   // Units past the contraction's end are read as past the buffer's.
   struct Turn {
@@ -1022,7 +1022,7 @@ void launch_layer(const LayerArgs &a, const LayerPlan &p, hipStream_t s) {
   q.rows = a.rows;
   q.features = a.features;
   q.depth = depth % 8 == 0 ? depth : up64(depth);      // then B is packed, and A too if it lies along k
-  q.a_rows = depth;
+  q.true_depth = depth;
   q.a = static_cast<const uint16_t *>(p.pack_a ? a.work : a.weight);
   q.lda = p.pack_a ? up64(a.shape.in) : a.shape.in;
   q.a_part = a.shape.out * q.lda;

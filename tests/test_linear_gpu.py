@@ -76,7 +76,9 @@ def _round(x, dtype):
 SHAPES = [  # rows, out, in, x's extra columns and offset in elements
     (1, 1, 1, 0, 0), (1, 5, 8, 0, 0), (1, 129, 64, 0, 0), (2, 64, 65, 1, 1), (7, 40, 72, 8, 8), (16, 300, 136, 0, 0),
     (31, 33, 31, 0, 4), (33, 256, 200, 24, 0), (64, 72, 1000, 0, 0), (129, 130, 264, 7, 0), (300, 257, 96, 0, 0),
-    (513, 520, 328, 16, 8), (1, 4096, 1024, 0, 0), (5, 1000, 4104, 0, 0)]
+    (513, 520, 328, 16, 8), (1, 4096, 1024, 0, 0), (5, 1000, 4104, 0, 0),
+    # contractions whose last 64 steps hold 6: several slices, the last of them shorter
+    (40, 4102, 64, 0, 0), (40, 64, 4102, 0, 0), (200, 4102, 72, 0, 0)]
 
 
 @pytest.mark.parametrize("rows,out,inp,extra,offset", SHAPES)
