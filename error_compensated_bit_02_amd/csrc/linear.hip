@@ -10,12 +10,20 @@
 // the forward and along f in the backward.  The weight is the instruction's first
 // operand, so a lane's four results are four consecutive f of one token.
 //
-// fp32 operands are cut into three bf16 parts each (pack_units), rounded to
-// nearest, so that each part is at most 2^-8 of the one before and they add up to
-// the value exactly (but for bits below bf16's last, 2^-133).  Of two fp32 operands
-// the products of parts whose order sums to at most 2 are taken, six of nine; the
-// others are below 2^-25 of the product.  With one bf16 operand all three are taken
-// and products are exact.
+// fp32 operands are cut into three bf16 parts each (pack_kernel, or on their way into
+// LDS), rounded to nearest, so that each part is at most 2^-8 of the one before and
+// they add up to the value exactly (but for bits below bf16's last, 2^-133).  Of two
+// fp32 operands the products of parts whose order sums to at most 2 are taken, six of
+// nine; the others are below 2^-25 of the product.  With one bf16 operand all three
+// are taken and products are exact.
+//
+// What bounds it, measured on one card.  Large bf16 products: the matrix units at the
+// clock that the card holds under them (about 1.8 GHz), 418 us for 16384 tokens of 2048 ->
+// 8192 (1315 TFLOP/s; the library's product alone 375-391), 400 us for the gradient to
+// the input of 8192 -> 2048 (1370; the library 435); of the 418, 55 are the copies beside
+// the products.  fp32 at 4096^3: 640 us and 54 for the parts, 1290 TFLOP/s in six products.
+// Few tokens: reading the weight (8192 x 8192 bf16 for one token 20.6 us, 6.5 TB/s).
+// Between them, launches and the start and end of workgroups that have a CU to themselves.
 #include "internal.h"
 #include "activation.h"
 #include "act_math.h"
@@ -32,11 +40,12 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
-// What multiplies: matrices of bf16 parts whose rows start on 16 bytes.
+// What multiplies: bf16 matrices whose rows start on 16 bytes, or bf16 parts of fp32
+// ones (pack_kernel), or fp32 matrices as they lie, cut on their way into LDS.
 struct Product {
   int64_t rows, features, depth;     // of C, and the contraction's length: a multiple of 8, past its true end B is zero
   int64_t true_depth;
-  const uint16_t *a, *b;
+  const void *a, *b;
   int64_t lda, ldb, a_part, b_part;  // row strides and distances of the parts, in elements
 };
 
@@ -296,16 +305,27 @@ constexpr int kPartA[] = {2, 0, 1, 1, 0, 0}, kPartB[] = {0, 2, 1, 0, 1, 0};
 // products.  A turn's barrier stands where its last operands have been read: behind
 // it the next turn's tile is in LDS and nobody reads the present one any more, so the
 // copies of the turn STAGES ahead go into its place.
-// Parts: all products of a step run
-// on the same reads, so a part is loaded once a tile and not once a product (fp32
-// 777 x 2048 -> 1000: 27 us for the products one after the other).
-template <int BF, int BT, int WF, int WT, int KT, int PA, int PB, int STAGES, int WGS, bool BACK, int FN>
+// Parts: all products of a step run on the same reads, so a part is loaded once a tile
+// and not once a product.
+// RAW: parts are cut from fp32 on the way into LDS instead of being read from a copy.
+//
+// Tiles.  256 x 256 on eight wavefronts of 64 x 128, two stages of 64: a byte of LDS is
+// read for the fewest products, and the 128 sums a lane leave room for two steps'
+// operands.  At 16384 x 2048 -> 8192, 418 us: 128 x 128 tiles 532, four wavefronts of
+// 128 x 128 552, 128 x 256 on half a CU 530-540, five stages of 32 550, 32 x 32 x 16
+// products 480-495, 256 lasting workgroups 505.  Copies in the first half of a step's
+// products 418, over all of them 460, in a burst 451; no fences 460.
+template <int BF, int BT, int WF, int WT, int KT, int PA, int PB, bool RAW, int STAGES, int WGS, bool BACK, int FN>
 __global__ __launch_bounds__(64 * WF * WT, WGS * WF * WT / 4) void layer_kernel(const LayerArgs a, const Product q, const Split sp, float *part) {
   constexpr int NW = WF * WT, FI = BF / WF / 16, FO = BT / WT / 16, FW = FI * 16;      // fragments of a wavefront
   constexpr int UNITS = KT / 8, ROWS = 64 / UNITS;       // units of a row, rows of one copy
   constexpr int A_PART = BF * KT * 2, B_PART = BT * KT * 2, A_BYTES = PA * A_PART, STAGE = A_BYTES + PB * B_PART;
   constexpr int JA = A_PART / 1024 / NW, JB = B_PART / 1024 / NW, RA = 512 / BF;
+  // RAW: fp32 operands pass through registers, UA and UB units of eight elements a lane
+  constexpr bool RAW_A = RAW && PA == 3, RAW_B = RAW && PB == 3;
+  constexpr int NT = 64 * NW, UA = RAW_A ? BF * KT / 8 / NT : 0, UB = RAW_B ? BT * KT / 8 / NT : 0, U = UA + UB;
   static_assert(JA * NW * 1024 == A_PART && JB * NW * 1024 == B_PART && FO % 2 == 0, "tile shape");
+  static_assert(U == 0 || (KT == 32 && STAGES == 2), "a unit is cut a turn ahead of its products");
   static_assert(!BACK || BF >= 128, "the transposing read's swizzle spans eight units");
   static_assert(NW * 32 * kSlabRow<FW> * 4 <= STAGES * STAGE, "the epilogue's sums fit the stages");
   static_assert(WGS * STAGES * STAGE <= 160 * 1024, "LDS of a CU");
@@ -346,9 +366,10 @@ __global__ __launch_bounds__(64 * WF * WT, WGS * WF * WT / 4) void layer_kernel(
   // The next turn to be copied: where it reads, how much of the contraction is left,
   // and how many turns.
   const int64_t k0 = first * KT;
-  const char *at_a = reinterpret_cast<const char *>(q.a + (BACK ? k0 * q.lda + f0 : f0 * q.lda + k0));
-  const char *at_b = reinterpret_cast<const char *>(q.b + t0 * q.ldb + k0);
+  const char *at_a = static_cast<const char *>(q.a) + (BACK ? k0 * q.lda + f0 : f0 * q.lda + k0) * 2;
+  const char *at_b = static_cast<const char *>(q.b) + (t0 * q.ldb + k0) * 2;
   int left = turns, depth = static_cast<int>(q.depth - k0), a_rows = static_cast<int>(q.true_depth - k0);
+
   // The copies of a turn: their buffers and offsets, then the copies one by one.
   // Units past the contraction's end are read as past the buffer's.
   struct Turn {
@@ -358,27 +379,104 @@ __global__ __launch_bounds__(64 * WF * WT, WGS * WF * WT / 4) void layer_kernel(
   const auto aim = [&](Turn &n) __attribute__((always_inline)) {
     const int any = -left >> 31;     // all ones or zeros by whether there is a turn
     const int steps = min(depth, KT), rows = min(a_rows, KT);
-    const int size_a = (BACK ? (rows - 1) * lda + static_cast<int>(q.features - f0) : (features - 1) * lda + steps) * 2;
-    const int size_b = ((tokens - 1) * ldb + steps) * 2;
-#pragma unroll
-    for (int s = 0; s < PA; ++s) n.a[s] = buffer(at_a + s * q.a_part * 2, size_a & any);
-#pragma unroll
-    for (int s = 0; s < PB; ++s) n.b[s] = buffer(at_b + s * q.b_part * 2, size_b & any);
     const auto inside = [&](int copy, int from) __attribute__((always_inline)) { return unit_of(copy) * 8 < steps ? from : 0x7ffffff0; };
+    if constexpr (!RAW_A) {
+      const int size = (BACK ? (rows - 1) * lda + static_cast<int>(q.features - f0) : (features - 1) * lda + steps) * 2;
 #pragma unroll
-    for (int j = 0; j < JA; ++j) n.from_a[j] = BACK ? from_a[j] : inside(wave * JA + j, from_a[j]);
+      for (int s = 0; s < PA; ++s) n.a[s] = buffer(at_a + s * q.a_part * 2, size & any);
 #pragma unroll
-    for (int j = 0; j < JB; ++j) n.from_b[j] = inside(wave * JB + j, from_b[j]);
+      for (int j = 0; j < JA; ++j) n.from_a[j] = BACK ? from_a[j] : inside(wave * JA + j, from_a[j]);
+    }
+    if constexpr (!RAW_B) {
+      const int size = ((tokens - 1) * ldb + steps) * 2;
+#pragma unroll
+      for (int s = 0; s < PB; ++s) n.b[s] = buffer(at_b + s * q.b_part * 2, size & any);
+#pragma unroll
+      for (int j = 0; j < JB; ++j) n.from_b[j] = inside(wave * JB + j, from_b[j]);
+    }
     --left;
     depth -= KT;
     a_rows -= KT;
     at_a += BACK ? static_cast<int64_t>(lda) * (KT * 2) : KT * 2;
     at_b += KT * 2;
   };
-  constexpr int kLoads = PA * JA + PB * JB;
+  constexpr int kCopiesA = RAW_A ? 0 : PA * JA, kLoads = kCopiesA + (RAW_B ? 0 : PB * JB);
   const auto copy = [&](const Turn &n, int c, OB_LDS unsigned char *dst) __attribute__((always_inline)) {
-    if (c < PA * JA) copy16(n.a[c / JA], dst + c / JA * A_PART + (wave * JA + c % JA) * 1024, n.from_a[c % JA]);
-    else copy16(n.b[(c - PA * JA) / JB], dst + A_BYTES + (c - PA * JA) / JB * B_PART + (wave * JB + (c - PA * JA) % JB) * 1024, n.from_b[(c - PA * JA) % JB]);
+    if (c < kCopiesA) {
+      copy16(n.a[c / JA], dst + c / JA * A_PART + (wave * JA + c % JA) * 1024, n.from_a[c % JA]);
+    } else {
+      const int d = c - kCopiesA;
+      copy16(n.b[d / JB], dst + A_BYTES + d / JB * B_PART + (wave * JB + d % JB) * 1024, n.from_b[d % JB]);
+    }
+  };
+
+  // RAW: fp32 operands.  Rows past the end are read as the last one (their results are
+  // dropped); of a row that ends within a unit the rest is 0, and so are the weight's
+  // rows past the contraction's end.  raw_k: the first k of the turn to be read.
+  float raw[U > 0 ? U : 1][8];
+  int64_t raw_k = k0;
+  int raw_left = turns;
+  const auto fill = [&](int u) __attribute__((always_inline)) {
+    const bool is_a = u < UA, along_f = BACK && is_a;
+    const int id = static_cast<int>(threadIdx.x) + (is_a ? u : u - UA) * NT;
+    const float *p;
+    int64_t n;
+    if (along_f) {
+      const int64_t k = raw_k + id / (BF / 8), f = f0 + id % (BF / 8) * 8;
+      p = static_cast<const float *>(q.a) + min(k, q.true_depth - 1) * q.lda + f;
+      n = k < q.true_depth ? q.features - f : 0;
+    } else {
+      const int64_t k = raw_k + id % 4 * 8, r = id / 4;
+      if (is_a) p = static_cast<const float *>(q.a) + min(f0 + r, q.features - 1) * q.lda + k;
+      else p = static_cast<const float *>(q.b) + min(t0 + r, q.rows - 1) * q.ldb + k;
+      n = q.true_depth - k;
+    }
+    if (n >= 8) {
+      __builtin_memcpy(raw[u], p, sizeof(raw[u]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) raw[u][k] = k < n ? p[k] : 0.0f;
+    }
+  };
+  // Two elements as three parts each, every part the rest rounded to nearest: the first
+  // is held to the finite range, so a value past bf16's largest is its and its rest.
+  const auto cut = [&](float x, float y, uint32_t (&w)[3]) __attribute__((always_inline)) {
+    constexpr float kMost = 3.3895313892515355e38f;
+    float px = __builtin_amdgcn_fmed3f(x, -kMost, kMost), py = __builtin_amdgcn_fmed3f(y, -kMost, kMost);
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      w[s] = pack_bf16(px, py);
+      x = x - __uint_as_float(w[s] << 16);
+      y = y - __uint_as_float(w[s] & 0xffff0000u);
+      px = x;
+      py = y;
+    }
+  };
+  uint32_t parts[3][4];              // of the unit that is being cut
+  const auto cut_pair = [&](int u, int pair) __attribute__((always_inline)) {
+    uint32_t w[3];
+    cut(raw[u][2 * pair], raw[u][2 * pair + 1], w);
+#pragma unroll
+    for (int s = 0; s < 3; ++s) parts[s][pair] = w[s];
+  };
+  const auto settle = [&](int u, OB_LDS unsigned char *dst) __attribute__((always_inline)) {
+    const bool is_a = u < UA;
+    const int id = static_cast<int>(threadIdx.x) + (is_a ? u : u - UA) * NT;
+    int at_lds;
+    if (BACK && is_a) {
+      const int k = id / (BF / 8), c = id % (BF / 8);
+      at_lds = k * (BF * 2) + (((c >> 1) ^ swizzle_a(k)) << 5) + (c & 1) * 16;
+    } else {
+      const int r = id / 4;
+      at_lds = (is_a ? 0 : A_BYTES) + r * 64 + (((id % 4) ^ swizzle_k<32>(r)) << 4);
+    }
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+      *(OB_LDS u32x4 *)(dst + at_lds + s * (is_a ? A_PART : B_PART)) = u32x4{parts[s][0], parts[s][1], parts[s][2], parts[s][3]};
+  };
+  const auto next_raw = [&]() __attribute__((always_inline)) {
+    raw_k += KT;
+    --raw_left;
   };
 
   struct Operands {                // of a step of 32
@@ -422,12 +520,24 @@ __global__ __launch_bounds__(64 * WF * WT, WGS * WF * WT / 4) void layer_kernel(
       if constexpr (decltype(copies)::value) {
         constexpr int c0 = m < kSpan ? m * kLoads / kSpan : kLoads, c1 = m < kSpan ? (m + 1) * kLoads / kSpan : kLoads;
         each<c1 - c0>([&](auto c) __attribute__((always_inline)) { copy(n, c0 + c, dst); });
+        // what is in registers is cut into the stage, four pairs a unit, by three quarters of the products, then read anew
+        constexpr int kCut = kMul * 3 / 4, p0 = m < kCut ? m * 4 * U / kCut : 4 * U, p1 = m < kCut ? (m + 1) * 4 * U / kCut : 4 * U;
+        each<p1 - p0>([&](auto pair) __attribute__((always_inline)) {
+          constexpr int at_pair = p0 + pair;
+          cut_pair(at_pair / 4, at_pair % 4);
+          if constexpr (at_pair % 4 == 3) settle(at_pair / 4, dst);
+        });
+        if constexpr (U > 0 && m == kCut) {
+          if (raw_left > 0) each<U>([&](auto u) __attribute__((always_inline)) { fill(u); });
+          next_raw();
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     });
   };
   const auto arrived = [&]() __attribute__((always_inline)) {
-    wait_loads<(STAGES - 2) * kLoads>();
+    if constexpr (kLoads > 0) wait_loads<(STAGES - 2) * kLoads>();
+    else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
@@ -457,8 +567,23 @@ __global__ __launch_bounds__(64 * WF * WT, WGS * WF * WT / 4) void layer_kernel(
     aim(n);
 #pragma unroll
     for (int c = 0; c < kLoads; ++c) copy(n, c, lds + s * STAGE);
+    if constexpr (U > 0) {
+      if (raw_left > 0) {
+        each<U>([&](auto u) __attribute__((always_inline)) { fill(u); });
+        each<U>([&](auto u) __attribute__((always_inline)) {
+          each<4>([&](auto pair) __attribute__((always_inline)) { cut_pair(u, pair); });
+          settle(u, lds + s * STAGE);
+        });
+      }
+      next_raw();
+    }
   }
-  wait_loads<(STAGES - 1) * kLoads>();
+  if constexpr (U > 0) {
+    if (raw_left > 0) each<U>([&](auto u) __attribute__((always_inline)) { fill(u); });
+    next_raw();
+  }
+  if constexpr (U > 0) wait_loads<0>();
+  else wait_loads<(STAGES - 1) * kLoads>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   {
@@ -519,48 +644,41 @@ __global__ __launch_bounds__(64 * WF * WT, WGS * WF * WT / 4) void layer_kernel(
   }
 }
 
-// The slices' sums and the epilogue: a workgroup takes 32 tokens of 32 features, in
-// GROUPS groups of 256 work-items that add up every GROUPS-th slice (few tokens in
-// many slices would otherwise wait for one load after the other: 32 tokens of 1024
-// features in 32 slices took 20 us with a wavefront a block).
+// The slices' sums and the epilogue: a workgroup adds up 32 tokens of 32 features, four
+// features a work-item, and its first wavefront finishes them.  Small blocks, as few
+// tokens in many slices wait for one load after the other: 6-8 us where a wavefront
+// with a block of its own took 20 (32 tokens of 1024 features in 32 slices).
 constexpr int kJoinWidth = 32;
-template <int GROUPS, bool BACK, int FN>
-__global__ __launch_bounds__(kBlock * GROUPS) void layer_join_kernel(const LayerArgs a, const float *part, int splits) {
-  constexpr int SLAB = 32 * kSlabRow<kJoinWidth>;
-  __shared__ __attribute__((aligned(16))) float shared[GROUPS * SLAB];
-  OB_LDS float *slabs = (OB_LDS float *)shared;
+template <bool BACK, int FN>
+__global__ __launch_bounds__(kBlock) void layer_join_kernel(const LayerArgs a, const float *part, int splits) {
+  __shared__ __attribute__((aligned(16))) float shared[32 * kSlabRow<kJoinWidth>];
+  OB_LDS float *slab = (OB_LDS float *)shared;
   const uint32_t across = static_cast<uint32_t>((a.features + kJoinWidth - 1) / kJoinWidth);
   const uint32_t band = blockIdx.x / across;
   const int64_t t0 = static_cast<int64_t>(band) * 32, f0 = static_cast<int64_t>(blockIdx.x - band * across) * kJoinWidth;
   const int64_t ldp = (a.features + 3) / 4 * 4, each = a.rows * ldp;
-  const int group = threadIdx.x / kBlock, id = threadIdx.x % kBlock, r = id / 8, c = id % 8 * 4;
+  const int r = threadIdx.x / 8, c = threadIdx.x % 8 * 4;
   Beside<kJoinWidth> beside;
   if (threadIdx.x < 64) load_beside<kJoinWidth, BACK, FN>(a, t0, f0, beside);
   f32x4 v = {0, 0, 0, 0};
   if (t0 + r < a.rows && f0 + c < a.features) {
     const float *p = part + (t0 + r) * ldp + f0 + c;
 #pragma unroll 4
-    for (int s = group; s < splits; s += GROUPS) v += *reinterpret_cast<const f32x4 *>(p + s * each);
+    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * each);
   }
-  OB_LDS f32x4 *mine = (OB_LDS f32x4 *)(slabs + group * SLAB + r * kSlabRow<kJoinWidth> + c);
-  *mine = v;
+  *(OB_LDS f32x4 *)(slab + r * kSlabRow<kJoinWidth> + c) = v;
   __syncthreads();
-  if constexpr (GROUPS > 1) {
-    if (group == 0) {
-#pragma unroll
-      for (int s = 1; s < GROUPS; ++s) v += *(OB_LDS f32x4 *)(slabs + s * SLAB + r * kSlabRow<kJoinWidth> + c);
-      *mine = v;
-    }
-    __syncthreads();
-  }
-  if (threadIdx.x < 64) finish<kJoinWidth, BACK, FN>(a, slabs, t0, f0, beside);
+  if (threadIdx.x < 64) finish<kJoinWidth, BACK, FN>(a, slab, t0, f0, beside);
 }
 
 // ---------------------------------------------------------------------------
 // a few tokens: bound by reading the weight
 // ---------------------------------------------------------------------------
 // Up to kFewTokens tokens are multiplied on the vector units in fp32, straight from
-// the weight as it lies in the list, whatever its type or alignment.
+// the weight as it lies in the list, whatever its type or alignment: no copies of
+// parts, no tile that is mostly padding, and in the forward no join.  One token of
+// 1024 -> 4096 in bf16 7.5 us a call (the kernel 3.5), 13 through a tile of the matrix
+// units; where these win, few_by_vectors says.
 constexpr int kFewTokens = 8;
 constexpr int kFewRows = 4;           // forward: features of a wavefront
 constexpr int kFewLanes = 4;          // backward: lanes, of eight features each, of a workgroup
@@ -672,7 +790,8 @@ __device__ __forceinline__ void finish_few(const LayerArgs &a, int64_t f, float 
 
 // Forward: a wavefront multiplies kFewRows rows of the weight with all tokens, 512
 // steps of the contraction at a time.  SLICED: the four wavefronts of a workgroup
-// share the rows and divide the contraction; otherwise each has rows of its own.
+// share the rows and divide the contraction; otherwise each has rows of its own, which
+// launch_layer takes where the contraction gives not every wavefront work.
 template <int R, typename TW, typename TX, bool SLICED>
 __global__ __launch_bounds__(kBlock) void layer_few_kernel(const LayerArgs a) {
   constexpr int FEATURES = SLICED ? kFewRows : kFewRows * kWaves;      // of a workgroup
@@ -887,14 +1006,32 @@ __global__ __launch_bounds__(kBlock) void pack_kernel(const PackArgs a, const Pa
 // plans
 // ---------------------------------------------------------------------------
 // Tiles that are built, and their times in microseconds: of a workgroup's start and
-// end, of a turn on a CU of its own and with as many workgroups as a CU holds.
+// end, of a turn on a CU of its own and with as many workgroups as a CU holds.  The
+// plan is the tile and the number of slices with the least time by them.  Forward /
+// gradient in us with each tile's best slices, the taken one marked:
+//   bf16               256 x 256    128 x 128      128 x 32
+//   1024^3             30 / 31      11.6 / 11.7    8.7 / 8.6 *
+//   4096 x 2048^2      44 / 44      36 / 36 *      62 / 61
+//   4096^3             100 / 100 *  129 / 130      226 / 232
+//   16384 2048->8192   422 / 402 *  532 / 508      918 / 965
+//   fp32               128 x 128    128 x 64       128 x 64, cut on the way
+//   777 2048->1000     37* / 35     41 / 34 *      45 / 43
+//   256 x 2048^2       33 / 32      32 / 32        28 / 30 *
+//   4096^3             703 / 668 *  860 / 770      850 / 884
+//   bf16 and fp32 weights
+//   64 x 4096^2        62 / 49      60 / 49        26 / 27 *
+//   777 2048->1000     29* / 35     32 / 32 *      42 / 33
+//   2048^3             64 / 58 *    78 / 58        77 / 84
+// Cutting on the way saves the parts' copy, whose cost the weight's size settles, and
+// cuts an operand again in every tile that reads it: it wins where few tiles share it.
 struct Tiles {
   int features, tokens, depth, per_cu;
+  bool raw;                          // fp32 as it lies
   double start, alone, full;
 };
-constexpr Tiles kPlainTiles[] = {{256, 256, 64, 1, 9.0, 1.40, 1.40}, {128, 128, 64, 2, 4.5, 0.60, 1.0}, {128, 32, 64, 2, 4.0, 0.40, 0.55}};
-constexpr Tiles kPartTiles[] = {{128, 128, 32, 1, 5.0, 1.25, 1.25}, {128, 64, 32, 1, 4.0, 0.62, 0.62}};      // six products
-constexpr Tiles kThreeTiles[] = {{128, 128, 32, 2, 5.0, 0.50, 0.85}, {128, 64, 32, 2, 4.0, 0.40, 0.60}};      // three
+constexpr Tiles kPlainTiles[] = {{256, 256, 64, 1, false, 9.0, 1.40, 1.40}, {128, 128, 64, 2, false, 4.5, 0.60, 1.0}, {128, 32, 64, 2, false, 4.0, 0.40, 0.55}};
+constexpr Tiles kSixTiles[] = {{128, 128, 32, 1, false, 5.0, 1.20, 1.25}, {128, 64, 32, 1, false, 4.0, 0.70, 0.78}, {128, 64, 32, 1, true, 4.0, 1.20, 1.20}};
+constexpr Tiles kThreeTiles[] = {{128, 128, 32, 2, false, 5.0, 0.50, 0.85}, {128, 64, 32, 2, false, 4.0, 0.40, 0.60}, {128, 64, 32, 1, true, 4.0, 0.70, 0.70}};
 
 int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -914,12 +1051,12 @@ void by_kind(const LayerArgs &a, F &&f) {
   else by_fn(std::false_type{});
 }
 
-template <int BF, int BT, int WF, int WT, int KT, int PA, int PB, int STAGES, int WGS>
+template <int BF, int BT, int WF, int WT, int KT, int PA, int PB, bool RAW, int STAGES, int WGS>
 void layer_one(const LayerArgs &a, const LayerPlan &p, const Product &q, float *part, hipStream_t s) {
   const Split sp{p.m_tiles, p.n_tiles, p.splits, p.turns_each};
   const dim3 grid(static_cast<unsigned>(p.m_tiles) * p.n_tiles * p.splits);
   by_kind(a, [&](auto back, auto fn) {
-    layer_kernel<BF, BT, WF, WT, KT, PA, PB, STAGES, WGS, decltype(back)::value, decltype(fn)::value>
+    layer_kernel<BF, BT, WF, WT, KT, PA, PB, RAW, STAGES, WGS, decltype(back)::value, decltype(fn)::value>
         <<<grid, 64 * WF * WT, 0, s>>>(a, q, sp, part);
   });
 }
@@ -927,8 +1064,12 @@ void layer_one(const LayerArgs &a, const LayerPlan &p, const Product &q, float *
 template <int R, typename TW, typename TX>
 void layer_few(const LayerArgs &a, int slices, float *part, hipStream_t s) {
   const auto groups = [&](int64_t each) { return static_cast<unsigned>((a.features + each - 1) / each); };
+  // Wavefronts that share their rows, but where four times 512 steps are more than there are:
+  // 8 tokens of 1024 -> 8192 in bf16 15.4 us so and 7.5 the other way, of 2048 -> 8192 17.9
+  // and 9.6; of 8192 -> 2048 10.5 and 19.1, one token of 8192 -> 8192 20.6 and 28.7.
+  const bool own = R > 1 && a.shape.in <= 512 * kWaves && a.features >= 4096;
   if (a.shape.back) layer_few_back_kernel<R, TW, TX><<<dim3(groups(kFewLanes * 8), slices), kFewBlock, 0, s>>>(a, part);
-  else if (a.features >= 4096) layer_few_kernel<R, TW, TX, false><<<groups(kFewRows * kWaves), kBlock, 0, s>>>(a);
+  else if (own) layer_few_kernel<R, TW, TX, false><<<groups(kFewRows * kWaves), kBlock, 0, s>>>(a);
   else layer_few_kernel<R, TW, TX, true><<<groups(kFewRows), kBlock, 0, s>>>(a);
 }
 
@@ -939,43 +1080,61 @@ void layer_few_by_rows(const LayerArgs &a, int slices, float *part, hipStream_t 
   else layer_few<8, TW, TX>(a, slices, part, s);
 }
 
+// Whether few tokens go through the vector units.  Their time grows with the tokens, the
+// matrix units' hardly does.  Forward / gradient in us, vector units against matrix units:
+//   bf16  1 token    4096 x 4096  8 / 12.5 : 13 / 13    8192 x 8192  21 / 30 : 25 / 27
+//         4 tokens   4096 x 4096  8 / 14 : 13 / 13      8192 x 8192  22 / 42 : 25 / 27
+//         8 tokens   2048 x 2048  8 / 13.5 : 13 / 13    4096 x 4096  12.5 / 27 : 13 / 13
+//                    8192 x 8192  35 / 89 : 25 / 27
+//   fp32  1 token    8192 x 8192  42 / 43 : 89 / 84
+//         8 tokens   4096 x 4096  18 / 29 : 29 / 28     8192 x 8192  55 / 92 : 92 / 85
+// A bf16 weight that the matrix units cannot read as it lies would be copied first.
+bool few_by_vectors(const LayerShape &s) {
+  if (s.rows > kFewTokens) return false;
+  const int64_t work = s.rows * s.out * s.in;
+  if (s.weight_f32) return !s.back || work <= int64_t{1} << 28;
+  return s.in % 8 != 0 || work <= int64_t{1} << (s.back ? 25 : 28);
+}
+
 char *work_at(const LayerArgs &a, size_t bytes) { return static_cast<char *>(a.work) + bytes; }
 
 }  // namespace
 
 bool layer_fits(int64_t rows, int64_t out, int64_t in) {
-  // a tile's 256 rows (or 64 of the weight) lie within 2 GB; the large tiles fit the grid
+  // a tile's 256 rows (or 64 of the weight) lie within 2 GB; tiles of 128 x 128 fit the grid
   constexpr int64_t kMost = int64_t{1} << 21;
   return rows >= 0 && rows <= (int64_t{1} << 24) && out >= 1 && out <= kMost && in >= 1 && in <= kMost &&
-         ((rows + 255) / 256) * ((std::max(out, in) + 255) / 256) <= kMaxGrid / 2;
+         ((rows + 127) / 128) * ((std::max(out, in) + 127) / 128) <= kMaxGrid / 2;
 }
 
 LayerPlan layer_plan(const LayerShape &s) {
   LayerPlan p{};
   const int64_t features = features_of(s), depth = depth_of(s);
   p.splits = 1;
-  if (s.rows <= kFewTokens) {
+  if (few_by_vectors(s)) {
     p.tile = -1;
     if (s.back) p.splits = static_cast<int>((depth + kFewChunk - 1) / kFewChunk);
   } else {
     p.a_parts = s.weight_f32 ? 3 : 1;
     p.b_parts = s.f32 ? 3 : 1;
-    p.pack_a = s.weight_f32 || s.in % 8 != 0;
-    p.pack_b = s.f32 || depth % 8 != 0 || !s.aligned;
-    if (p.pack_a) p.a_bytes = up256(static_cast<size_t>(p.a_parts) * s.out * up64(s.in) * 2);
-    if (p.pack_b) p.b_bytes = up256(static_cast<size_t>(p.b_parts) * s.rows * up64(depth) * 2);
+    const bool raw_rows_a = !s.weight_f32 && s.in % 8 != 0, raw_rows_b = !s.f32 && (depth % 8 != 0 || !s.aligned);
+    const size_t a_bytes = up256(static_cast<size_t>(p.a_parts) * s.out * up64(s.in) * 2);
+    const size_t b_bytes = up256(static_cast<size_t>(p.b_parts) * s.rows * up64(depth) * 2);
     const int products = p.a_parts * p.b_parts;
-    const Tiles *tiles = products == 1 ? kPlainTiles : products == 9 ? kPartTiles : kThreeTiles;
+    const Tiles *tiles = products == 1 ? kPlainTiles : products == 9 ? kSixTiles : kThreeTiles;
     const double part = static_cast<double>(s.rows) * features * 4 / 3e6;
     double best = 0.0;
     p.tile = -1;
-    for (int k = 0; k < (products == 1 ? 3 : 2); ++k) {
+    for (int k = 0; k < 3; ++k) {
       const int64_t m = (features + tiles[k].features - 1) / tiles[k].features, n = (s.rows + tiles[k].tokens - 1) / tiles[k].tokens;
       const int64_t turns = (depth + tiles[k].depth - 1) / tiles[k].depth, most = m * n >= 512 ? 1 : std::min<int64_t>(turns, 64);      // no slices where the tiles fill the card
+      // packing: its launch, and ten bytes read and written an fp32 element (four a bf16 one)
+      const bool pack_a = raw_rows_a || (s.weight_f32 && !tiles[k].raw), pack_b = raw_rows_b || (s.f32 && !tiles[k].raw);
+      const double packing = (pack_a || pack_b ? 4.0 : 0.0) + (pack_a ? a_bytes / 3.5e6 : 0.0) + (pack_b ? b_bytes / 3.5e6 : 0.0);
       for (int64_t want = 1; want <= most; ++want) {
         const int64_t each = (turns + want - 1) / want, splits = (turns + each - 1) / each, groups = m * n * splits;
         if (splits != want || groups > kMaxGrid / 2) continue;
-        double t = tiles[k].start + (splits > 1 ? 4.0 + splits * part : 0.0);
+        double t = packing + tiles[k].start + (splits > 1 ? 4.0 + splits * part : 0.0);
         const int64_t held = 256 * tiles[k].per_cu;
         if (groups <= 256) t += each * tiles[k].alone;
         else t += static_cast<double>((groups + held - 1) / held) * each * tiles[k].full;
@@ -986,9 +1145,13 @@ LayerPlan layer_plan(const LayerShape &s) {
           p.n_tiles = static_cast<int>(n);
           p.splits = static_cast<int>(splits);
           p.turns_each = each;
+          p.pack_a = pack_a;
+          p.pack_b = pack_b;
         }
       }
     }
+    p.a_bytes = p.pack_a ? a_bytes : 0;
+    p.b_bytes = p.pack_b ? b_bytes : 0;
   }
   p.part_bytes = p.splits > 1 ? up256(static_cast<size_t>(p.splits) * s.rows * ((features + 3) / 4 * 4) * 4) : 0;
   return p;
@@ -1021,27 +1184,30 @@ void launch_layer(const LayerArgs &a, const LayerPlan &p, hipStream_t s) {
   Product q{};
   q.rows = a.rows;
   q.features = a.features;
-  q.depth = depth % 8 == 0 ? depth : up64(depth);      // then B is packed, and A too if it lies along k
+  q.depth = depth % 8 == 0 ? depth : up64(depth);      // then operands that lie along k are packed (or fp32 as they lie)
   q.true_depth = depth;
-  q.a = static_cast<const uint16_t *>(p.pack_a ? a.work : a.weight);
+  q.a = p.pack_a ? a.work : a.weight;
   q.lda = p.pack_a ? up64(a.shape.in) : a.shape.in;
   q.a_part = a.shape.out * q.lda;
-  q.b = static_cast<const uint16_t *>(p.pack_b ? work_at(a, p.a_bytes) : a.x);
+  q.b = p.pack_b ? work_at(a, p.a_bytes) : a.x;
   q.ldb = p.pack_b ? up64(depth) : a.ldx;
   q.b_part = a.rows * q.ldb;
   if (p.a_parts * p.b_parts == 1) {
-    if (p.tile == 0) layer_one<256, 256, 4, 2, 64, 1, 1, 2, 1>(a, p, q, part, s);
-    else if (p.tile == 1) layer_one<128, 128, 4, 2, 64, 1, 1, 2, 2>(a, p, q, part, s);
-    else layer_one<128, 32, 4, 1, 64, 1, 1, 4, 2>(a, p, q, part, s);
+    if (p.tile == 0) layer_one<256, 256, 4, 2, 64, 1, 1, false, 2, 1>(a, p, q, part, s);
+    else if (p.tile == 1) layer_one<128, 128, 4, 2, 64, 1, 1, false, 2, 2>(a, p, q, part, s);
+    else layer_one<128, 32, 4, 1, 64, 1, 1, false, 4, 2>(a, p, q, part, s);
   } else if (p.a_parts == 3 && p.b_parts == 3) {
-    if (p.tile == 0) layer_one<128, 128, 2, 2, 32, 3, 3, 3, 1>(a, p, q, part, s);
-    else layer_one<128, 64, 4, 1, 32, 3, 3, 4, 1>(a, p, q, part, s);
+    if (p.tile == 0) layer_one<128, 128, 2, 2, 32, 3, 3, false, 3, 1>(a, p, q, part, s);
+    else if (p.tile == 1) layer_one<128, 64, 4, 1, 32, 3, 3, false, 4, 1>(a, p, q, part, s);
+    else layer_one<128, 64, 4, 1, 32, 3, 3, true, 2, 1>(a, p, q, part, s);
   } else if (p.a_parts == 3) {
-    if (p.tile == 0) layer_one<128, 128, 2, 2, 32, 3, 1, 2, 2>(a, p, q, part, s);
-    else layer_one<128, 64, 4, 1, 32, 3, 1, 2, 2>(a, p, q, part, s);
+    if (p.tile == 0) layer_one<128, 128, 2, 2, 32, 3, 1, false, 2, 2>(a, p, q, part, s);
+    else if (p.tile == 1) layer_one<128, 64, 4, 1, 32, 3, 1, false, 2, 2>(a, p, q, part, s);
+    else layer_one<128, 64, 4, 1, 32, 3, 1, true, 2, 1>(a, p, q, part, s);
   } else {
-    if (p.tile == 0) layer_one<128, 128, 2, 2, 32, 1, 3, 2, 2>(a, p, q, part, s);
-    else layer_one<128, 64, 4, 1, 32, 1, 3, 2, 2>(a, p, q, part, s);
+    if (p.tile == 0) layer_one<128, 128, 2, 2, 32, 1, 3, false, 2, 2>(a, p, q, part, s);
+    else if (p.tile == 1) layer_one<128, 64, 4, 1, 32, 1, 3, false, 2, 2>(a, p, q, part, s);
+    else layer_one<128, 64, 4, 1, 32, 1, 3, true, 2, 1>(a, p, q, part, s);
   }
 }
 
@@ -1049,8 +1215,7 @@ void launch_layer_join(const LayerArgs &a, const LayerPlan &p, hipStream_t s) {
   const float *part = reinterpret_cast<const float *>(work_at(a, p.a_bytes + p.b_bytes));
   const dim3 grid(static_cast<unsigned>((a.rows + 31) / 32 * ((a.features + kJoinWidth - 1) / kJoinWidth)));
   by_kind(a, [&](auto back, auto fn) {
-    if (p.splits >= 4 && grid.x < 256) layer_join_kernel<4, decltype(back)::value, decltype(fn)::value><<<grid, kBlock * 4, 0, s>>>(a, part, p.splits);
-    else layer_join_kernel<1, decltype(back)::value, decltype(fn)::value><<<grid, kBlock, 0, s>>>(a, part, p.splits);
+    layer_join_kernel<decltype(back)::value, decltype(fn)::value><<<grid, kBlock, 0, s>>>(a, part, p.splits);
   });
 }
 

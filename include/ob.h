@@ -403,7 +403,8 @@ int ob_cltk_step(ob_ctx *ctx, int64_t step, const void *grads, float *memory, in
 
 /* ------------------------------------------------------------------------
  * What fills a worker's gradient row: embedding lookup and gradient, 8-bit
- * activation checkpoints, and the linear layer's gradient from one.
+ * activation checkpoints, and the linear layer: its forward, the gradient to
+ * its input, and its weight's gradient from a checkpoint.
  *
  * Matrices are [rows][cols] with a row stride of ld >= cols elements; their
  * pointers need the alignment of their element only (rows that all start on
@@ -493,7 +494,8 @@ int ob_linear_grad(ob_ctx *ctx, int32_t worker, int32_t weight, int32_t bias, in
  * bf16 parts (bits below 2^-133 are dropped), and of two fp32 operands the
  * products of parts below 2^-25 of the whole are left out.  An infinity in an fp32 operand may
  * give NaN where plain arithmetic gives an infinity.  fn as in ob_act_save.
- * rows up to 2^24, features up to 2^21.
+ * rows up to 2^24, features up to 2^21, and ceil(rows/128) * ceil(f/128) at most
+ * 8,388,607 for the larger f of the two.
  *
  * ob_linear_work (host only): the scratch of a call.  aligned != 0 promises that
  * x (dy) starts on 16 bytes, its row stride is a multiple of 16 bytes and at most

@@ -152,6 +152,21 @@ def test_many_tiles(rows, out, inp, extra, xt, lt):
     assert np.array_equal(_f64(dx), _round(_f64(dy) @ ly.w, xt))
 
 
+@pytest.mark.parametrize("rows,out,inp,extra", [(8, 8200, 4104, 0), (8, 8200, 4101, 0), (8, 8200, 4104, 3), (6, 4104, 2048, 0),
+                                                (6, 4100, 2056, 0), (8, 4104, 1032, 8)])
+@pytest.mark.parametrize("xt,lt", TYPES)
+def test_few_tokens_of_large_weights(rows, out, inp, extra, xt, lt):
+    """Both sides of the sizes from which few tokens take the matrix units; whole numbers, bit for bit."""
+    ly = Layer(out, inp, lt, seed=4, whole=True)
+    x, _ = _put(_values(rows, inp, 1, True), xt, extra)
+    dy, _ = _put(_values(rows, out, 2, True), xt, extra)
+    y, dx = torch.empty(rows, out, dtype=xt, device=DEV), torch.empty(rows, inp, dtype=xt, device=DEV)
+    ly.opt.linear(1, 2, x, ly.list, y)
+    assert np.array_equal(_f64(y), _round(_f64(x) @ ly.w.T + ly.b, xt))
+    ly.opt.linear_input_grad(1, dy, ly.list, dx)
+    assert np.array_equal(_f64(dx), _round(_f64(dy) @ ly.w, xt))
+
+
 def _sum_error(n, mag, xt, lt):
     """n additions in any order are off by n * 2^-24 of the sum of magnitudes, twice that for the matrix unit, whose
     inner sums may truncate; each fp32 operand has three parts, two of them six products, whose leading ones alone
@@ -352,7 +367,7 @@ def test_no_rows():
 
 def test_work_streams_and_repeats():
     """A caller's own scratch, full of NaN, another stream, two calls at once on two streams: the same bits."""
-    rows, out, inp = 65, 300, 1000
+    rows, out, inp = 65, 300, 4000
     ly = Layer(out, inp, F32, seed=2)
     x = _values(rows, inp, 1, False).to(DEV)
     y = [torch.empty(rows, out, device=DEV) for _ in range(4)]
