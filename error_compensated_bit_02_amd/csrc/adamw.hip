@@ -26,6 +26,13 @@
 // is this rounding, carry into the exponent and subnormals included.
 // A root above 0 keeps the smallest code at least: 0 under a moment that is not 0
 // would make the step m/eps.
+//
+// Bound by the memory: gradients are streamed past the caches, eight workers' rows
+// loaded four at a time before they are added.  Eight workers of fp32 gradients with
+// fp32 moments and a bf16 copy of the weights (107 M elements, 6.2 GB) 1145 us, 5.4 TB/s;
+// one worker's bf16 gradients with 8-bit moments (334 M, 5.4 GB) 975-1020 us, 5.3-5.6; their
+// values read back as bf16 (2.1 GB) 393-401 us.  Small lists are the launch's: 2050
+// elements 3 us, 1.8 M with 8-bit moments 10.
 #include "internal.h"
 #include "activation.h"
 

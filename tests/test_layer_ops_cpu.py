@@ -44,6 +44,9 @@ def test_linear_work_sizes(lib):
         for bad in [(-1, 8, 8), ((1 << 24) + 1, 8, 8), (8, 0, 8), (8, 8, 0), (8, (1 << 21) + 1, 8), (8, 8, (1 << 21) + 1),
                     (1 << 24, 1 << 21, 8)]:
             assert work(*bad, back=back) == -INVALID, bad
+        # the tiles of 128 x 128 fit a grid
+        assert work(1 << 24, (1 << 13) - 128, 8, dt=0, back=back) >= 0 and work(1 << 24, 8, (1 << 13) - 128, lt=0, back=back) >= 0
+        assert work(1 << 24, 1 << 13, 8, dt=0, back=back) == -INVALID and work(1 << 24, 8, 1 << 13, back=back) == -INVALID
         assert work(8, 8, 8, dt=2, back=back) == -INVALID and work(8, 8, 8, lt=-1, back=back) == -INVALID
     assert work(64, 64, 7) >= 2 * 64 * 64 * 2                                # rows of 7 elements: both operands are copied
     assert lib.ob_linear_work(1, 1, 1, 0, 0, 1, 0, None) == INVALID
