@@ -8,6 +8,7 @@ back to.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Dict, List, Optional, Sequence
 
@@ -521,7 +522,9 @@ class OneBitAdam:
         bfloat16, the new parameters; seed: of the 8-bit moments' rounding, another one every step."""
         f32 = torch.float32
         kind, m, ms, v, vs = self._moments(state)
-        seed = int(seed)
+        step, seed = operator.index(step), int(seed)
+        if not -(1 << 63) <= step < 1 << 63:      # ctypes would take it modulo 2^64
+            raise OneBitError(f"step {step} is not a 64-bit integer", OB_ERR_INVALID)
         if not 0 <= seed < 1 << 64:
             raise OneBitError(f"seed {seed} is not a 64-bit unsigned integer", OB_ERR_INVALID)
         _check(_call(

@@ -389,3 +389,25 @@ def test_refusals():
         x.opt.adamw_load(x.state, torch.zeros(x.N, device=DEV), torch.zeros(x.N, dtype=torch.bfloat16, device=DEV))
     with pytest.raises(OneBitError, match="unknown moments"):
         x.opt.adamw_state("4bit")
+
+
+def test_steps_of_other_integer_types():
+    """A step counted by numpy or torch is the same step; one past 64 bits is refused, not taken modulo 2^64."""
+    want = List([100], 1, "f32", "8bit", seed=2)
+    g = want.new_grads()
+    want.step(g, 3, seed=9)
+    real = want.real.to(DEV)
+    for kind in (np.int64, np.int32, torch.tensor):
+        x = List([100], 1, "f32", "8bit", seed=2)
+        x.step(g, kind(3), seed=9)
+        assert torch.equal(x.params[real], want.params[real])
+        for k in ("m", "m_scale", "v", "v_scale"):
+            assert torch.equal(x.state[k], want.state[k])
+    x = List([100], 1, "f32", "8bit", seed=2)
+    before = x.params.clone()
+    for step in ((1 << 64) + 3, 1 << 63, -(1 << 63) - 1):
+        with pytest.raises(OneBitError, match="64-bit"):
+            x.step(g, step)
+    with pytest.raises(TypeError):
+        x.step(g, 1.5)
+    assert torch.equal(x.params[real], before[real]) and int(x.state["m_scale"].count_nonzero()) == 0
