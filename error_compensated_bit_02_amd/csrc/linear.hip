@@ -1067,10 +1067,17 @@ void layer_few(const LayerArgs &a, int slices, float *part, hipStream_t s) {
   // Wavefronts that share their rows, but where four times 512 steps are more than there are:
   // 8 tokens of 1024 -> 8192 in bf16 15.4 us so and 7.5 the other way, of 2048 -> 8192 17.9
   // and 9.6; of 8192 -> 2048 10.5 and 19.1, one token of 8192 -> 8192 20.6 and 28.7.
-  const bool own = R > 1 && a.shape.in <= 512 * kWaves && a.features >= 4096;
-  if (a.shape.back) layer_few_back_kernel<R, TW, TX><<<dim3(groups(kFewLanes * 8), slices), kFewBlock, 0, s>>>(a, part);
-  else if (own) layer_few_kernel<R, TW, TX, false><<<groups(kFewRows * kWaves), kBlock, 0, s>>>(a);
-  else layer_few_kernel<R, TW, TX, true><<<groups(kFewRows), kBlock, 0, s>>>(a);
+  if (a.shape.back) {
+    layer_few_back_kernel<R, TW, TX><<<dim3(groups(kFewLanes * 8), slices), kFewBlock, 0, s>>>(a, part);
+    return;
+  }
+  if constexpr (R > 1) {
+    if (a.shape.in <= 512 * kWaves && a.features >= 4096) {
+      layer_few_kernel<R, TW, TX, false><<<groups(kFewRows * kWaves), kBlock, 0, s>>>(a);
+      return;
+    }
+  }
+  layer_few_kernel<R, TW, TX, true><<<groups(kFewRows), kBlock, 0, s>>>(a);
 }
 
 template <typename TW, typename TX>
