@@ -839,11 +839,7 @@ __global__ __launch_bounds__(kBlock) void layer_few_kernel(const LayerArgs a) {
     add(w, x);
   }
   const int at = scatter_sums<kFewRows * R, 32, 1>(acc);
-  if constexpr (kFewRows * R == 32) {
-    if ((lane & 1) == 0) sums[wave][at] = acc[0];
-  } else {
-    if ((lane & (64 / (kFewRows * R) - 1)) == 0) sums[wave][at] = acc[0];
-  }
+  if ((lane & (64 / (kFewRows * R) - 1)) == 0) sums[wave][at] = acc[0];      // the lanes' last bits hold copies
   __syncthreads();
   const int c = threadIdx.x;
   if (c >= FEATURES || g0 + c >= a.features) return;
