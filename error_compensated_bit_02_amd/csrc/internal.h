@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <cstdint>
 
+#include "layer_plan.h"
+
 namespace ob {
 
 // One workgroup handles one tile (or one chunk of one; see kChunk): kTile
@@ -344,23 +346,7 @@ void launch_linear_grad(const LinearArgs &a, hipStream_t s);
 bool linear_needs_join(const LinearArgs &a);
 void launch_linear_join(const LinearArgs &a, hipStream_t s);
 
-// A linear layer's forward and input gradient (linear.hip).
-struct LayerShape {
-  int64_t rows, out, in;     // tokens, rows of the weight, columns of the weight
-  bool f32;                  // type of x (or dy), y (dx) and what is added
-  bool weight_f32;           // type of the list that holds weight and bias
-  bool aligned;              // x's (dy's) rows start on 16 bytes
-  bool back;                 // the input gradient
-};
-// How a call of this shape runs: operands packed into the workspace, tiles,
-// slices of the contraction.  The workspace holds A's parts, B's and the slices' sums.
-struct LayerPlan {
-  bool pack_a, pack_b;       // A: the weight, B: x or dy
-  int a_parts, b_parts;
-  int tile, m_tiles, n_tiles, splits;
-  int64_t turns_each;
-  size_t a_bytes, b_bytes, part_bytes;
-};
+// A linear layer's forward and input gradient (linear.hip, layer_plan.h).
 struct LayerArgs {
   LayerShape shape;
   int64_t rows, features;    // of y or dx
@@ -381,8 +367,6 @@ struct LayerArgs {
   bool vec_y, vec_add;       // their rows start on 16 bytes
   void *work;
 };
-bool layer_fits(int64_t rows, int64_t out, int64_t in);
-LayerPlan layer_plan(const LayerShape &s);
 void launch_layer_pack(const LayerArgs &a, const LayerPlan &p, hipStream_t s);   // if pack_a or pack_b
 void launch_layer(const LayerArgs &a, const LayerPlan &p, hipStream_t s);
 void launch_layer_join(const LayerArgs &a, const LayerPlan &p, hipStream_t s);   // if splits > 1

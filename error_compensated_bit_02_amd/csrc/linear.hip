@@ -674,16 +674,16 @@ __global__ __launch_bounds__(kBlock) void layer_join_kernel(const LayerArgs a, c
 // ---------------------------------------------------------------------------
 // a few tokens: bound by reading the weight
 // ---------------------------------------------------------------------------
-// Up to kFewTokens tokens are multiplied on the vector units in fp32, straight from
+// Up to kLayerFew tokens are multiplied on the vector units in fp32, straight from
 // the weight as it lies in the list, whatever its type or alignment: no copies of
 // parts, no tile that is mostly padding, and in the forward no join.  One token of
 // 1024 -> 4096 in bf16 7.5 us a call (the kernel 3.5), 13 through a tile of the matrix
 // units; where these win, few_by_vectors says.
-constexpr int kFewTokens = 8;
 constexpr int kFewRows = 4;           // forward: features of a wavefront
 constexpr int kFewLanes = 4;          // backward: lanes, of eight features each, of a workgroup
 constexpr int kFewBlock = 512, kFewGroups = kFewBlock / kFewLanes;
-constexpr int kFewEach = 8, kFewChunk = kFewEach * kFewGroups;        // backward: rows of a group, of a workgroup, under way together
+constexpr int kFewEach = 8;           // backward: rows of a group, under way together with the others'
+static_assert(kFewEach * kFewGroups == kLayerSlice, "a workgroup's rows are a slice");
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v) {
@@ -866,13 +866,13 @@ __global__ __launch_bounds__(kBlock) void layer_few_kernel(const LayerArgs a) {
 template <int R, typename TW, typename TX>
 __global__ __launch_bounds__(kFewBlock) void layer_few_back_kernel(const LayerArgs a, float *part) {
   constexpr int FEATURES = kFewLanes * 8, WAVES = kFewBlock / 64;
-  __shared__ __attribute__((aligned(16))) float dys[kFewChunk][R];
+  __shared__ __attribute__((aligned(16))) float dys[kLayerSlice][R];
   __shared__ float sums[WAVES][R][FEATURES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = threadIdx.x / kFewLanes, l = threadIdx.x % kFewLanes;
   const uint32_t xcd = blockIdx.x % kXcds, place = xcd * (gridDim.x / kXcds) + min(xcd, gridDim.x % kXcds) + blockIdx.x / kXcds;
-  const int64_t g0 = static_cast<int64_t>(place) * FEATURES, f = g0 + l * 8, c0 = static_cast<int64_t>(blockIdx.y) * kFewChunk;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(kFewChunk), a.shape.out - c0));
+  const int64_t g0 = static_cast<int64_t>(place) * FEATURES, f = g0 + l * 8, c0 = static_cast<int64_t>(blockIdx.y) * kLayerSlice;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(kLayerSlice), a.shape.out - c0));
   const int64_t n = a.features - f;
   Eight<TW> w[kFewEach];
 #pragma unroll
@@ -999,41 +999,8 @@ __global__ __launch_bounds__(kBlock) void pack_kernel(const PackArgs a, const Pa
 }
 
 // ---------------------------------------------------------------------------
-// plans
+// launches
 // ---------------------------------------------------------------------------
-// Tiles that are built, and their times in microseconds: of a workgroup's start and
-// end, of a turn on a CU of its own and with as many workgroups as a CU holds.  The
-// plan is the tile and the number of slices with the least time by them.  Forward /
-// gradient in us with each tile's best slices, the taken one marked:
-//   bf16               256 x 256    128 x 128      128 x 32
-//   1024^3             30 / 31      11.6 / 11.7    8.7 / 8.6 *
-//   4096 x 2048^2      44 / 44      36 / 36 *      62 / 61
-//   4096^3             100 / 100 *  129 / 130      226 / 232
-//   16384 2048->8192   422 / 402 *  532 / 508      918 / 965
-//   fp32               128 x 128    128 x 64       128 x 64, cut on the way
-//   777 2048->1000     37* / 35     41 / 34 *      45 / 43
-//   256 x 2048^2       33 / 32      32 / 32        28 / 30 *
-//   4096^3             703 / 668 *  860 / 770      850 / 884
-//   bf16 and fp32 weights
-//   64 x 4096^2        62 / 49      60 / 49        26 / 27 *
-//   777 2048->1000     29* / 35     32 / 32 *      42 / 33
-//   2048^3             64 / 58 *    78 / 58        77 / 84
-// Cutting on the way saves the parts' copy, whose cost the weight's size settles, and
-// cuts an operand again in every tile that reads it: it wins where few tiles share it.
-struct Tiles {
-  int features, tokens, depth, per_cu;
-  bool raw;                          // fp32 as it lies
-  double start, alone, full;
-};
-constexpr Tiles kPlainTiles[] = {{256, 256, 64, 1, false, 9.0, 1.40, 1.40}, {128, 128, 64, 2, false, 4.5, 0.60, 1.0}, {128, 32, 64, 2, false, 4.0, 0.40, 0.55}};
-constexpr Tiles kSixTiles[] = {{128, 128, 32, 1, false, 5.0, 1.20, 1.25}, {128, 64, 32, 1, false, 4.0, 0.70, 0.78}, {128, 64, 32, 1, true, 4.0, 1.20, 1.20}};
-constexpr Tiles kThreeTiles[] = {{128, 128, 32, 2, false, 5.0, 0.50, 0.85}, {128, 64, 32, 2, false, 4.0, 0.40, 0.60}, {128, 64, 32, 1, true, 4.0, 0.70, 0.70}};
-
-int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-int64_t features_of(const LayerShape &s) { return s.back ? s.in : s.out; }
-int64_t depth_of(const LayerShape &s) { return s.back ? s.out : s.in; }
-
 // Calls f with the direction and the activation as constants.
 template <typename F>
 void by_kind(const LayerArgs &a, F &&f) {
@@ -1083,87 +1050,14 @@ void layer_few_by_rows(const LayerArgs &a, int slices, float *part, hipStream_t 
   else layer_few<8, TW, TX>(a, slices, part, s);
 }
 
-// Whether few tokens go through the vector units.  Their time grows with the tokens, the
-// matrix units' hardly does.  Forward / gradient in us, vector units against matrix units:
-//   bf16  1 token    4096 x 4096  8 / 12.5 : 13 / 13    8192 x 8192  21 / 30 : 25 / 27
-//         4 tokens   4096 x 4096  8 / 14 : 13 / 13      8192 x 8192  22 / 42 : 25 / 27
-//         8 tokens   2048 x 2048  8 / 13.5 : 13 / 13    4096 x 4096  12.5 / 27 : 13 / 13
-//                    8192 x 8192  35 / 89 : 25 / 27
-//   fp32  1 token    8192 x 8192  42 / 43 : 89 / 84
-//         8 tokens   4096 x 4096  18 / 29 : 29 / 28     8192 x 8192  55 / 92 : 92 / 85
-// A bf16 weight that the matrix units cannot read as it lies would be copied first.
-bool few_by_vectors(const LayerShape &s) {
-  if (s.rows > kFewTokens) return false;
-  const int64_t work = s.rows * s.out * s.in;
-  if (s.weight_f32) return !s.back || work <= int64_t{1} << 28;
-  return s.in % 8 != 0 || work <= int64_t{1} << (s.back ? 25 : 28);
-}
-
 char *work_at(const LayerArgs &a, size_t bytes) { return static_cast<char *>(a.work) + bytes; }
 
 }  // namespace
 
-bool layer_fits(int64_t rows, int64_t out, int64_t in) {
-  // a tile's 256 rows (or 64 of the weight) lie within 2 GB; tiles of 128 x 128 fit the grid
-  constexpr int64_t kMost = int64_t{1} << 21;
-  return rows >= 0 && rows <= (int64_t{1} << 24) && out >= 1 && out <= kMost && in >= 1 && in <= kMost &&
-         ((rows + 127) / 128) * ((std::max(out, in) + 127) / 128) <= kMaxGrid / 2;
-}
-
-LayerPlan layer_plan(const LayerShape &s) {
-  LayerPlan p{};
-  const int64_t features = features_of(s), depth = depth_of(s);
-  p.splits = 1;
-  if (few_by_vectors(s)) {
-    p.tile = -1;
-    if (s.back) p.splits = static_cast<int>((depth + kFewChunk - 1) / kFewChunk);
-  } else {
-    p.a_parts = s.weight_f32 ? 3 : 1;
-    p.b_parts = s.f32 ? 3 : 1;
-    const bool raw_rows_a = !s.weight_f32 && s.in % 8 != 0, raw_rows_b = !s.f32 && (depth % 8 != 0 || !s.aligned);
-    const size_t a_bytes = up256(static_cast<size_t>(p.a_parts) * s.out * up64(s.in) * 2);
-    const size_t b_bytes = up256(static_cast<size_t>(p.b_parts) * s.rows * up64(depth) * 2);
-    const int products = p.a_parts * p.b_parts;
-    const Tiles *tiles = products == 1 ? kPlainTiles : products == 9 ? kSixTiles : kThreeTiles;
-    const double part = static_cast<double>(s.rows) * features * 4 / 3e6;
-    double best = 0.0;
-    p.tile = -1;
-    for (int k = 0; k < 3; ++k) {
-      const int64_t m = (features + tiles[k].features - 1) / tiles[k].features, n = (s.rows + tiles[k].tokens - 1) / tiles[k].tokens;
-      const int64_t turns = (depth + tiles[k].depth - 1) / tiles[k].depth, most = m * n >= 512 ? 1 : std::min<int64_t>(turns, 64);      // no slices where the tiles fill the card
-      // packing: its launch, and ten bytes read and written an fp32 element (four a bf16 one)
-      const bool pack_a = raw_rows_a || (s.weight_f32 && !tiles[k].raw), pack_b = raw_rows_b || (s.f32 && !tiles[k].raw);
-      const double packing = (pack_a || pack_b ? 4.0 : 0.0) + (pack_a ? a_bytes / 3.5e6 : 0.0) + (pack_b ? b_bytes / 3.5e6 : 0.0);
-      for (int64_t want = 1; want <= most; ++want) {
-        const int64_t each = (turns + want - 1) / want, splits = (turns + each - 1) / each, groups = m * n * splits;
-        if (splits != want || groups > kMaxGrid / 2) continue;
-        double t = packing + tiles[k].start + (splits > 1 ? 4.0 + splits * part : 0.0);
-        const int64_t held = 256 * tiles[k].per_cu;
-        if (groups <= 256) t += each * tiles[k].alone;
-        else t += static_cast<double>((groups + held - 1) / held) * each * tiles[k].full;
-        if (p.tile < 0 || t < best) {
-          best = t;
-          p.tile = k;
-          p.m_tiles = static_cast<int>(m);
-          p.n_tiles = static_cast<int>(n);
-          p.splits = static_cast<int>(splits);
-          p.turns_each = each;
-          p.pack_a = pack_a;
-          p.pack_b = pack_b;
-        }
-      }
-    }
-    p.a_bytes = p.pack_a ? a_bytes : 0;
-    p.b_bytes = p.pack_b ? b_bytes : 0;
-  }
-  p.part_bytes = p.splits > 1 ? up256(static_cast<size_t>(p.splits) * s.rows * ((features + 3) / 4 * 4) * 4) : 0;
-  return p;
-}
-
 void launch_layer_pack(const LayerArgs &a, const LayerPlan &p, hipStream_t s) {
-  const int64_t depth = depth_of(a.shape);
-  const PackArgs w{a.weight, a.weight_f32, a.shape.in, static_cast<uint16_t *>(a.work), a.shape.out, a.shape.in, up64(a.shape.in)};
-  const PackArgs x{a.x, a.f32, a.ldx, reinterpret_cast<uint16_t *>(work_at(a, p.a_bytes)), a.rows, depth, up64(depth)};
+  const int64_t depth = layer_depth(a.shape);
+  const PackArgs w{a.weight, a.weight_f32, a.shape.in, static_cast<uint16_t *>(a.work), a.shape.out, a.shape.in, layer_pitch(a.shape.in)};
+  const PackArgs x{a.x, a.f32, a.ldx, reinterpret_cast<uint16_t *>(work_at(a, p.a_bytes)), a.rows, depth, layer_pitch(depth)};
   const auto blocks = [](const PackArgs &q) {
     return static_cast<uint32_t>(std::min<int64_t>((q.rows * (q.pitch / 8) + kBlock - 1) / kBlock, 1 << 15));
   };
@@ -1183,17 +1077,17 @@ void launch_layer(const LayerArgs &a, const LayerPlan &p, hipStream_t s) {
     }
     return;
   }
-  const int64_t depth = depth_of(a.shape);
+  const int64_t depth = layer_depth(a.shape);
   Product q{};
   q.rows = a.rows;
   q.features = a.features;
-  q.depth = depth % 8 == 0 ? depth : up64(depth);      // then operands that lie along k are packed (or fp32 as they lie)
+  q.depth = depth % 8 == 0 ? depth : layer_pitch(depth);      // then operands that lie along k are packed (or fp32 as they lie)
   q.true_depth = depth;
   q.a = p.pack_a ? a.work : a.weight;
-  q.lda = p.pack_a ? up64(a.shape.in) : a.shape.in;
+  q.lda = p.pack_a ? layer_pitch(a.shape.in) : a.shape.in;
   q.a_part = a.shape.out * q.lda;
   q.b = p.pack_b ? work_at(a, p.a_bytes) : a.x;
-  q.ldb = p.pack_b ? up64(depth) : a.ldx;
+  q.ldb = p.pack_b ? layer_pitch(depth) : a.ldx;
   q.b_part = a.rows * q.ldb;
   if (p.a_parts * p.b_parts == 1) {
     if (p.tile == 0) layer_one<256, 256, 4, 2, 64, 1, 1, false, 2, 1>(a, p, q, part, s);
