@@ -1,0 +1,194 @@
+"""A linear layer's forward and input gradient at the ends of their documented ranges:
+matrices past 2^31 elements, the longest contraction, the most features and rows, the
+longest row stride.  Whole numbers whose sums fp32 holds, compared bit
+for bit on the GPU, slice by slice."""
+import pytest
+import torch
+
+import linear_cases as cases
+import test_linear_gpu as base
+import test_linear_plans_gpu as plans
+from error_compensated_bit_02_amd import ActCheckpoint, OneBitAdam
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, BF16 = cases.F32, cases.BF16
+TYPES = base.TYPES
+SLICE = 1 << 17
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    yield
+    torch.cuda.empty_cache()      # some cases take tens of GB
+
+
+def whole(rows, cols, dtype, seed, lim=3, extra=0):
+    """Whole numbers of at most lim, rows and columns of a buffer `extra` columns wider."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    t = torch.randint(-lim, lim + 1, (rows, cols + extra), generator=g, device=DEV, dtype=torch.int8).to(dtype)
+    return t[:, :cols]
+
+
+class Layer:
+    """A list of one weight and one bias on the GPU."""
+
+    def __init__(self, out, inp, dtype, lim=2, seed=5):
+        self.opt = OneBitAdam([out * inp, out], 1)
+        o = self.opt.offsets
+        self.list = torch.zeros(self.opt.N, dtype=dtype, device=DEV)
+        self.w = self.list[: out * inp].view(out, inp)
+        self.w.copy_(whole(out, inp, dtype, seed, lim))
+        self.b = self.list[o[1]: o[1] + out]
+        self.b.copy_(whole(1, out, dtype, seed + 1, 9)[0])
+
+
+def forward(x, ly):
+    """The sums in fp32, which holds them (a copy of the right operand that lies along its columns)."""
+    return x.float() @ ly.w.float().t().contiguous() + ly.b.float()
+
+
+def backward(dy, ly):
+    return dy.float() @ ly.w.float()
+
+
+MANY = (1 << 21) + 77             # times 1032: past 2^31
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_results_past_2_to_the_31(dt):
+    """y (in place over the residual), codes and scales; a last block of 32 rows that is not full."""
+    rows, out, inp = MANY, 1032, 16
+    ly, x = Layer(out, inp, dt), whole(rows, inp, dt, 1)
+    y = whole(rows, out, dt, 2)
+    res = [y[a: a + SLICE].clone() for a in range(0, rows, SLICE)]
+    ck = ActCheckpoint(rows, out, "e4m3", device=DEV)
+    ly.opt.linear(0, 1, x, ly.list, y, residual=y, keep=ck)
+    for k, a in enumerate(range(0, rows, SLICE)):
+        h = forward(x[a: a + SLICE], ly)
+        assert torch.equal(y[a: a + SLICE], (h + res[k].float()).to(dt)), a
+        other = ActCheckpoint(len(h), out, "e4m3", device=DEV)
+        other.save(h)
+        assert torch.equal(ck.codes[a: a + SLICE, :out], other.codes[:, :out])
+        assert torch.equal(ck.scales[a // 32: a // 32 + len(other.scales), :out], other.scales[:, :out])
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_input_gradients_past_2_to_the_31(dt):
+    """dx in place over the added gradient, and with the activation's derivative from codes past 2^31 bytes."""
+    rows, out, inp = MANY, 16, 1032
+    ly, dy = Layer(out, inp, dt), whole(rows, out, dt, 1)
+    dx = whole(rows, inp, dt, 2)
+    add = [dx[a: a + SLICE].clone() for a in range(0, rows, SLICE)]
+    ly.opt.linear_input_grad(0, dy, ly.list, dx, add=dx)
+    for k, a in enumerate(range(0, rows, SLICE)):
+        assert torch.equal(dx[a: a + SLICE], (backward(dy[a: a + SLICE], ly) + add[k].float()).to(dt)), a
+    del add
+    ck = ActCheckpoint(rows, inp, "int8", device=DEV)
+    for a in range(0, rows, SLICE):
+        dx[a: a + SLICE].mul_(0.0625)
+    ck.save(dx)
+    held = torch.empty(rows, inp, dtype=BF16, device=DEV)
+    ck.load(held)
+    ly.opt.linear_input_grad(0, dy, ly.list, dx, act="silu", kept=ck)
+    for a in list(range(0, rows - SLICE, 4 * SLICE)) + [rows - 5000]:
+        at = slice(a, a + 4096)
+        z, g = held[at].double(), backward(dy[at], ly).double()
+        want = g * plans.slope(z, "silu")[0]
+        plans.near(dx[at], want, g.abs() * plans.slope_error(z, "silu") + base.ref.U32 * want.abs(), dt)
+
+
+@pytest.mark.parametrize("extra", [0, 1])
+@pytest.mark.parametrize("dt,lt", TYPES)
+def test_inputs_past_2_to_the_31(dt, lt, extra):
+    """x and dy of more than 2^31 elements, read as they lie and through a copy."""
+    rows, long, short = (1 << 20) + 5, 2056, 24
+    x = whole(rows, long, dt, 1, extra=extra)
+    ly = Layer(short, long, lt)
+    y = torch.empty(rows, short, dtype=dt, device=DEV)
+    ly.opt.linear(0, 1, x, ly.list, y)
+    for a in range(0, rows, SLICE):
+        assert torch.equal(y[a: a + SLICE], forward(x[a: a + SLICE], ly).to(dt)), a
+    ly = Layer(long, short, lt)
+    ly.opt.linear_input_grad(0, x, ly.list, y)
+    for a in range(0, rows, SLICE):
+        assert torch.equal(y[a: a + SLICE], backward(x[a: a + SLICE], ly).to(dt)), a
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+@pytest.mark.parametrize("long", [1 << 21, (1 << 21) - 5])
+@pytest.mark.parametrize("dt,lt", TYPES)
+def test_longest_contraction(dt, lt, long, rows):
+    """2^21 steps, values of at most 1: sums of at most 2^21."""
+    x = whole(rows, long, dt, 1, lim=1)
+    ly = Layer(24, long, lt, lim=1)
+    y = torch.empty(rows, 24, dtype=dt, device=DEV)
+    ly.opt.linear(0, 1, x, ly.list, y)
+    assert torch.equal(y, forward(x, ly).to(dt))
+    ly = Layer(long, 24, lt, lim=1)
+    ly.opt.linear_input_grad(0, x, ly.list, y)
+    assert torch.equal(y, backward(x, ly).to(dt))
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+@pytest.mark.parametrize("wide", [1 << 21, (1 << 21) - 5])
+@pytest.mark.parametrize("dt,lt", TYPES)
+def test_most_features(dt, lt, wide, rows):
+    x = whole(rows, 24, dt, 1)
+    ly = Layer(wide, 24, lt)
+    y = torch.empty(rows, wide, dtype=dt, device=DEV)
+    ly.opt.linear(0, 1, x, ly.list, y)
+    assert torch.equal(y, forward(x, ly).to(dt))
+    ly = Layer(24, wide, lt)
+    ly.opt.linear_input_grad(0, x, ly.list, y)
+    assert torch.equal(y, backward(x, ly).to(dt))
+
+
+def test_large_tiles_of_the_longest_rows():
+    """Rows of 2^21 elements in both operands, 300 of each: the farthest offsets within a tile."""
+    n, long = 300, 1 << 21
+    x = whole(n, long, BF16, 1, lim=1)
+    ly = Layer(n, long, BF16, lim=1)
+    y = torch.empty(n, n, dtype=BF16, device=DEV)
+    ly.opt.linear(0, 1, x, ly.list, y)
+    assert torch.equal(y, forward(x, ly).to(BF16))
+    dx = torch.empty(n, long, dtype=BF16, device=DEV)
+    dy = whole(n, n, BF16, 3, lim=1)
+    ly.opt.linear_input_grad(0, dy, ly.list, dx)
+    assert torch.equal(dx, backward(dy, ly).to(BF16))
+
+
+@pytest.mark.parametrize("stride", [1 << 21, (1 << 21) + 8, (1 << 22) + 3])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_long_row_strides(dt, stride):
+    """x up to and past the stride that tiles read as it lies; y, residual and added gradient at the same stride."""
+    rows, out, inp = 300, 136, 72
+    buf = [torch.full((rows, stride), 7.0, dtype=dt, device=DEV) for _ in range(2)]
+    x, y = buf[0][:, :inp], buf[1][:, :out]
+    x.copy_(whole(rows, inp, dt, 1))
+    res = whole(rows, out, dt, 2)
+    y.copy_(res)
+    ly = Layer(out, inp, dt)
+    ly.opt.linear(0, 1, x, ly.list, y, residual=y)
+    assert torch.equal(y, (forward(x, ly) + res.float()).to(dt))
+    assert all(bool((b[:, 136:].amin(dim=1) == 7.0).all() and (b[:, 136:].amax(dim=1) == 7.0).all()) for b in buf)
+    back = Layer(inp, out, dt)
+    ly = back
+    y.copy_(res)
+    ly.opt.linear_input_grad(0, x, ly.list, y, add=y)
+    assert torch.equal(y, (backward(x, ly) + res.float()).to(dt))
+
+
+@pytest.mark.parametrize("dt,lt", TYPES)
+def test_most_rows(dt, lt):
+    rows = 1 << 24
+    x = whole(rows, 8, dt, 1)
+    ly = Layer(8, 8, lt)
+    y = torch.empty(rows, 8, dtype=dt, device=DEV)
+    ly.opt.linear(0, 1, x, ly.list, y)
+    assert torch.equal(y, forward(x, ly).to(dt))
+    ly.opt.linear_input_grad(0, x, ly.list, y)
+    assert torch.equal(y, backward(x, ly).to(dt))
