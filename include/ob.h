@@ -492,8 +492,10 @@ int ob_linear_grad(ob_ctx *ctx, int32_t worker, int32_t weight, int32_t bias, in
  * Sums are fp32 in an order that the sizes, types and x's row stride and
  * alignment settle.  Products of bf16 operands are exact; an fp32 operand is cut into three
  * bf16 parts (bits below 2^-133 are dropped), and of two fp32 operands the
- * products of parts below 2^-25 of the whole are left out.  An infinity in an fp32 operand may
- * give NaN where plain arithmetic gives an infinity.  fn as in ob_act_save.
+ * products of parts below 2^-25 of the whole are left out.  Where an operand is fp32, an infinity
+ * in either gives an infinity or NaN where plain arithmetic gives an infinity, by the kernel that
+ * the sizes settle, and so may a product or sum within 2^-6 of fp32's largest; never a finite
+ * value.  fn as in ob_act_save.
  * rows up to 2^24, features up to 2^21, and ceil(rows/128) * ceil(f/128) at most
  * 8,388,607 for the larger f of the two.
  *

@@ -1,6 +1,6 @@
 """A linear layer's forward and input gradient at the ends of their documented ranges:
 matrices past 2^31 elements, the longest contraction, the most features and rows, the
-longest row stride.  Whole numbers whose sums fp32 holds, compared bit
+longest row stride, and infinities.  Whole numbers whose sums fp32 holds, compared bit
 for bit on the GPU, slice by slice."""
 import pytest
 import torch
@@ -192,3 +192,48 @@ def test_most_rows(dt, lt):
     assert torch.equal(y, forward(x, ly).to(dt))
     ly.opt.linear_input_grad(0, x, ly.list, y)
     assert torch.equal(y, backward(x, ly).to(dt))
+
+
+@pytest.mark.parametrize("rows", [5, 70, 700])
+@pytest.mark.parametrize("dt,lt", TYPES)
+def test_infinities(dt, lt, rows):
+    """An infinity changes its row (of x or dy) or column (of the weight) only.  In bf16 the results are plain
+    arithmetic's; where an operand is fp32 an infinite result may be NaN instead, and none turns finite or changes sign."""
+    n, inf = 80, float("inf")
+    ly = base.Layer(n, n, lt, seed=1, whole=True)
+    at = ly.opt.offsets[1]
+    for back in (False, True):
+        x = base._put(base._values(rows, n, 1, True), dt)[0]
+        y = [torch.empty(rows, n, dtype=dt, device=DEV) for _ in range(2)]
+        ly.list[at: at + n * n] = torch.from_numpy(ly.w).reshape(-1).to(DEV).to(lt)
+
+        def run(out):
+            if back:
+                ly.opt.linear_input_grad(1, x, ly.list, out)
+            else:
+                ly.opt.linear(1, 2, x, ly.list, out)
+
+        run(y[0])
+        x[4, 5], x[rows - 1, 70] = inf, -inf
+        ly.list[at + 9 * n + 3], ly.list[at + 33 * n + 61] = -inf, inf
+        w = ly.list[at: at + n * n].view(n, n).double().cpu()
+        want = x.double().cpu() @ (w if back else w.t().contiguous())
+        want = (want if back else want + torch.from_numpy(ly.b)).to(dt)
+        run(y[1])
+        got, finite = y[1].cpu(), torch.isfinite(want)
+        assert torch.equal(got[finite], want[finite]) and torch.equal(got[finite], y[0].cpu()[finite])
+        nan, up = torch.isnan(want), torch.isinf(want)
+        assert int(up.sum()) > 20 and torch.isnan(got[nan]).all()
+        if dt == lt == BF16:
+            assert torch.equal(got[up], want[up])
+        else:
+            assert (torch.isnan(got[up]) | (got[up] == want[up])).all()
+    x = base._put(base._values(rows, n, 1, True), dt)[0]
+    res = torch.zeros(rows, n, dtype=dt, device=DEV)
+    res[2, 7], res[3, 8] = inf, -inf
+    ly.list[at: at + n * n] = 0.0
+    y = torch.empty(rows, n, dtype=dt, device=DEV)
+    ly.opt.linear(1, None, x, ly.list, y, residual=res, act="gelu")
+    assert torch.equal(y, res)
+    ly.opt.linear_input_grad(1, x, ly.list, y, add=res)
+    assert torch.equal(y, res)
