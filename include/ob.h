@@ -495,7 +495,8 @@ int ob_linear_grad(ob_ctx *ctx, int32_t worker, int32_t weight, int32_t bias, in
  * products of parts below 2^-25 of the whole are left out.  Where an operand is fp32, an infinity
  * in either gives an infinity or NaN where plain arithmetic gives an infinity, by the kernel that
  * the sizes settle, and so may a product or sum within 2^-6 of fp32's largest; never a finite
- * value.  fn as in ob_act_save.
+ * value.  fn as in ob_act_save (gelu_tanh of bf16 results takes fewer operations here, so a
+ * result that lies between two of them may round the other way).
  * rows up to 2^24, features up to 2^21, and ceil(rows/128) * ceil(f/128) at most
  * 8,388,607 for the larger f of the two.
  *
@@ -516,7 +517,7 @@ int ob_linear(ob_ctx *ctx, int32_t weight, int32_t bias, int64_t rows, int64_t o
  * the same place another way (NULL: none).  dy [rows][out_features], add and dx
  * [rows][in_features] have type dtype; dx may be add (with the same row stride), not dy.
  * W, sums, products, limits and scratch as for ob_linear (ob_linear_work with
- * input_grad != 0); fn' as in ob_act_backward. */
+ * input_grad != 0); fn' as in ob_act_backward, with the same remark. */
 int ob_linear_input_grad(ob_ctx *ctx, int32_t weight, int64_t rows, int64_t out_features, int64_t in_features,
                          int32_t dtype, const void *dy, int64_t lddy, int32_t list_dtype, const void *list, int32_t fn,
                          int32_t format, const uint8_t *codes, const uint8_t *scales, const void *add, int64_t ldadd,
