@@ -18,8 +18,8 @@
 // it by a thousandth, a code's half step is a thirtieth, so v stayed at a quarter
 // of its true value while gradients grew and at six times it after they fell
 // tenfold (simulated over 6000 steps).  So codes are rounded down or up with the
-// probability of the remainder: unbiased (v's median within 5% over the same
-// steps, 90% of the elements within a factor of 1.5 to 2).  The 16 bits that
+// probability of the remainder in 16 bits: unbiased to within 2^-16 of a step (v's
+// median within 5% over the same steps, 90% of the elements within a factor of 1.5 to 2).  The 16 bits that
 // settle it are a hash of the element's place and the caller's seed, so a step
 // repeats bit for bit.  Where x is scaled so that the format's subnormal codes
 // lie at fp32's, adding them below the code's last bit and cutting off the rest

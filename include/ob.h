@@ -293,7 +293,9 @@ int ob_warmup_step(ob_ctx *ctx, const void *grads, float *m, float *v, float *pa
  * to nearest even: what ob_linear multiplies with.  grads [W][N] read; m, v
  * [N] and params [N] read and overwritten; lr finite, weight_decay >= 0, beta2 in [0, 1);
  * decay and *grad_scale need their element's alignment only.
- * A captured call keeps its step, lr and seed at every replay.
+ * A captured call keeps its step, lr and seed at every replay: one step's bias correction and,
+ * in 8 bits, one dither, over which rounding is not unbiased.  A graph that is replayed as
+ * step after step leaves this call outside.
  *
  * moments = OB_MOMENTS_F32: m, v [N] fp32; m_scale and v_scale are NULL.
  * moments = OB_MOMENTS_8BIT: m, v [N] are codes, m_scale, v_scale [N/64] scale
@@ -309,11 +311,11 @@ int ob_warmup_step(ob_ctx *ctx, const void *grads, float *m, float *v, float *pa
  * hi: the 32-bit halves), the low 16 bits are m's and the high 16 r's.  A magnitude
  * between two codes takes the upper one if its remainder in steps plus the
  * dither / 2^16 reaches 1 (below the smallest normal code the remainder is first rounded
- * to nearest even at 2^-20 of a step, of r 2^-19), so rounding is unbiased over seeds: give
- * every step another seed.  A root above 0 takes code 1 at least.  A block with a NaN or an
- * infinity has scale 255 and codes 0 and stands for NaN throughout.  Zero-filled
- * buffers stand for zeros: the state to start from.  m_scale and v_scale are
- * aligned to 16 bytes as well. */
+ * to nearest even at 2^-20 of a step, of r 2^-19), so over seeds rounding is unbiased to within
+ * 2^-16 of a step (a remainder below that never rounds up): give every step another seed.
+ * A root above 0 takes code 1 at least.  A block with a NaN or an infinity has scale 255 and
+ * codes 0 and stands for NaN throughout.  Zero-filled buffers stand for zeros: the state to
+ * start from.  m_scale and v_scale are aligned to 16 bytes as well. */
 int ob_adamw_step(ob_ctx *ctx, int32_t moments, const void *grads, const float *grad_scale, void *m, uint8_t *m_scale,
                   void *v, uint8_t *v_scale, float *params, uint16_t *model, int64_t step, double lr, double beta2,
                   double weight_decay, const float *decay, uint64_t seed, void *stream);

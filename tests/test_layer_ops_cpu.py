@@ -77,3 +77,16 @@ def test_the_reference_dither_is_even():
             assert abs(int(((half >> np.uint64(bit)) & np.uint64(1)).sum()) - (1 << 15)) < 6 * 128
     far = ref.dither(np.arange(1 << 16, dtype=np.uint64) + np.uint64(1 << 32), 3)
     assert (far[0] != d[0]).mean() > 0.99
+
+
+def test_the_reference_rounding_is_unbiased_to_the_dither():
+    """Over all dithers a remainder q of a step goes up floor(2^16 q) times of 2^16: short by less than 2^-16 of a step,
+    and one below 2^-16 never does."""
+    every = np.arange(1 << 16, dtype=np.uint64)
+    for least, bits, fine in ((-6, 3, 20), (4, 4, 19)):
+        step = 2.0 ** (least + 1 - bits)                     # of the values from 2^(least + 1) on
+        for q in (0.0, 2.0 ** -17, 2.0 ** -16, 0.25, 1 / 3, 1 - 2.0 ** -16, 1 - 2.0 ** -18):
+            x = np.full(1 << 16, 2.0 ** (least + 1) + q * step)
+            _, v = ref._pick(x, every, least, bits, fine)
+            ups = (v > 2.0 ** (least + 1)).sum()
+            assert set(v) <= {2.0 ** (least + 1), 2.0 ** (least + 1) + step} and ups == int(q * 65536)
