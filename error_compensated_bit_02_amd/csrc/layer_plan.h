@@ -34,7 +34,7 @@ constexpr int kLayerFew = 8, kLayerSlice = 1024;
 constexpr int64_t kMostGroups = 0xffffffffLL / 512;
 
 // Tiles that are built, and their times in microseconds: of a workgroup's start and
-// end, of a turn on a CU of its own and with as many workgroups as a CU holds.  The
+// end, of a turn on a CU of its own and with per_cu workgroups on it.  The
 // plan is the tile and the number of slices with the least time by them.  Forward /
 // gradient in us with each tile's best slices, the taken one marked:
 //   bf16               256 x 256    128 x 128      128 x 32
@@ -50,8 +50,17 @@ constexpr int64_t kMostGroups = 0xffffffffLL / 512;
 //   64 x 4096^2        62 / 49      60 / 49        26 / 27 *
 //   777 2048->1000     29* / 35     32 / 32 *      42 / 33
 //   2048^3             64 / 58 *    78 / 58        77 / 84
+//   fp32 and bf16 weights
+//   64 x 4096^2        24 / 22      22 / 21 *      23 / 21
+//   777 2048->1000     28* / 33     28 / 28 *      35 / 22
+//   2048^3             64 / 68 *    70 / 63        62 / 60
+//   4096^3             362 / 345 *  424 / 396      460 / 449
 // Cutting on the way saves the parts' copy, whose cost the weight's size settles, and
 // cuts an operand again in every tile that reads it: it wins where few tiles share it.
+// One table serves both mixed types, whose times differ: fp32 x with bf16 weights is up to a
+// quarter from its best tile by it.  per_cu: workgroups of a CU that the estimate
+// counts on; of the tiles that cut on the way two fit and one is counted, so beyond
+// 256 workgroups their estimate is too long.
 struct LayerTiles {
   int features, tokens, depth, per_cu;
   bool raw;                          // fp32 as it lies
