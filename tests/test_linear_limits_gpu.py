@@ -1,7 +1,9 @@
 """A linear layer's forward and input gradient at the ends of their documented ranges:
 matrices past 2^31 elements, the longest contraction, the most features and rows, the
-longest row stride, and infinities.  Whole numbers whose sums fp32 holds, compared bit
+longest row stride, infinities, and calls from several threads.  Whole numbers whose sums fp32 holds, compared bit
 for bit on the GPU, slice by slice."""
+import threading
+
 import pytest
 import torch
 
@@ -237,3 +239,38 @@ def test_infinities(dt, lt, rows):
     assert torch.equal(y, res)
     ly.opt.linear_input_grad(1, x, ly.list, y, add=res)
     assert torch.equal(y, res)
+
+
+def test_calls_from_several_threads():
+    """Four threads with a stream each call both directions on one context, with slices, copies and scratch from torch:
+    the bits of calls one after the other."""
+    rows, out, inp = 200, 264, 1544
+    ly = Layer(out, inp, F32)
+    x = [torch.randn(rows, inp, device=DEV, generator=torch.Generator(device=DEV).manual_seed(k)) for k in range(4)]
+
+    def both(k, stream=None):
+        y, dx = torch.empty(rows, out, device=DEV), torch.empty(rows, inp, device=DEV)
+        ck = ActCheckpoint(rows, out, device=DEV)
+        ly.opt.linear(0, 1, x[k], ly.list, y, act="gelu", keep=ck, stream=stream)
+        ly.opt.linear_input_grad(0, y, ly.list, dx, add=x[k], stream=stream)
+        return y, dx, ck.codes[:, :out], ck.scales[:, :out]
+
+    want = [both(k) for k in range(4)]
+    torch.cuda.synchronize()
+    got, streams = [None] * 4, [torch.cuda.Stream() for _ in range(4)]
+    start = threading.Barrier(4)
+
+    def work(k):
+        start.wait(timeout=30)
+        with torch.cuda.stream(streams[k]):
+            for _ in range(50):
+                got[k] = both(k, streams[k])
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=60)
+    torch.cuda.synchronize()
+    for k in range(4):
+        assert got[k] is not None and all(torch.equal(a, b) for a, b in zip(got[k], want[k])), k
